@@ -15,6 +15,7 @@ import ctypes
 import math
 import os
 import re
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -26,7 +27,10 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_delta", "attn_bwd_dkdv", "attn_bwd_
            "DetAttnError", "STATUS", "header_symbols", "build", "embed_grad",
            "embed_grad_workspace_bytes", "attn_fwd_varlen", "attn_bwd_varlen",
            "varlen_workspace_bytes", "layer_gemm", "layer_workspace_bytes", "LayerState",
-           "layer_train_step", "ds_workspace_bytes", "set_bwd_dq_mode"]
+           "layer_train_step", "ds_workspace_bytes", "set_bwd_dq_mode", "Act8", "act8_pack",
+           "act8_unpack", "act8_wgrad", "act8_wgrad_workspace_bytes", "swiglu_fwd", "swiglu_bwd",
+           "BlockNormKept", "BlockNormGrads", "block_norm_fwd", "block_norm_bwd",
+           "block_norm_bwd_workspace_bytes"]
 
 STATUS = {0: "DETATTN_OK", -1: "DETATTN_ERR_NULL", -2: "DETATTN_ERR_ALIGN",
           -3: "DETATTN_ERR_SHAPE", -4: "DETATTN_ERR_HEADDIM", -5: "DETATTN_ERR_SCALE",
@@ -85,6 +89,20 @@ def lib() -> ctypes.CDLL:
     L.embed_grad_workspace_bytes.restype = sz
     L.embed_grad.argtypes = [vp, vp, vp, vp, sz, i, i, i, vp]
     L.embed_grad.restype = i
+    L.act8_pack.argtypes = [vp, vp, vp, i, i, vp]
+    L.act8_unpack.argtypes = [vp, vp, vp, i, i, vp]
+    L.act8_wgrad_workspace_bytes.argtypes = [i, i, i]
+    L.act8_wgrad_workspace_bytes.restype = sz
+    L.act8_wgrad.argtypes = [vp] * 6 + [sz, i, i, i, vp]
+    L.swiglu_fwd.argtypes = [vp, vp, vp, vp, i, i, vp]
+    L.swiglu_bwd.argtypes = [vp] * 6 + [i, i, vp]
+    L.block_norm_fwd.argtypes = [vp] * 13 + [i] * 6 + [f] * 3 + [vp]
+    L.block_norm_bwd_workspace_bytes.argtypes = [i, i, i]
+    L.block_norm_bwd_workspace_bytes.restype = sz
+    L.block_norm_bwd.argtypes = [vp] * 19 + [sz] + [i] * 6 + [f] * 2 + [vp]
+    for name in ("act8_pack", "act8_unpack", "act8_wgrad", "swiglu_fwd", "swiglu_bwd",
+                 "block_norm_fwd", "block_norm_bwd"):
+        getattr(L, name).restype = i
     L.detattn_check_status.argtypes = [vp]
     L.detattn_diag_exp2.argtypes = [vp, vp, vp, vp, i, vp]
     L.detattn_diag_exp2.restype = i
@@ -391,6 +409,288 @@ def layer_train_step(state, x, dy, lr=3e-4, weight_decay=0.1, beta1=0.9, beta2=0
                                   float(weight_decay), float(beta1), float(beta2), float(eps),
                                   _stream()), "layer_train_step")
     return s.g_qkv, s.g_o
+
+
+# ------------------------------------------------------------ block norms, 8-bit checkpoints
+class Act8(NamedTuple):
+    """An 8-bit checkpoint of a [rows, d] activation (include/detattn.h):
+    q int8 [rows, d], e uint8 [rows, d / 32]; the values are q 2^(e - 127)."""
+    q: torch.Tensor
+    e: torch.Tensor
+
+
+class BlockNormKept(NamedTuple):
+    """What block_norm_bwd needs of a forward: the row statistics, and either
+    the tensors x (x', the stream after the block) and y, or the 8-bit
+    checkpoints of the normed x' and y."""
+    rstd_pre: Optional[torch.Tensor] = None
+    rstd_post: Optional[torch.Tensor] = None
+    x: Optional[torch.Tensor] = None
+    y: Optional[torch.Tensor] = None
+    xhat8: Optional[Act8] = None
+    yhat8: Optional[Act8] = None
+
+
+class BlockNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+
+
+def _need_current(t, name):
+    """The calls run on the current device's current stream: what lies on
+    another device is refused."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, name):
+    """(rows, d) of a [..., d] tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() < 1 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must be [..., d] with d >= 1")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def _need_act8(c, name, shape):
+    if not isinstance(c, tuple) or len(c) != 2:
+        raise TypeError(f"{name} must be an Act8 (q, e)")
+    _need(c[0], name + ".q", torch.int8, shape)
+    _need(c[1], name + ".e", torch.uint8, tuple(shape[:-1]) + (shape[-1] // 32,))
+
+
+def _new_act8(shape, device):
+    if shape[-1] % 32:
+        raise ValueError(f"an 8-bit checkpoint needs a multiple of 32 columns, got {shape[-1]}")
+    return Act8(torch.empty(shape, dtype=torch.int8, device=device),
+                torch.empty(tuple(shape[:-1]) + (shape[-1] // 32,), dtype=torch.uint8, device=device))
+
+
+def act8_pack(x, out=None):
+    """The 8-bit checkpoint of x, bf16 [..., d], d a multiple of 32."""
+    rows, d = _rows(x, "x")
+    _need(x, "x", torch.bfloat16, x.shape)
+    _need_current(x, "x")
+    c = _new_act8(x.shape, x.device) if out is None else out
+    _need_act8(c, "out", tuple(x.shape))
+    _check(lib().act8_pack(_ptr(x), _ptr(c[0]), _ptr(c[1]), rows, d, _stream()), "act8_pack")
+    return c
+
+
+def act8_unpack(c, out=None):
+    """The values of an 8-bit checkpoint, bf16 [..., d] (exact)."""
+    rows, d = _rows(c[0], "q")
+    _need_act8(c, "checkpoint", tuple(c[0].shape))
+    _need_current(c[0], "checkpoint")
+    x = torch.empty(c[0].shape, dtype=torch.bfloat16, device=c[0].device) if out is None else out
+    _need(x, "out", torch.bfloat16, c[0].shape)
+    _check(lib().act8_unpack(_ptr(c[0]), _ptr(c[1]), _ptr(x), rows, d, _stream()), "act8_unpack")
+    return x
+
+
+def act8_wgrad_workspace_bytes(rows, d, n) -> int:
+    return int(lib().act8_wgrad_workspace_bytes(rows, d, n))
+
+
+def act8_wgrad(c, dy, row_scale=None, dw=None, workspace=None):
+    """Weight gradient dw fp32 [d, n] = diag(row_scale) x^T dy from the 8-bit
+    checkpoint of the layer input x [..., d] and dy bf16 [..., n]."""
+    rows, d = _rows(c[0], "q")
+    rows_dy, n = _rows(dy, "dy")
+    _need_act8(c, "checkpoint", tuple(c[0].shape))
+    _need(dy, "dy", torch.bfloat16, dy.shape)
+    _need_current(dy, "dy")
+    if rows != rows_dy:
+        raise ValueError(f"the checkpoint has {rows} rows, dy {rows_dy}")
+    if row_scale is not None:
+        _need(row_scale, "row_scale", torch.float32, (d,))
+    dw = torch.empty((d, n), dtype=torch.float32, device=dy.device) if dw is None else dw
+    _need(dw, "dw", torch.float32, (d, n))
+    if workspace is None:
+        size = act8_wgrad_workspace_bytes(rows, d, n)
+        if size:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=dy.device)
+    _check(lib().act8_wgrad(_ptr(c[0]), _ptr(c[1]), _ptr(dy), _ptr(row_scale), _ptr(dw),
+                            _ptr(workspace), 0 if workspace is None else workspace.numel(), rows, d,
+                            n, _stream()), "act8_wgrad")
+    return dw
+
+
+def swiglu_fwd(u, keep8=False, out=None):
+    """h = a sigma(a) b for u = [a | b], bf16 [..., 2 f]; with keep8 returns
+    (h, the 8-bit checkpoint of u)."""
+    rows, f2 = _rows(u, "u")
+    _need(u, "u", torch.bfloat16, u.shape)
+    _need_current(u, "u")
+    if f2 % 2:
+        raise ValueError(f"u has {f2} columns, needs 2 f")
+    f = f2 // 2
+    if keep8 and f % 32:
+        raise ValueError(f"an 8-bit checkpoint of u needs f a multiple of 32, got {f}")
+    shape = tuple(u.shape[:-1]) + (f,)
+    h = torch.empty(shape, dtype=torch.bfloat16, device=u.device) if out is None else out
+    _need(h, "out", torch.bfloat16, shape)
+    c = _new_act8(u.shape, u.device) if keep8 else (None, None)
+    _check(lib().swiglu_fwd(_ptr(u), _ptr(h), _ptr(c[0]), _ptr(c[1]), rows, f, _stream()),
+           "swiglu_fwd")
+    return (h, c) if keep8 else h
+
+
+def swiglu_bwd(dh, u, with_h=False, du=None):
+    """du bf16 [..., 2 f] from dh [..., f] and u, bf16 [..., 2 f] or its 8-bit
+    checkpoint; with_h: (du, h), h recomputed from the same u."""
+    rows, f = _rows(dh, "dh")
+    _need(dh, "dh", torch.bfloat16, dh.shape)
+    _need_current(dh, "dh")
+    shape = tuple(dh.shape[:-1]) + (2 * f,)
+    if isinstance(u, torch.Tensor):
+        _need(u, "u", torch.bfloat16, shape)
+        src = (u, None, None)
+    else:
+        _need_act8(u, "u", shape)
+        src = (None, u[0], u[1])
+    du = torch.empty(shape, dtype=torch.bfloat16, device=dh.device) if du is None else du
+    _need(du, "du", torch.bfloat16, shape)
+    h = torch.empty(dh.shape, dtype=torch.bfloat16, device=dh.device) if with_h else None
+    _check(lib().swiglu_bwd(_ptr(dh), _ptr(src[0]), _ptr(src[1]), _ptr(src[2]), _ptr(du), _ptr(h),
+                            rows, f, _stream()), "swiglu_bwd")
+    return (du, h) if with_h else du
+
+
+def _need_stream(x, name, shape=None):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    _need(x, name, x.dtype, x.shape if shape is None else shape)
+
+
+def _gate_rows(gate, rows, d):
+    """G of a gate [d], [..., d] whose rows divide the stream's."""
+    if gate is None:
+        return 1
+    _need_stream(gate, "gate")
+    g, dg = _rows(gate, "gate")
+    if dg != d or g < 1 or (rows and (g > rows or rows % g)):
+        raise ValueError(f"gate has shape {tuple(gate.shape)}: needs d = {d} columns and a number "
+                         f"of rows that divides {rows}")
+    return g
+
+
+def block_norm_fwd(x, y=None, gate=None, w_post=None, w_pre=None, res_scale=1.0, block_scale=1.0,
+                   eps=1e-6, gate_sigmoid=False, keep8=False, x_out=None):
+    """x' = res_scale x + block_scale g norm(y) w_post, h = norm(x') w_pre
+    (include/detattn.h): returns (x', h, kept).  x [..., d] is the residual
+    stream (bf16 or fp32), y bf16 the block's output (None: x' is x), gate
+    [d] or [..., d] (one row for every channel, sequence or token; its sigmoid
+    with gate_sigmoid), w_post and w_pre fp32 [d] or None.  kept is what
+    block_norm_bwd takes: the row statistics with x' and y, or, with keep8,
+    with their normed values in 8 bits."""
+    _need_stream(x, "x")
+    _need_current(x, "x")
+    rows, d = _rows(x, "x")
+    dev, f32 = x.device, torch.float32
+    if y is not None:
+        _need(y, "y", torch.bfloat16, x.shape)
+    elif gate is not None or w_post is not None:
+        raise ValueError("gate and w_post belong to a block output y")
+    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            _need(w, name, f32, (d,))
+    G = _gate_rows(gate, rows, d)
+    out = x
+    if y is not None:
+        out = torch.empty_like(x) if x_out is None else x_out
+        _need(out, "x_out", x.dtype, x.shape)
+    pre, post = w_pre is not None, w_post is not None
+    h = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if pre else None
+    rp = torch.empty(x.shape[:-1], dtype=f32, device=dev) if pre else None
+    ro = torch.empty(x.shape[:-1], dtype=f32, device=dev) if post else None
+    x8 = _new_act8(x.shape, dev) if keep8 and pre else None
+    y8 = _new_act8(x.shape, dev) if keep8 and y is not None else None
+    xq, xe = x8 if x8 is not None else (None, None)
+    yq, ye = y8 if y8 is not None else (None, None)
+    _check(lib().block_norm_fwd(_ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                _ptr(out) if y is not None else None, _ptr(h), _ptr(ro), _ptr(rp),
+                                _ptr(yq), _ptr(ye), _ptr(xq), _ptr(xe), rows, d, G,
+                                int(x.dtype == f32), int(gate is not None and gate.dtype == f32),
+                                int(bool(gate_sigmoid)), float(res_scale), float(block_scale),
+                                float(eps), _stream()), "block_norm_fwd")
+    if keep8:
+        return out, h, BlockNormKept(rp, ro, None, None, x8, y8)
+    return out, h, BlockNormKept(rp, ro, out, y, None, None)
+
+
+def block_norm_bwd_workspace_bytes(N, d, G=1) -> int:
+    return int(lib().block_norm_bwd_workspace_bytes(N, d, G))
+
+
+def block_norm_bwd(dx_out, dh, kept, gate=None, w_post=None, w_pre=None, res_scale=1.0,
+                   block_scale=1.0, gate_sigmoid=False, has_block=None, dx=None, workspace=None):
+    """Gradients (dx, dy, dgate, dw_post, dw_pre) of block_norm_fwd from dx_out,
+    the gradient of x' (None: zero; then the stream is bf16 unless kept.x says
+    otherwise), dh, the gradient of h (None with w_pre None), and what the
+    forward kept.  has_block: whether the forward had a y (None: whether kept
+    holds y or its checkpoint)."""
+    like = dx_out if dx_out is not None else dh
+    if like is None:
+        raise ValueError("dx_out and dh are both None: no gradient to carry back")
+    rows, d = _rows(like, "dx_out" if dx_out is not None else "dh")
+    shape, dev, f32, bf = tuple(like.shape), like.device, torch.float32, torch.bfloat16
+    _need_current(like, "dx_out" if dx_out is not None else "dh")
+    pre, post = w_pre is not None, w_post is not None
+    block = (kept.y is not None or kept.yhat8 is not None) if has_block is None else bool(has_block)
+    if pre != (dh is not None):
+        raise ValueError("dh and w_pre go together")
+    if not block and (post or gate is not None):
+        raise ValueError("gate and w_post belong to a block output y")
+    stream = dx_out.dtype if dx_out is not None else kept.x.dtype if kept.x is not None else bf
+    if dx_out is not None:
+        _need_stream(dx_out, "dx_out")
+    xq = xe = yq = ye = x = y = rp = ro = None
+    if pre:
+        _need(dh, "dh", bf, shape)
+        _need(w_pre, "w_pre", f32, (d,))
+        rp = kept.rstd_pre
+        _need(rp, "kept.rstd_pre", f32, shape[:-1])
+        if kept.xhat8 is not None:
+            _need_act8(kept.xhat8, "kept.xhat8", shape)
+            xq, xe = kept.xhat8
+        else:
+            x = kept.x
+            _need(x, "kept.x", stream, shape)
+    if post:
+        _need(w_post, "w_post", f32, (d,))
+        ro = kept.rstd_post
+        _need(ro, "kept.rstd_post", f32, shape[:-1])
+    if post or gate is not None:
+        if kept.yhat8 is not None:
+            _need_act8(kept.yhat8, "kept.yhat8", shape)
+            yq, ye = kept.yhat8
+        else:
+            y = kept.y
+            _need(y, "kept.y", bf, shape)
+    G = _gate_rows(gate, rows, d)
+    dx = torch.empty(shape, dtype=stream, device=dev) if dx is None else dx
+    _need(dx, "dx", stream, shape)
+    dy = torch.empty(shape, dtype=bf, device=dev) if block else None
+    dgate = torch.empty_like(gate) if gate is not None else None
+    dwo = torch.empty_like(w_post) if post else None
+    dwp = torch.empty_like(w_pre) if pre else None
+    if workspace is None:
+        workspace = torch.empty((max(16, block_norm_bwd_workspace_bytes(rows, d, G)),),
+                                dtype=torch.uint8, device=dev)
+    _check(lib().block_norm_bwd(_ptr(dx_out), _ptr(dh), _ptr(x), _ptr(y), _ptr(xq), _ptr(xe),
+                                _ptr(yq), _ptr(ye), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(ro),
+                                _ptr(rp), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dwo), _ptr(dwp),
+                                _ptr(workspace), workspace.numel(), rows, d, G, int(stream == f32),
+                                int(gate is not None and gate.dtype == f32), int(bool(gate_sigmoid)),
+                                float(res_scale), float(block_scale), _stream()), "block_norm_bwd")
+    return BlockNormGrads(dx, dy, dgate, dwo, dwp)
 
 
 def embed_grad_workspace_bytes(N, V, E) -> int:

@@ -1,0 +1,116 @@
+// The 8-bit checkpoint format on the device: int8 values with one power-of-two
+// exponent for every 32 consecutive columns of a row.
+//
+// For a group whose largest magnitude is m, the exponent is the smallest k
+// with m <= 127 2^k, and a value x is stored as q = x 2^-k rounded to the
+// nearest whole number (ties to even).  A power of two makes both directions
+// exact but for that one rounding: x 2^-k is exact in fp32, and q 2^k has at
+// most 7 significant bits, so it is a bf16 number and a tensor core can take
+// it as it is.  The rounding is off by at most 2^(k-1), m / 127 at worst.
+// (int8 with a shared exponent rather than e4m3: for the near-normal values
+// of a norm its error is about a third of e4m3's 2^-4 steps.)
+#pragma once
+#include <cstdint>
+
+#include "sm103_ptx.cuh"
+
+namespace detattn {
+
+// Bits of |x|: ordered like the magnitudes, with infinity and every NaN on top
+// (a floating-point maximum would drop a NaN).
+__device__ __forceinline__ uint32_t act8_abs_bits(float x) {
+  return __float_as_uint(x) & 0x7FFFFFFFu;
+}
+
+// Exponent byte of a group with largest magnitude bits m.  With m = f 2^E, f
+// in [1, 2): m <= 127 2^k needs k = E - 6 when f <= 127 / 64, else E - 5.
+// Kept at 1 (k = -126) from below: what is smaller rounds to multiples of
+// 2^-126.
+__device__ __forceinline__ uint32_t act8_exponent(uint32_t m) {
+  if (m >= 0x7F800000u) return 255u;
+  const int e = static_cast<int>(m >> 23) - 6 + ((m & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+  return static_cast<uint32_t>(e > 1 ? e : 1);
+}
+
+// Eight values of one lane; the four lanes of an aligned quad hold one group.
+// Returns the exponent byte and writes the eight int8 values.  Every lane of
+// the warp takes part.
+__device__ __forceinline__ uint32_t act8_quantise8(const float (&v)[8], uint2* q) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, act8_abs_bits(v[i]));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const uint32_t e = act8_exponent(m);
+  if (e == 255u) {
+    *q = make_uint2(0u, 0u);
+    return e;
+  }
+  // x 2^-k + 1.5 2^23: the sum's low byte is the rounded value in two's
+  // complement.
+  const float inv = __uint_as_float((254u - e) << 23);
+  float r[8];
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = fmaf(v[i], inv, 12582912.0f);
+  // k = 122: 64 2^122 would be infinity, so what rounds there stays at 63.
+  if (e == 249u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = fminf(fmaxf(r[i], 12582912.0f - 63.0f), 12582912.0f + 63.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(r[i]);
+  const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  *q = make_uint2(lo, hi);
+  return e;
+}
+
+// 2^(e - 127); infinity for e = 255, whose group holds zeros: 0 * inf is NaN.
+__device__ __forceinline__ float act8_scale(uint32_t e) { return __uint_as_float(e << 23); }
+
+// The whole numbers of four int8 bytes as floats: byte + 128 in the low bits
+// of 2^23's mantissa, less 2^23 + 128.
+__device__ __forceinline__ void act8_int4(uint32_t q, float (&f)[4]) {
+  const uint32_t u = q ^ 0x80808080u;
+  f[0] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.0f;
+  f[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.0f;
+  f[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.0f;
+  f[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.0f;
+}
+__device__ __forceinline__ void act8_values8(uint2 q, float scale, float (&v)[8]) {
+  float a[4], b[4];
+  act8_int4(q.x, a);
+  act8_int4(q.y, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i] * scale;
+    v[4 + i] = b[i] * scale;
+  }
+}
+
+// ------------------------------------------------------------ eight bf16 / fp32 values
+__device__ __forceinline__ void bf16x8_to_float(uint4 x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 float_to_bf16x8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void f32x8_to_float(uint4 a, uint4 b, float (&f)[8]) {
+  f[0] = __uint_as_float(a.x);
+  f[1] = __uint_as_float(a.y);
+  f[2] = __uint_as_float(a.z);
+  f[3] = __uint_as_float(a.w);
+  f[4] = __uint_as_float(b.x);
+  f[5] = __uint_as_float(b.y);
+  f[6] = __uint_as_float(b.z);
+  f[7] = __uint_as_float(b.w);
+}
+
+}  // namespace detattn

@@ -1,0 +1,766 @@
+// Norms before and after a block, fused with the block's gate, its scale and
+// the residual stream, for sm_103a (RustingBrain vs PyTorch/TensorFlow page,
+// "The setup": a decoder-only model with RMSNorm; "What didn't work": folding
+// the residual add into the norm).
+//
+// Forward, per row of width d (r, s: residual and block scale, g the gate or
+// its sigmoid; every norm is x / sqrt(mean x^2 + eps)):
+//   yhat = y rstd_y,  x' = r x + s g (yhat w_post),  xhat = x' rstd_x,  h = xhat w_pre
+// Backward, from dx' and dh:
+//   D  = dx' + rstd_x (dh w_pre - xhat mean(dh w_pre xhat)),   dx = r D
+//   dz = s g D,  dg = s (yhat w_post) D  (through the sigmoid: times g (1 - g))
+//   dy = rstd_y (dz w_post - yhat mean(dz w_post yhat))
+//   dw_pre = sum_rows dh xhat,  dw_post = sum_rows dz yhat,  dgate = sum of dg
+//            over the rows that share a gate row
+// xhat and yhat come from the stored tensors or from 8-bit checkpoints that
+// the forward wrote while it had them in registers.
+//
+// Everything is 32-bit between the loads and the one rounding at each store.
+// Column sums have a fixed order and no atomics: a row team's threads own
+// fixed columns and add their rows in ascending order in registers, the teams
+// of a block are added in team order, and a second kernel adds the blocks in
+// block order.  The deal of rows follows from the shape alone.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "act8.cuh"
+#include "block_launch.h"
+
+namespace detattn {
+
+// Set when a bounded wait of the backward runs out.
+__device__ unsigned int g_norm_status;
+
+namespace {
+
+__device__ __forceinline__ void set_norm_status() { atomicOr(&g_norm_status, 1u); }
+
+// ------------------------------------------------------------ row teams
+// A row belongs to a team of W warps; thread t of the team holds the vectors
+// of eight columns t, t + 32 W, ... (CH of them).  Sums over a row: shuffles,
+// then, where W > 1, one word per warp in shared memory and the team's own
+// barrier.  `slot` alternates between two sets of words, so one barrier per
+// sum is enough.
+template <bool MULTI>
+__device__ __forceinline__ float team_sum(float v, float* words, int W, int team, int warp_in_team,
+                                          int lane, int& slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if constexpr (MULTI) {
+    float* w = words + slot * 32 + team * W;
+    if (lane == 0) w[warp_in_team] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory");
+    v = 0.0f;
+    for (int i = 0; i < W; ++i) v += w[i];
+    slot ^= 1;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void load_f32x8(const float* p, float (&f)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  f32x8_to_float(a, b, f);
+}
+// Eight gate values of one gate row, and (for the backward) their slopes by
+// the stored value.
+__device__ __forceinline__ void load_gate8(const void* gate, size_t at, bool fp32, bool sigmoid,
+                                           float (&g)[8], float (&slope)[8]) {
+  if (fp32)
+    load_f32x8(static_cast<const float*>(gate) + at, g);
+  else
+    bf16x8_to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gate) + at)), g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    slope[i] = 1.0f;
+    if (sigmoid) {
+      g[i] = 1.0f / (1.0f + __expf(-g[i]));
+      slope[i] = g[i] * (1.0f - g[i]);
+    }
+  }
+}
+
+// Eight stream values (bf16 or fp32) as raw words.
+template <bool F32>
+struct Raw8 {
+  uint4 a, b;  // b: fp32 only
+  __device__ __forceinline__ void zero() {
+    a = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (F32) b = a;
+  }
+  __device__ __forceinline__ void load(const void* p, size_t at) {
+    if constexpr (F32) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+      a = q[0];
+      b = q[1];
+    } else {
+      a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (F32)
+      f32x8_to_float(a, b, f);
+    else
+      bf16x8_to_float(a, f);
+  }
+};
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, size_t at, const float (&f)[8]) {
+  if constexpr (F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) = float_to_bf16x8(f);
+  }
+}
+// Eight checkpointed values; lanes past the row (`in` false) take part in the
+// group's shuffles and store nothing.
+__device__ __forceinline__ void keep8(const float (&v)[8], bool in, size_t at, int8_t* q,
+                                      uint8_t* e) {
+  uint2 out;
+  const uint32_t ex = act8_quantise8(v, &out);
+  if (in) {
+    *reinterpret_cast<uint2*>(q + at) = out;
+    if ((at & 31) == 0) e[at >> 5] = static_cast<uint8_t>(ex);
+  }
+}
+
+// ------------------------------------------------------------ forward
+constexpr int kFwdWarps = 4;  // warps per block where a row takes one warp
+
+template <int CH, bool MULTI, bool F32, bool KEEP8>
+__global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const BlockNormFwdArgs a) {
+  __shared__ float words[64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = MULTI ? blockDim.x >> 5 : 1;
+  const int team = MULTI ? 0 : warp, wt = MULTI ? warp : 0;
+  const int t = wt * 32 + lane;
+  const int row = MULTI ? blockIdx.x : blockIdx.x * kFwdWarps + warp;
+  if (row >= a.N) return;
+  const int n_vec = a.d >> 3;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const size_t base = static_cast<size_t>(row) * a.d;
+  int slot = 0;
+
+  Raw8<F32> xr[CH];
+  uint4 yr[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int v = c * W * 32 + t;
+    xr[c].zero();
+    yr[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (v < n_vec) {
+      if (a.y) yr[c] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.y) + base + v * 8);
+      xr[c].load(a.x, base + v * 8);
+    }
+  }
+  float rstd_y = 1.0f;
+  if (a.w_post) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float f[8];
+      bf16x8_to_float(yr[c], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+    }
+    ss = team_sum<MULTI>(ss, words, W, team, wt, lane, slot);
+    rstd_y = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
+    if (t == 0) a.rstd_post[row] = rstd_y;
+  }
+  float xf[CH][8];
+  float ss = 0.0f;
+  const size_t gate_row = a.gate ? static_cast<size_t>(row / a.rows_per_gate) * a.d : 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int v = c * W * 32 + t;
+    const bool in = v < n_vec;
+    xr[c].get(xf[c]);
+    if (a.y) {
+      float z[8];
+      bf16x8_to_float(yr[c], z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] *= rstd_y;
+      if constexpr (KEEP8) keep8(z, in, base + v * 8, a.yhat_q, a.yhat_e);
+      if (in) {
+        if (a.w_post) {
+          float w[8];
+          load_f32x8(a.w_post + v * 8, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] *= w[i];
+        }
+        if (a.gate) {
+          float g[8], slope[8];
+          load_gate8(a.gate, gate_row + v * 8, a.gate_fp32, a.gate_sigmoid, g, slope);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xf[c][i] = fmaf(a.block_scale, z[i], a.res_scale * xf[c][i]);
+        store8<F32>(a.x_out, base + v * 8, xf[c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(xf[c][i], xf[c][i], ss);
+  }
+  if (!a.w_pre) return;
+  ss = team_sum<MULTI>(ss, words, W, team, wt, lane, slot);
+  const float rstd_x = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
+  if (t == 0) a.rstd_pre[row] = rstd_x;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int v = c * W * 32 + t;
+    const bool in = v < n_vec;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xf[c][i] *= rstd_x;
+    if constexpr (KEEP8) keep8(xf[c], in, base + v * 8, a.xhat_q, a.xhat_e);
+    if (in) {
+      float w[8];
+      load_f32x8(a.w_pre + v * 8, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] *= xf[c][i];
+      store8<false>(a.h, base + v * 8, w);
+    }
+  }
+}
+
+// ------------------------------------------------------------ backward
+// One persistent block per SM.  Every row team has a ring of stages in shared
+// memory that bulk copies fill a row ahead (each tensor's row is one
+// contiguous piece), so that loads are in flight at all times while the
+// registers hold the column sums.  The exponent bytes of the checkpoints
+// (rows of d / 32 bytes, not a multiple of 16) come by plain loads a row
+// ahead.
+constexpr int kBwdWarps = 12;       // warps per block
+constexpr int kBwdCols = 768;       // columns per warp (three vectors of eight per thread)
+constexpr int kBwdBlocks = 152;     // one block per SM of the GB300
+constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdMaxStages = 4;
+constexpr int kBwdSmem = 226 * 1024;  // dynamic shared memory at most (1 KB is left for the static part)
+
+// Where the pieces of a row lie in a stage, and the ring's shape.
+struct BwdRing {
+  int off_d, off_x, off_y, bytes;  // dh at 0
+  int teams, stages;
+};
+
+// This team's rows, in order: rows team, team + teams, ... of each item.
+struct BwdCursor {
+  int item, row, end;
+  __device__ __forceinline__ void open(const BlockNormBwdArgs& a, int team) {
+    const int group_rows = a.N / (a.items / a.slices);
+    const int per = (group_rows + a.slices - 1) / a.slices;
+    const int group = item / a.slices, slice = item - group * a.slices;
+    const int lo = min(slice * per, group_rows), hi = min(lo + per, group_rows);
+    row = group * group_rows + lo + team;
+    end = group * group_rows + hi;
+  }
+  // To the first row at or after `row`; false when there is none.
+  __device__ __forceinline__ bool settle(const BlockNormBwdArgs& a, int team) {
+    while (row >= end) {
+      if (item + static_cast<int>(gridDim.x) >= a.items) return false;
+      item += gridDim.x;
+      open(a, team);
+    }
+    return true;
+  }
+};
+
+// Adds the teams' column sums in team order and writes them out.
+template <int CH>
+__device__ void block_columns(const float (&acc)[CH][8], float* sums, int d, int W, int teams, int team,
+                              int t, float* out_f32, __nv_bfloat16* out_bf16) {
+  for (int k = 0; k < teams; ++k) {
+    if (team == k) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int v = c * W * 32 + t;
+        if (v < (d >> 3)) {
+          float f[8];
+          if (k > 0) {
+            const uint4* p = reinterpret_cast<const uint4*>(sums + v * 8);
+            f32x8_to_float(p[0], p[1], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += acc[c][i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = acc[c][i];
+          }
+          if (k < teams - 1)
+            store8<true>(sums, v * 8, f);
+          else if (out_f32)
+            store8<true>(out_f32, v * 8, f);
+          else
+            store8<false>(out_bf16, v * 8, f);
+        }
+      }
+    }
+    if (k < teams - 1) __syncthreads();
+  }
+}
+
+template <int CH, bool MULTI, bool F32, bool FROM8>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float words[64];
+  __shared__ __align__(8) uint64_t bars[kBwdWarps * kBwdMaxStages];
+  __shared__ BwdCursor cursors[kBwdWarps];
+  __shared__ int issued[kBwdWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = MULTI ? (a.d + kBwdCols - 1) / kBwdCols : 1;
+  const int teams = ring.teams;
+  const int team = warp / W, wt = warp - team * W;
+  const int t = wt * 32 + lane;
+  const int n_vec = a.d >> 3;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const bool pre = a.dh != nullptr;
+  const bool per_row_gate = a.gate != nullptr && a.rows_per_gate == 1;
+  const bool sum_gate = a.gate != nullptr && !per_row_gate;
+  const bool need_y = a.dy != nullptr && (a.w_post != nullptr || a.gate != nullptr);
+  constexpr int kX = F32 ? 4 : 2;
+  float* sums = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);
+  uint8_t* mine = smem + team * ring.stages * ring.bytes;
+  const uint32_t bar0 = smem_u32(&bars[team * kBwdMaxStages]);
+  int slot = 0;
+  bool ok = true;
+
+  if (t == 0)
+    for (int s = 0; s < ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+  if (t == 0) fence_barrier_init();
+  __syncthreads();
+
+  const uint32_t row_tx = (pre ? 2u * a.d : 0u) + (a.dx_out ? kX * a.d : 0u) +
+                          (pre ? (FROM8 ? 1u : kX) * a.d : 0u) + (need_y ? (FROM8 ? 1u : 2u) * a.d : 0u);
+  auto issue = [&](int row, int s) {
+    const size_t at = static_cast<size_t>(row) * a.d;
+    const uint32_t dst = smem_u32(mine + s * ring.bytes), bar = bar0 + 8 * s;
+    mbar_arrive_expect_tx(bar, row_tx);
+    if (pre) {
+      bulk_load(dst, static_cast<const uint8_t*>(a.dh) + at * 2, 2 * a.d, bar);
+      if constexpr (FROM8)
+        bulk_load(dst + ring.off_x, a.xhat_q + at, a.d, bar);
+      else
+        bulk_load(dst + ring.off_x, static_cast<const uint8_t*>(a.x) + at * kX, kX * a.d, bar);
+    }
+    if (a.dx_out)
+      bulk_load(dst + ring.off_d, static_cast<const uint8_t*>(a.dx_out) + at * kX, kX * a.d, bar);
+    if (need_y) {
+      if constexpr (FROM8)
+        bulk_load(dst + ring.off_y, a.yhat_q + at, a.d, bar);
+      else
+        bulk_load(dst + ring.off_y, static_cast<const uint8_t*>(a.y) + at * 2, 2 * a.d, bar);
+    }
+  };
+
+  // The team's first thread issues the copies; its cursor, which runs
+  // ring.stages rows ahead, lives in shared memory (the other threads need
+  // no registers for it).
+  BwdCursor* ahead = &cursors[team];
+  if (t == 0) {
+    int n = 0;
+    ahead->item = blockIdx.x;
+    ahead->open(a, team);
+    for (; n < ring.stages && ahead->settle(a, team); ++n, ahead->row += teams) issue(ahead->row, n);
+    issued[team] = n;
+  }
+  // What plain loads bring, one row ahead.
+  struct Small {
+    float rx, ry;
+    uint32_t e[CH];  // exponent bytes: xhat's, yhat's << 8
+  };
+  auto load_small = [&](int row) {
+    Small m;
+    m.rx = pre ? a.rstd_pre[row] : 0.0f;
+    m.ry = a.w_post ? a.rstd_post[row] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      m.e[c] = 0u;
+      if constexpr (FROM8) {
+        const int v = c * W * 32 + t;
+        const size_t at = static_cast<size_t>(row) * (a.d >> 5) + (v >> 2);
+        if (v < n_vec) {
+          if (pre) m.e[c] = a.xhat_e[at];
+          if (need_y) m.e[c] |= static_cast<uint32_t>(a.yhat_e[at]) << 8;
+        }
+      }
+    }
+    return m;
+  };
+
+  float acc_pre[CH][8], acc_post[CH][8], acc_gate[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc_pre[c][i] = acc_post[c][i] = acc_gate[c][i] = 0.0f;
+
+  int s = 0;           // this row's stage
+  uint32_t phase = 0;  // and the parity of its barrier
+  BwdCursor cur;
+  for (cur.item = blockIdx.x; cur.item < a.items; cur.item += gridDim.x) {
+    cur.open(a, team);
+    Small next{};
+    if (cur.row < cur.end) next = load_small(cur.row);
+    for (; cur.row < cur.end; cur.row += teams) {
+      const int row = cur.row;
+      const size_t base = static_cast<size_t>(row) * a.d;
+      const uint8_t* st = mine + s * ring.bytes;
+      const Small m = next;
+      if (row + teams < cur.end) next = load_small(row + teams);
+      if (ok) ok = mbar_wait(bar0 + 8 * s, phase, a.wait_ns);
+      auto hat_x = [&](int c, int v, float (&f)[8]) {
+        if constexpr (FROM8) {
+          act8_values8(*reinterpret_cast<const uint2*>(st + ring.off_x + v * 8), act8_scale(m.e[c] & 255u), f);
+        } else {
+          Raw8<F32> r;
+          r.load(st + ring.off_x, v * 8);
+          r.get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= m.rx;
+        }
+      };
+      auto hat_y = [&](int c, int v, float (&f)[8]) {
+        if constexpr (FROM8) {
+          act8_values8(*reinterpret_cast<const uint2*>(st + ring.off_y + v * 8), act8_scale(m.e[c] >> 8), f);
+        } else {
+          Raw8<false> r;
+          r.load(st + ring.off_y, v * 8);
+          r.get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= m.ry;
+        }
+      };
+      float s1 = 0.0f;
+      if (pre) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int v = c * W * 32 + t;
+          if (v < n_vec) {
+            float dh[8], xh[8], w[8];
+            bf16x8_to_float(*reinterpret_cast<const uint4*>(st + v * 16), dh);
+            hat_x(c, v, xh);
+            load_f32x8(a.w_pre + v * 8, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float p = dh[i] * xh[i];
+              acc_pre[c][i] += p;
+              s1 = fmaf(p, w[i], s1);
+            }
+          }
+        }
+        s1 = team_sum<MULTI>(s1, words, W, team, wt, lane, slot) * inv_d;
+      }
+      float s2 = 0.0f;
+      float dz[CH][8];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int v = c * W * 32 + t;
+        if (v < n_vec) {
+          const size_t at = base + v * 8;
+          if (a.dx_out) {
+            Raw8<F32> r;
+            r.load(st + ring.off_d, v * 8);
+            r.get(dz[c]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dz[c][i] = 0.0f;
+          }
+          if (pre) {
+            float dh[8], xh[8], w[8];
+            bf16x8_to_float(*reinterpret_cast<const uint4*>(st + v * 16), dh);
+            hat_x(c, v, xh);
+            load_f32x8(a.w_pre + v * 8, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dz[c][i] = fmaf(m.rx, fmaf(dh[i], w[i], -xh[i] * s1), dz[c][i]);
+          }
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = a.res_scale * dz[c][i];
+          store8<F32>(a.dx, at, o);
+          if (a.dy) {
+            float yh[8], w[8];
+            if (need_y) hat_y(c, v, yh);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              dz[c][i] *= a.block_scale;
+              w[i] = 1.0f;
+            }
+            if (a.w_post) load_f32x8(a.w_post + v * 8, w);
+            if (a.gate) {
+              float g[8], slope[8];
+              load_gate8(a.gate, static_cast<size_t>(row / a.rows_per_gate) * a.d + v * 8, a.gate_fp32,
+                         a.gate_sigmoid, g, slope);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float dg = dz[c][i] * (yh[i] * w[i]) * slope[i];
+                dz[c][i] *= g[i];
+                acc_gate[c][i] += dg;
+                slope[i] = dg;
+              }
+              if (per_row_gate) {
+                if (a.gate_fp32)
+                  store8<true>(a.dgate, at, slope);
+                else
+                  store8<false>(a.dgate, at, slope);
+              }
+            }
+            if (a.w_post) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float p = dz[c][i] * yh[i];
+                acc_post[c][i] += p;
+                s2 = fmaf(p, w[i], s2);
+                dz[c][i] *= w[i];
+              }
+            }
+          }
+        }
+      }
+      if (a.dy) {
+        if (a.w_post) s2 = team_sum<MULTI>(s2, words, W, team, wt, lane, slot) * inv_d;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int v = c * W * 32 + t;
+          if (v < n_vec) {
+            if (a.w_post) {
+              float yh[8];
+              hat_y(c, v, yh);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dz[c][i] = m.ry * fmaf(-yh[i], s2, dz[c][i]);
+            }
+            store8<false>(a.dy, base + v * 8, dz[c]);
+          }
+        }
+      }
+      // The whole team is past this stage: refill it.
+      if constexpr (MULTI)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory");
+      else
+        __syncwarp();
+      if (t == 0 && ok && ahead->settle(a, team)) {
+        issue(ahead->row, s);
+        ahead->row += teams;
+        ++issued[team];
+      }
+      if (++s == ring.stages) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    if (sum_gate) {
+      // This item's share of its gate row, or all of it.
+      const int group = cur.item / a.slices;
+      float* f32 = a.part_gate ? a.part_gate + static_cast<size_t>(cur.item) * a.d
+                   : a.gate_fp32 ? static_cast<float*>(a.dgate) + static_cast<size_t>(group) * a.d
+                                 : nullptr;
+      __syncthreads();  // the sums of the item before have been read
+      block_columns<CH>(acc_gate, sums, a.d, W, teams, team, t, f32,
+                        f32 ? nullptr : static_cast<__nv_bfloat16*>(a.dgate) + static_cast<size_t>(group) * a.d);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc_gate[c][i] = 0.0f;
+    }
+  }
+  if (pre) {
+    __syncthreads();
+    block_columns<CH>(acc_pre, sums, a.d, W, teams, team, t,
+                      a.part_pre + static_cast<size_t>(blockIdx.x) * a.d, nullptr);
+  }
+  if (a.w_post) {
+    __syncthreads();
+    block_columns<CH>(acc_post, sums, a.d, W, teams, team, t,
+                      a.part_post + static_cast<size_t>(blockIdx.x) * a.d, nullptr);
+  }
+  if (!ok) {
+    // A wait ran out: the copies in flight, before the block ends.
+    if (t == 0)
+      for (int n = issued[team], k = n > ring.stages ? n - ring.stages : 0; k < n; ++k)
+        mbar_wait(bar0 + 8 * (k % ring.stages), (k / ring.stages) & 1, a.wait_ns);
+    set_norm_status();
+  }
+}
+
+// Adds the parts of a column sum in ascending order: 32 columns per block,
+// eight runs of parts each, then the runs in order.
+struct SumJob {
+  const float* parts;  // [n][d]
+  void* out;           // [d]
+  int n;
+  bool out_fp32;
+};
+struct SumJobs {
+  SumJob pre, post, gate;  // gate: row z of [G][d], parts [G][n][d]
+  int n_pre, n_post;       // 1 or 0
+  int d;
+};
+__global__ void __launch_bounds__(256) sum_parts_kernel(const SumJobs j) {
+  __shared__ float run[8][32];
+  const int z = blockIdx.y;
+  SumJob s;
+  size_t at = 0;
+  if (z < j.n_pre) {
+    s = j.pre;
+  } else if (z < j.n_pre + j.n_post) {
+    s = j.post;
+  } else {
+    s = j.gate;
+    at = z - j.n_pre - j.n_post;
+  }
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + tx;
+  const float* p = s.parts + at * s.n * j.d + col;
+  const int per = (s.n + 7) / 8, lo = min(ty * per, s.n), hi = min(lo + per, s.n);
+  float acc = 0.0f;
+  if (col < j.d) {
+#pragma unroll 8
+    for (int k = lo; k < hi; ++k) acc += p[static_cast<size_t>(k) * j.d];
+  }
+  run[ty][tx] = acc;
+  __syncthreads();
+  if (ty == 0 && col < j.d) {
+    for (int k = 1; k < 8; ++k) acc += run[k][tx];
+    if (s.out_fp32)
+      static_cast<float*>(s.out)[at * j.d + col] = acc;
+    else
+      static_cast<__nv_bfloat16*>(s.out)[at * j.d + col] = __float2bfloat16(acc);
+  }
+}
+
+template <int CH, bool MULTI>
+cudaError_t fwd_of(const BlockNormFwdArgs& a, bool f32, int W, cudaStream_t st) {
+  const unsigned grid = MULTI ? a.N : (a.N + kFwdWarps - 1) / kFwdWarps;
+  const unsigned block = MULTI ? W * 32 : kFwdWarps * 32;
+  const bool keep = a.xhat_q != nullptr || a.yhat_q != nullptr;
+  if (f32) {
+    if (keep)
+      block_norm_fwd_kernel<CH, MULTI, true, true><<<grid, block, 0, st>>>(a);
+    else
+      block_norm_fwd_kernel<CH, MULTI, true, false><<<grid, block, 0, st>>>(a);
+  } else {
+    if (keep)
+      block_norm_fwd_kernel<CH, MULTI, false, true><<<grid, block, 0, st>>>(a);
+    else
+      block_norm_fwd_kernel<CH, MULTI, false, false><<<grid, block, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+template <int CH, bool MULTI, bool F32, bool FROM8>
+cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
+  static unsigned long long attr_ctx[64] = {};
+  auto kernel = block_norm_bwd_kernel<CH, MULTI, F32, FROM8>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long ctx = current_context_id();
+  if (dev >= 64 || ctx == 0 || attr_ctx[dev] != ctx) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_ctx[dev] = current_context_id();
+  }
+  const bool pre = a.dh != nullptr;
+  const bool need_y = a.dy != nullptr && (a.w_post != nullptr || a.gate != nullptr);
+  const int x_bytes = F32 ? 4 : 2;
+  BwdRing r{};
+  r.off_d = pre ? 2 * a.d : 0;
+  r.off_x = r.off_d + (a.dx_out ? x_bytes * a.d : 0);
+  r.off_y = r.off_x + (pre ? (FROM8 ? 1 : x_bytes) * a.d : 0);
+  r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
+  r.teams = kBwdWarps / W;
+  auto sums = [&](int teams) { return teams > 1 ? 4 * a.d : 0; };
+  while (r.teams > 1 && r.teams * 2 * r.bytes + sums(r.teams) > kBwdSmem) --r.teams;
+  r.stages = 2;
+  while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + sums(r.teams) <= kBwdSmem)
+    ++r.stages;
+  const int smem = r.teams * r.stages * r.bytes + sums(r.teams);
+  kernel<<<a.blocks, r.teams * W * 32, smem, st>>>(a, r);
+  return cudaGetLastError();
+}
+
+template <int CH, bool MULTI>
+cudaError_t bwd_of(const BlockNormBwdArgs& a, bool f32, int W, cudaStream_t st) {
+  const bool from8 = a.xhat_q != nullptr || a.yhat_q != nullptr;
+  if (f32)
+    return from8 ? bwd_typed<CH, MULTI, true, true>(a, W, st) : bwd_typed<CH, MULTI, true, false>(a, W, st);
+  return from8 ? bwd_typed<CH, MULTI, false, true>(a, W, st) : bwd_typed<CH, MULTI, false, false>(a, W, st);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm_fwd(const BlockNormFwdArgs& a, bool x_fp32, cudaStream_t st) {
+  // Up to 1024 columns a row is one warp's; beyond, W warps share it.
+  const int W = (a.d + 1023) / 1024, ch = (a.d + 256 * W - 1) / (256 * W);
+  if (W == 1) {
+    if (ch == 1) return fwd_of<1, false>(a, x_fp32, W, st);
+    if (ch == 2) return fwd_of<2, false>(a, x_fp32, W, st);
+    if (ch == 3) return fwd_of<3, false>(a, x_fp32, W, st);
+    return fwd_of<4, false>(a, x_fp32, W, st);
+  }
+  if (ch <= 3) return fwd_of<3, true>(a, x_fp32, W, st);
+  return fwd_of<4, true>(a, x_fp32, W, st);
+}
+
+BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
+  BlockNormBwdPlan p{};
+  const int W = (d + kBwdCols - 1) / kBwdCols, teams = kBwdWarps / W;
+  const bool shared = G > 1 && G < N;
+  if (!shared) {
+    const int want = (N + teams - 1) / teams;
+    p.blocks = want < 1 ? 1 : (want < kBwdBlocks ? want : kBwdBlocks);
+    p.slices = p.items = p.blocks;
+    p.gate_parts = G == 1 && N > 1;
+    return p;
+  }
+  // About four items per block, so that their number divides well, and none
+  // without rows.
+  const int rows = N / G;
+  int s = 4 * kBwdBlocks / G;
+  s = s < 1 ? 1 : (s < rows ? s : rows);
+  p.slices = s;
+  p.items = G * s;
+  p.blocks = p.items < kBwdBlocks ? p.items : kBwdBlocks;
+  p.gate_parts = s > 1;
+  return p;
+}
+
+cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool x_fp32, cudaStream_t st) {
+  const int W = (a.d + kBwdCols - 1) / kBwdCols, ch = (a.d + 256 * W - 1) / (256 * W);
+  cudaError_t e;
+  if (W == 1)
+    e = ch == 1   ? bwd_of<1, false>(a, x_fp32, W, st)
+        : ch == 2 ? bwd_of<2, false>(a, x_fp32, W, st)
+                  : bwd_of<3, false>(a, x_fp32, W, st);
+  else
+    e = ch <= 2 ? bwd_of<2, true>(a, x_fp32, W, st) : bwd_of<3, true>(a, x_fp32, W, st);
+  if (e != cudaSuccess) return e;
+  SumJobs j{};
+  j.d = a.d;
+  j.n_pre = a.dh != nullptr;
+  j.n_post = a.w_post != nullptr;
+  j.pre = {a.part_pre, a.dw_pre, a.blocks, true};
+  j.post = {a.part_post, a.dw_post, a.blocks, true};
+  j.gate = {a.part_gate, a.dgate, a.slices, a.gate_fp32};
+  const int rows = j.n_pre + j.n_post + (a.part_gate ? a.items / a.slices : 0);
+  if (rows == 0) return cudaSuccess;
+  sum_parts_kernel<<<dim3((a.d + 31) / 32, rows), 256, 0, st>>>(j);
+  return cudaGetLastError();
+}
+
+cudaError_t take_norm_status(cudaStream_t st, unsigned* out) {
+  unsigned val = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&val, g_norm_status, sizeof(val), 0,
+                                            cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && val)
+    e = cudaMemcpyToSymbolAsync(g_norm_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  *out = val;
+  return e;
+}
+
+}  // namespace detattn

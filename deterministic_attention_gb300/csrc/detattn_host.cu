@@ -18,6 +18,7 @@
 
 #include "../../include/detattn.h"
 #include "attn_launch.h"
+#include "block_launch.h"
 #include "embed_launch.h"
 #include "layer_launch.h"
 
@@ -1167,6 +1168,95 @@ int check_embed_shape(int N, int V, int E) {
   return DETATTN_OK;
 }
 
+// ------------------------------------------------------------ block norms, checkpoints, gated unit
+int check_act8_shape(int rows, int d) {
+  if (rows < 0 || rows > (1 << 30)) return fail(DETATTN_ERR_SHAPE, "rows=%d: must be in [0, 2^30]", rows);
+  if (d < kAct8Group || d % kAct8Group != 0 || d > (1 << 20))
+    return fail(DETATTN_ERR_SHAPE, "d=%d columns: must be a positive multiple of 32 up to 2^20", d);
+  if (static_cast<double>(rows) * d > 68719476736.0)
+    return fail(DETATTN_ERR_SHAPE, "checkpoint too large (rows=%d d=%d)", rows, d);
+  return DETATTN_OK;
+}
+
+int check_wgrad_shape(int rows, int d, int n) {
+  if (rows < 0 || rows > (1 << 24)) return fail(DETATTN_ERR_SHAPE, "rows=%d: must be in [0, 2^24]", rows);
+  if (d < kAct8Group || d % kAct8Group != 0 || d > (1 << 20))
+    return fail(DETATTN_ERR_SHAPE, "d=%d columns: must be a positive multiple of 32 up to 2^20", d);
+  if (n < 8 || n % 8 != 0 || n > (1 << 20))
+    return fail(DETATTN_ERR_SHAPE, "n=%d columns: must be a positive multiple of 8 up to 2^20", n);
+  if (static_cast<double>(rows) * d > 4.0e9 || static_cast<double>(rows) * n > 4.0e9 ||
+      static_cast<double>(d) * n > 4.0e9)
+    return fail(DETATTN_ERR_SHAPE, "weight gradient too large (rows=%d d=%d n=%d)", rows, d, n);
+  return DETATTN_OK;
+}
+size_t wgrad_partial_bytes(const Act8WgradPlan& p) {
+  if (p.splits == 1) return 0;
+  const size_t rem = static_cast<size_t>(p.tiles_m) * p.tiles_n - p.whole_tiles;
+  return rem * p.splits * kWgradBM * kWgradBN * sizeof(float);
+}
+
+int check_swiglu(int rows, int f, bool kept) {
+  const int step = kept ? kAct8Group : 8;
+  if (rows < 0 || rows > (1 << 30)) return fail(DETATTN_ERR_SHAPE, "rows=%d: must be in [0, 2^30]", rows);
+  if (f < step || f % step != 0 || f > (1 << 20))
+    return fail(DETATTN_ERR_SHAPE, "f=%d columns: must be a positive multiple of %d up to 2^20", f, step);
+  if (static_cast<double>(rows) * f > 17179869184.0)
+    return fail(DETATTN_ERR_SHAPE, "gated unit too large (rows=%d f=%d)", rows, f);
+  return DETATTN_OK;
+}
+
+int check_norm_shape(int N, int d, int G, bool kept) {
+  const int step = kept ? kAct8Group : 8;
+  if (N < 0 || N > (1 << 30)) return fail(DETATTN_ERR_SHAPE, "N=%d rows: must be in [0, 2^30]", N);
+  if (d < step || d % step != 0 || d > kNormMaxD)
+    return fail(DETATTN_ERR_SHAPE, "d=%d columns: must be a positive multiple of %d up to %d", d, step,
+                kNormMaxD);
+  if (static_cast<double>(N) * d > 68719476736.0)
+    return fail(DETATTN_ERR_SHAPE, "norm too large (N=%d d=%d)", N, d);
+  if (G < 1 || (N > 0 && (G > N || N % G != 0)))
+    return fail(DETATTN_ERR_SHAPE, "G=%d gate rows: must divide N=%d", G, N);
+  return DETATTN_OK;
+}
+int check_flags(std::initializer_list<int> flags) {
+  for (int f : flags)
+    if (f != 0 && f != 1) return fail(DETATTN_ERR_SHAPE, "type and sigmoid flags must be 0 or 1");
+  return DETATTN_OK;
+}
+// Pointers that must be given (`must`) are not NULL and aligned; all others
+// must be NULL.
+struct NormPtr {
+  const void* p;
+  bool must;
+  bool aligned;
+  const char* name;
+};
+int check_norm_ptrs(std::initializer_list<NormPtr> ps) {
+  for (const NormPtr& p : ps) {
+    if (p.must && p.p == nullptr) return fail(DETATTN_ERR_NULL, "%s is NULL", p.name);
+    if (!p.must && p.p != nullptr)
+      return fail(DETATTN_ERR_NULL, "%s is given, but what it belongs to is not", p.name);
+  }
+  for (const NormPtr& p : ps)
+    if (p.aligned && !aligned16(p.p)) return fail(DETATTN_ERR_ALIGN, "%s is not 16-byte aligned", p.name);
+  return DETATTN_OK;
+}
+
+// Workspace of block_norm_bwd: the blocks' column sums for dw_pre and
+// dw_post, then the items' for dgate.
+struct NormLayout {
+  size_t pre, post, gate, total;
+};
+NormLayout norm_layout(const BlockNormBwdPlan& p, int d) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  NormLayout l{};
+  const size_t row = sizeof(float) * static_cast<size_t>(d);
+  l.pre = 0;
+  l.post = up(row * p.blocks);
+  l.gate = l.post + up(row * p.blocks);
+  l.total = l.gate + up(row * p.items);
+  return l;
+}
+
 }  // namespace
 
 namespace detattn {
@@ -1533,6 +1623,285 @@ int layer_train_step(const void* x, const void* dy, float* w_qkv, float* w_o, fl
   return rc != DETATTN_OK ? rc : jw;
 }
 
+int act8_pack(const void* x, void* q, void* e, int rows, int d, void* stream) {
+  int rc;
+  if ((rc = check_act8_shape(rows, d)) != DETATTN_OK) return rc;
+  if (rows == 0) return ok_status();
+  if ((rc = check_ptrs({{x, "x"}, {q, "q"}})) != DETATTN_OK) return rc;
+  if (e == nullptr) return fail(DETATTN_ERR_NULL, "e is NULL");
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  return launched(launch_act8_pack(x, static_cast<int8_t*>(q), static_cast<uint8_t*>(e), rows, d,
+                                   static_cast<cudaStream_t>(stream)),
+                  "act8_pack");
+}
+
+int act8_unpack(const void* q, const void* e, void* x, int rows, int d, void* stream) {
+  int rc;
+  if ((rc = check_act8_shape(rows, d)) != DETATTN_OK) return rc;
+  if (rows == 0) return ok_status();
+  if ((rc = check_ptrs({{q, "q"}, {x, "x"}})) != DETATTN_OK) return rc;
+  if (e == nullptr) return fail(DETATTN_ERR_NULL, "e is NULL");
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  return launched(launch_act8_unpack(static_cast<const int8_t*>(q), static_cast<const uint8_t*>(e),
+                                     x, rows, d, static_cast<cudaStream_t>(stream)),
+                  "act8_unpack");
+}
+
+size_t act8_wgrad_workspace_bytes(int rows, int d, int n) {
+  if (check_wgrad_shape(rows, d, n) != DETATTN_OK || rows == 0) return 0;
+  return wgrad_partial_bytes(act8_wgrad_plan(rows, d, n));
+}
+
+int act8_wgrad(const void* q, const void* e, const void* dy, const float* row_scale, float* dw,
+               void* workspace, size_t workspace_bytes, int rows, int d, int n, void* stream) {
+  int rc;
+  if ((rc = check_wgrad_shape(rows, d, n)) != DETATTN_OK) return rc;
+  if ((rc = check_ptrs({{dw, "dw"}})) != DETATTN_OK) return rc;
+  if (row_scale != nullptr && !aligned16(row_scale))
+    return fail(DETATTN_ERR_ALIGN, "row_scale is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Act8WgradArgs a{};
+  if (rows > 0) {
+    if ((rc = check_ptrs({{q, "q"}, {dy, "dy"}})) != DETATTN_OK) return rc;
+    if (e == nullptr) return fail(DETATTN_ERR_NULL, "e is NULL");
+    const Act8WgradPlan p = act8_wgrad_plan(rows, d, n);
+    const size_t need = wgrad_partial_bytes(p);
+    if (need > 0) {
+      if (workspace == nullptr || workspace_bytes < need)
+        return fail(DETATTN_ERR_WORKSPACE, "act8_wgrad workspace needs %zu bytes, got %zu%s", need,
+                    workspace_bytes, workspace ? "" : " (NULL)");
+      if (!aligned16(workspace)) return fail(DETATTN_ERR_ALIGN, "workspace is not 16-byte aligned");
+    }
+    a.e = static_cast<const uint8_t*>(e);
+    a.row_scale = row_scale;
+    a.dw = dw;
+    a.partial = static_cast<float*>(workspace);
+    a.rows = rows;
+    a.d = d;
+    a.n = n;
+    a.tiles_m = p.tiles_m;
+    a.tiles_n = p.tiles_n;
+    a.whole_tiles = p.whole_tiles;
+    a.splits = p.splits;
+    a.wait_ns = g_wait_ns;
+  }
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  if (rows == 0)
+    return launched(cudaMemsetAsync(dw, 0, static_cast<size_t>(d) * n * sizeof(float), st),
+                    "act8_wgrad (zeros)");
+  CUtensorMap mq, mdy;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+  const cuuint32_t box[2] = {kWgradBM, kWgradBK};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DETATTN_ERR_CUDA, "tensor map for q: CUresult %d", (int)r);
+  if ((rc = encode_2d(&mdy, dy, n, rows, n, 64, kWgradBK, "dy")) != DETATTN_OK) return rc;
+  return launched(launch_act8_wgrad(mq, mdy, a, st), "act8_wgrad");
+}
+
+int swiglu_fwd(const void* u, void* h, void* u_q, void* u_e, int rows, int f, void* stream) {
+  int rc;
+  if ((rc = check_swiglu(rows, f, u_q != nullptr || u_e != nullptr)) != DETATTN_OK) return rc;
+  if (rows == 0) return ok_status();
+  if ((rc = check_ptrs({{u, "u"}, {h, "h"}})) != DETATTN_OK) return rc;
+  const bool kept = u_q != nullptr || u_e != nullptr;
+  if ((rc = check_norm_ptrs({{u_q, kept, true, "u_q"}, {u_e, kept, false, "u_e"}})) != DETATTN_OK)
+    return rc;
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  return launched(launch_swiglu_fwd(u, h, static_cast<int8_t*>(u_q), static_cast<uint8_t*>(u_e),
+                                    rows, f, static_cast<cudaStream_t>(stream)),
+                  "swiglu_fwd");
+}
+
+int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, void* du, void* h,
+               int rows, int f, void* stream) {
+  int rc;
+  const bool kept = u_q != nullptr || u_e != nullptr;
+  if ((rc = check_swiglu(rows, f, kept)) != DETATTN_OK) return rc;
+  if (rows == 0) return ok_status();
+  if ((rc = check_ptrs({{dh, "dh"}, {du, "du"}})) != DETATTN_OK) return rc;
+  if ((rc = check_norm_ptrs({{u, !kept, true, "u"},
+                             {u_q, kept, true, "u_q"},
+                             {u_e, kept, false, "u_e"},
+                             {h, h != nullptr, true, "h"}})) != DETATTN_OK)
+    return rc;
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  return launched(launch_swiglu_bwd(dh, u, static_cast<const int8_t*>(u_q),
+                                    static_cast<const uint8_t*>(u_e), du, h, rows, f,
+                                    static_cast<cudaStream_t>(stream)),
+                  "swiglu_bwd");
+}
+
+int block_norm_fwd(const void* x, const void* y, const void* gate, const float* w_post,
+                   const float* w_pre, void* x_out, void* h, float* rstd_post, float* rstd_pre,
+                   void* yhat_q, void* yhat_e, void* xhat_q, void* xhat_e, int N, int d, int G,
+                   int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale, float block_scale,
+                   float eps, void* stream) {
+  int rc;
+  const bool keep_y = yhat_q != nullptr || yhat_e != nullptr;
+  const bool keep_x = xhat_q != nullptr || xhat_e != nullptr;
+  if ((rc = check_norm_shape(N, d, G, keep_x || keep_y)) != DETATTN_OK) return rc;
+  if ((rc = check_flags({x_fp32, gate_fp32, gate_sigmoid})) != DETATTN_OK) return rc;
+  if (!std::isfinite(res_scale) || !std::isfinite(block_scale))
+    return fail(DETATTN_ERR_SCALE, "res_scale and block_scale must be finite");
+  if (!std::isfinite(eps) || !(eps > 0.f)) return fail(DETATTN_ERR_SCALE, "eps=%g must be finite and > 0", eps);
+  if (N == 0) return ok_status();
+  const bool block = y != nullptr, pre = w_pre != nullptr, post = w_post != nullptr;
+  if (!block && !pre) return fail(DETATTN_ERR_NULL, "y and w_pre are both NULL: nothing to do");
+  if ((rc = check_norm_ptrs({{x, true, true, "x"},
+                             {y, block, true, "y"},
+                             {gate, block && gate != nullptr, true, "gate"},
+                             {w_post, block && post, true, "w_post"},
+                             {w_pre, pre, true, "w_pre"},
+                             {x_out, block, true, "x_out"},
+                             {h, pre, true, "h"},
+                             {rstd_post, post, true, "rstd_post"},
+                             {rstd_pre, pre, true, "rstd_pre"},
+                             {yhat_q, block && keep_y, true, "yhat_q"},
+                             {yhat_e, block && keep_y, false, "yhat_e"},
+                             {xhat_q, pre && keep_x, true, "xhat_q"},
+                             {xhat_e, pre && keep_x, false, "xhat_e"}})) != DETATTN_OK)
+    return rc;
+  if (block && pre && keep_x != keep_y)
+    return fail(DETATTN_ERR_NULL, "the checkpoints of yhat and xhat are kept both or neither");
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  BlockNormFwdArgs a{};
+  a.x = x;
+  a.y = y;
+  a.gate = gate;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.x_out = x_out;
+  a.h = h;
+  a.rstd_post = rstd_post;
+  a.rstd_pre = rstd_pre;
+  a.yhat_q = static_cast<int8_t*>(yhat_q);
+  a.yhat_e = static_cast<uint8_t*>(yhat_e);
+  a.xhat_q = static_cast<int8_t*>(xhat_q);
+  a.xhat_e = static_cast<uint8_t*>(xhat_e);
+  a.N = N;
+  a.d = d;
+  a.rows_per_gate = N / G;
+  a.gate_fp32 = gate_fp32 != 0;
+  a.gate_sigmoid = gate_sigmoid != 0;
+  a.res_scale = res_scale;
+  a.block_scale = block_scale;
+  a.eps = eps;
+  return launched(launch_block_norm_fwd(a, x_fp32 != 0, static_cast<cudaStream_t>(stream)),
+                  "block_norm_fwd");
+}
+
+size_t block_norm_bwd_workspace_bytes(int N, int d, int G) {
+  if (check_norm_shape(N, d, G, false) != DETATTN_OK || N == 0) return 0;
+  return norm_layout(block_norm_bwd_plan(N, d, G), d).total;
+}
+
+int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void* y,
+                   const void* xhat_q, const void* xhat_e, const void* yhat_q, const void* yhat_e,
+                   const void* gate, const float* w_post, const float* w_pre,
+                   const float* rstd_post, const float* rstd_pre, void* dx, void* dy, void* dgate,
+                   float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes, int N,
+                   int d, int G, int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale,
+                   float block_scale, void* stream) {
+  int rc;
+  const bool from_x8 = xhat_q != nullptr || xhat_e != nullptr;
+  const bool from_y8 = yhat_q != nullptr || yhat_e != nullptr;
+  if ((rc = check_norm_shape(N, d, G, from_x8 || from_y8)) != DETATTN_OK) return rc;
+  if ((rc = check_flags({x_fp32, gate_fp32, gate_sigmoid})) != DETATTN_OK) return rc;
+  if (!std::isfinite(res_scale) || !std::isfinite(block_scale))
+    return fail(DETATTN_ERR_SCALE, "res_scale and block_scale must be finite");
+  const bool pre = w_pre != nullptr, post = w_post != nullptr;
+  if (N > 0) {
+    const bool block = dy != nullptr, gated = gate != nullptr;
+    const bool need_y = block && (post || gated);
+    if (dx_out == nullptr && !pre)
+      return fail(DETATTN_ERR_NULL, "dx_out and w_pre are both NULL: no gradient to carry back");
+    if (from_x8 && y != nullptr && need_y)
+      return fail(DETATTN_ERR_NULL, "xhat comes from a checkpoint and yhat from a tensor: one kind for both");
+    if (from_y8 && x != nullptr && pre)
+      return fail(DETATTN_ERR_NULL, "yhat comes from a checkpoint and xhat from a tensor: one kind for both");
+    if ((rc = check_norm_ptrs({{dx_out, dx_out != nullptr, true, "dx_out"},
+                               {dh, pre, true, "dh"},
+                               {x, pre && !from_x8, true, "x"},
+                               {xhat_q, pre && from_x8, true, "xhat_q"},
+                               {xhat_e, pre && from_x8, false, "xhat_e"},
+                               {y, need_y && !from_y8, true, "y"},
+                               {yhat_q, need_y && from_y8, true, "yhat_q"},
+                               {yhat_e, need_y && from_y8, false, "yhat_e"},
+                               {gate, block && gated, true, "gate"},
+                               {w_post, block && post, true, "w_post"},
+                               {rstd_post, block && post, true, "rstd_post"},
+                               {rstd_pre, pre, true, "rstd_pre"},
+                               {dx, true, true, "dx"},
+                               {dgate, block && gated, true, "dgate"},
+                               {dw_post, block && post, true, "dw_post"},
+                               {dw_pre, pre, true, "dw_pre"}})) != DETATTN_OK)
+      return rc;
+    if (!aligned16(dy)) return fail(DETATTN_ERR_ALIGN, "dy is not 16-byte aligned");
+  } else if ((rc = check_norm_ptrs({{dgate, gate != nullptr, true, "dgate"},
+                                    {dw_post, post, true, "dw_post"},
+                                    {dw_pre, pre, true, "dw_pre"}})) != DETATTN_OK) {
+    return rc;
+  }
+  const BlockNormBwdPlan p = block_norm_bwd_plan(N, d, G);
+  const NormLayout l = norm_layout(p, d);
+  if (N > 0) {
+    if (workspace == nullptr || workspace_bytes < l.total)
+      return fail(DETATTN_ERR_WORKSPACE, "block_norm_bwd workspace needs %zu bytes, got %zu%s",
+                  l.total, workspace_bytes, workspace ? "" : " (NULL)");
+    if (!aligned16(workspace)) return fail(DETATTN_ERR_ALIGN, "workspace is not 16-byte aligned");
+  }
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    cudaError_t e = cudaSuccess;
+    if (pre) e = cudaMemsetAsync(dw_pre, 0, sizeof(float) * d, st);
+    if (e == cudaSuccess && post) e = cudaMemsetAsync(dw_post, 0, sizeof(float) * d, st);
+    if (e == cudaSuccess && gate != nullptr)
+      e = cudaMemsetAsync(dgate, 0, static_cast<size_t>(G) * d * (gate_fp32 ? 4 : 2), st);
+    return launched(e, "block_norm_bwd (zeros)");
+  }
+  char* w = static_cast<char*>(workspace);
+  BlockNormBwdArgs a{};
+  a.dx_out = dx_out;
+  a.dh = dh;
+  a.x = x;
+  a.y = y;
+  a.xhat_q = static_cast<const int8_t*>(xhat_q);
+  a.xhat_e = static_cast<const uint8_t*>(xhat_e);
+  a.yhat_q = static_cast<const int8_t*>(yhat_q);
+  a.yhat_e = static_cast<const uint8_t*>(yhat_e);
+  a.gate = gate;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.rstd_post = rstd_post;
+  a.rstd_pre = rstd_pre;
+  a.dx = dx;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.dw_post = dw_post;
+  a.dw_pre = dw_pre;
+  a.N = N;
+  a.d = d;
+  a.rows_per_gate = N / G;
+  a.gate_fp32 = gate_fp32 != 0;
+  a.gate_sigmoid = gate_sigmoid != 0;
+  a.res_scale = dy != nullptr ? res_scale : 1.0f;
+  a.block_scale = block_scale;
+  a.part_pre = reinterpret_cast<float*>(w + l.pre);
+  a.part_post = reinterpret_cast<float*>(w + l.post);
+  a.part_gate = gate != nullptr && p.gate_parts ? reinterpret_cast<float*>(w + l.gate) : nullptr;
+  a.slices = p.slices;
+  a.items = p.items;
+  a.blocks = p.blocks;
+  a.wait_ns = g_wait_ns;
+  return launched(launch_block_norm_bwd(a, x_fp32 != 0, st), "block_norm_bwd");
+}
+
 int detattn_check_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned f = 0, b = 0, em = 0, ly = 0;
@@ -1543,6 +1912,11 @@ int detattn_check_status(void* stream) {
   unsigned dsf = 0;
   if (e == cudaSuccess) e = take_ds_status(st, &dsf);
   if (dsf) b |= 32u;
+  unsigned wg = 0, nm = 0;
+  if (e == cudaSuccess) e = take_wgrad_status(st, &wg);
+  if (e == cudaSuccess) e = take_norm_status(st, &nm);
+  if (wg) ly |= 2u;
+  if (nm) ly |= 4u;
   if (e != cudaSuccess) return fail(DETATTN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (em & 1u)
     return fail(DETATTN_ERR_INDEX,

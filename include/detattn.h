@@ -326,6 +326,122 @@ int layer_train_step(const void* x, const void* dy, float* w_qkv, float* w_o, fl
                      float lr, float weight_decay, float beta1, float beta2, float eps,
                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the layer: block norms, activation checkpoints in 8 bits, the gated
+ * unit (RustingBrain vs PyTorch/TensorFlow page, "The setup": a decoder-only
+ * model with RMSNorm and SwiGLU; the checkpoints have no counterpart on the
+ * pages).  Every result is written once in a fixed order, with no atomics on
+ * data, so repeated calls give identical bytes.  All arithmetic between the
+ * loads and the one rounding of each store is fp32.
+ *
+ * A checkpoint of a [rows, d] activation (d a multiple of 32) is two arrays:
+ *   q int8  [rows, d]         e uint8 [rows, d / 32]
+ * one exponent byte for every 32 consecutive columns of a row; the value is
+ * q 2^(e - 127).  e is the smallest byte >= 1 for which no magnitude in the
+ * group exceeds 127 2^(e - 127), and q the value over 2^(e - 127) rounded to
+ * the nearest whole number, ties to even (at the largest exponent, e = 249,
+ * within +-63: 64 2^122 would be infinity).  A group that holds an infinity or
+ * a NaN is stored as e = 255 with q = 0 and reads back as NaN throughout.
+ * Every checkpointed value is a bf16 number.
+ */
+
+/* Writes the checkpoint (q, e) of x, bf16 [rows, d].  rows in [0, 2^30], d a
+ * multiple of 32 in [32, 2^20]; rows * d at most 2^36.  16-byte aligned
+ * device pointers (e, whose rows are d / 32 bytes, needs no alignment). */
+int act8_pack(const void* x, void* q, void* e, int rows, int d, void* stream);
+
+/* Reads a checkpoint back: x bf16 [rows, d].  Exact for every e in [1, 249]
+ * (all that act8_pack and the calls below write, besides 255). */
+int act8_unpack(const void* q, const void* e, void* x, int rows, int d, void* stream);
+
+/* Bytes of workspace act8_wgrad needs: fp32 128 x 256 tiles of partial sums,
+ * one for every token range of every tile that is cut (fixed by the shape).
+ * 0 for an invalid shape, and where no tile is cut. */
+size_t act8_wgrad_workspace_bytes(int rows, int d, int n);
+
+/* Weight gradient from the checkpoint of the layer's input:
+ *   dw[i, j] = row_scale[i] * sum_t x[t, i] dy[t, j],   x the checkpoint's values
+ * dy bf16 [rows, n]; dw fp32 [d, n], fully overwritten (zeros for rows = 0);
+ * row_scale fp32 [d] or NULL (1): the norm's weight where the checkpoint
+ * holds the normed input before it (block_norm_fwd).  bf16 tensor cores, fp32
+ * accumulation; each element's sum has a fixed order.  rows in [0, 2^24], d a
+ * multiple of 32 and n of 8, both up to 2^20, rows * d, rows * n and d * n
+ * at most 4e9.  q, dy, dw, row_scale and workspace 16-byte aligned. */
+int act8_wgrad(const void* q, const void* e, const void* dy, const float* row_scale, float* dw,
+               void* workspace, size_t workspace_bytes, int rows, int d, int n, void* stream);
+
+/* Gated unit: with u = [a | b], bf16 [rows, 2 f], h = a sigma(a) b, bf16
+ * [rows, f].  u_q, u_e (both or neither NULL): the checkpoint of u.  rows in
+ * [0, 2^30], f a multiple of 8 (of 32 with a checkpoint), rows * f at most
+ * 2^34.  h and u must not overlap. */
+int swiglu_fwd(const void* u, void* h, void* u_q, void* u_e, int rows, int f, void* stream);
+
+/* Its backward from dh, bf16 [rows, f], and either u (u_q, u_e NULL) or its
+ * checkpoint (u NULL): du = [da | db], bf16 [rows, 2 f],
+ *   da = dh b s (1 + a (1 - s)),  db = dh a s,  s = sigma(a)
+ * and, where h is not NULL, h again (from the same a, b), for the weight
+ * gradient of the projection that follows.  du must not overlap the inputs. */
+int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, void* du, void* h,
+               int rows, int f, void* stream);
+
+/* Norms after and before a block, with the block's gate, its scale and the
+ * residual stream.  For each of N rows of width d, with every norm
+ * v / sqrt(mean(v^2) + eps) and g the gate, or its sigmoid with gate_sigmoid:
+ *
+ *   yhat = norm(y), z = yhat * w_post     (w_post NULL: yhat = z = y)
+ *   x' = res_scale x + block_scale g z    (gate NULL: g = 1; y NULL: x' = x)
+ *   xhat = norm(x'), h = xhat * w_pre     (w_pre NULL: neither)
+ *
+ * x, x_out: the residual stream [N, d], bf16, or fp32 with x_fp32; y, h: bf16
+ * [N, d]; w_post, w_pre: fp32 [d].  gate: [G, d], G dividing N, fp32 with
+ * gate_fp32, else bf16: row t takes gate row t / (N / G) (G = 1: one for
+ * every channel; G = the sequences of a batch; G = N: one for every
+ * element).  The norm before the block takes x' before its rounding to the
+ * stream's type.
+ * Outputs: x_out = x' (with y; may be x itself), h (with w_pre), rstd_post
+ * and rstd_pre fp32 [N] = 1 / sqrt(mean + eps) (with w_post, w_pre), and,
+ * where not NULL, the checkpoints of yhat (with y) and xhat (with w_pre), for
+ * block_norm_bwd.  y or w_pre (or both) must be given; an argument that
+ * needs another which is NULL must be NULL as well (w_post, gate, x_out,
+ * yhat_q: y; rstd_post: w_post; h, rstd_pre, xhat_q: w_pre), and outputs named here with "(with ...)" must be given.
+ * N in [0, 2^30], d a multiple of 8 (of 32 with checkpoints) in [8, 8192],
+ * N * d at most 2^36.  eps > 0; the scales finite.  16-byte aligned pointers
+ * (yhat_e and xhat_e need none). */
+int block_norm_fwd(const void* x, const void* y, const void* gate, const float* w_post,
+                   const float* w_pre, void* x_out, void* h, float* rstd_post, float* rstd_pre,
+                   void* yhat_q, void* yhat_e, void* xhat_q, void* xhat_e, int N, int d, int G,
+                   int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale, float block_scale,
+                   float eps, void* stream);
+
+/* Bytes of workspace block_norm_bwd needs (column sums of its blocks; G = 1
+ * without a gate).  0 for an invalid shape or N = 0. */
+size_t block_norm_bwd_workspace_bytes(int N, int d, int G);
+
+/* Backward.  From dx_out, the gradient of x' (the stream's type; NULL: zero),
+ * and dh (bf16; NULL where w_pre is), with
+ *   D  = dx_out + rstd_pre (dh w_pre - xhat mean(dh w_pre xhat)),
+ *   dz = block_scale g D:
+ *   dx = res_scale D           (the stream's type; without a block, y's side, D)
+ *   dy = rstd_post (dz w_post - yhat mean(dz w_post yhat))   (w_post NULL: dz)
+ *   dgate = block_scale (yhat w_post) D, through the sigmoid where it is one,
+ *           summed over the rows that share a gate row (the gate's type)
+ *   dw_pre = sum_t dh xhat, dw_post = sum_t dz yhat          (fp32 [d])
+ * xhat is x * rstd_pre from x = the forward's x', or the checkpoint xhat_q,
+ * xhat_e; yhat is y * rstd_post (y without w_post), or the checkpoint.
+ * Both hats come from tensors or both from checkpoints.  dy NULL: there was
+ * no block (then y, gate, w_post and the scales are not used and the first
+ * three must be NULL).  y or its checkpoint is needed with w_post or gate,
+ * x or its checkpoint with dh.  dx_out or dh must be given.  dx may be
+ * dx_out itself, dy may be y.  Every output is fully overwritten; for N = 0 the sums are
+ * zero.  Shapes and flags as in block_norm_fwd. */
+int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void* y,
+                   const void* xhat_q, const void* xhat_e, const void* yhat_q, const void* yhat_e,
+                   const void* gate, const float* w_post, const float* w_pre,
+                   const float* rstd_post, const float* rstd_pre, void* dx, void* dy, void* dgate,
+                   float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes, int N,
+                   int d, int G, int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale,
+                   float block_scale, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device-side status word
  * that kernels set when a pipeline wait runs out (a bounded wait, default
  * limit 1 s).  Returns DETATTN_OK, DETATTN_ERR_DEVICE_TIMEOUT,
