@@ -12,6 +12,7 @@ Layouts: q, o, dout, dq are bf16 [B, T, Hq, D]; k, v, dk, dv are bf16
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -146,7 +147,9 @@ def _check(rc: int, where: str):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # The raw handle of the current device's current stream: 0.2 us, against
+    # 2.9 us for building the torch.cuda.Stream object around it.
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
@@ -439,12 +442,17 @@ class BlockNormGrads(NamedTuple):
     dw_pre: Optional[torch.Tensor]
 
 
-def _need_current(t, name):
-    """The calls run on the current device's current stream: what lies on
-    another device is refused."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _on_device(t, name, dtype, shape, dev):
+    """_need, on the device with index `dev`; one test where all is well."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t, name):
@@ -453,45 +461,65 @@ def _rows(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() < 1 or t.shape[-1] == 0:
         raise ValueError(f"{name} must be [..., d] with d >= 1")
-    return t.numel() // t.shape[-1], t.shape[-1]
+    d = t.shape[-1]
+    return t.numel() // d, d
 
 
-def _need_act8(c, name, shape):
+def _current(t, name):
+    """The current device's index; what is on the CPU has none.  (The calls run
+    on the current device's current stream; a tensor of another device is
+    refused by _on_device.)"""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (no CPU path)")
+    return torch._C._cuda_getDevice()
+
+
+def _need_act8(c, name, shape, dev):
     if not isinstance(c, tuple) or len(c) != 2:
         raise TypeError(f"{name} must be an Act8 (q, e)")
-    _need(c[0], name + ".q", torch.int8, shape)
-    _need(c[1], name + ".e", torch.uint8, tuple(shape[:-1]) + (shape[-1] // 32,))
+    _on_device(c[0], name + ".q", torch.int8, shape, dev)
+    _on_device(c[1], name + ".e", torch.uint8, shape[:-1] + (shape[-1] // 32,), dev)
 
 
 def _new_act8(shape, device):
     if shape[-1] % 32:
         raise ValueError(f"an 8-bit checkpoint needs a multiple of 32 columns, got {shape[-1]}")
     return Act8(torch.empty(shape, dtype=torch.int8, device=device),
-                torch.empty(tuple(shape[:-1]) + (shape[-1] // 32,), dtype=torch.uint8, device=device))
+                torch.empty(shape[:-1] + (shape[-1] // 32,), dtype=torch.uint8, device=device))
 
 
 def act8_pack(x, out=None):
     """The 8-bit checkpoint of x, bf16 [..., d], d a multiple of 32."""
     rows, d = _rows(x, "x")
-    _need(x, "x", torch.bfloat16, x.shape)
-    _need_current(x, "x")
-    c = _new_act8(x.shape, x.device) if out is None else out
-    _need_act8(c, "out", tuple(x.shape))
-    _check(lib().act8_pack(_ptr(x), _ptr(c[0]), _ptr(c[1]), rows, d, _stream()), "act8_pack")
+    dev = _current(x, "x")
+    _on_device(x, "x", torch.bfloat16, x.shape, dev)
+    c = out
+    if c is None:
+        c = _new_act8(x.shape, x.device)
+    else:
+        _need_act8(c, "out", x.shape, dev)
+    _check(lib().act8_pack(x.data_ptr(), c[0].data_ptr(), c[1].data_ptr(), rows, d, _stream()),
+           "act8_pack")
     return c
 
 
 def act8_unpack(c, out=None):
     """The values of an 8-bit checkpoint, bf16 [..., d] (exact)."""
-    rows, d = _rows(c[0], "q")
-    _need_act8(c, "checkpoint", tuple(c[0].shape))
-    _need_current(c[0], "checkpoint")
-    x = torch.empty(c[0].shape, dtype=torch.bfloat16, device=c[0].device) if out is None else out
-    _need(x, "out", torch.bfloat16, c[0].shape)
-    _check(lib().act8_unpack(_ptr(c[0]), _ptr(c[1]), _ptr(x), rows, d, _stream()), "act8_unpack")
+    q, e = c
+    rows, d = _rows(q, "q")
+    dev = _current(q, "q")
+    _need_act8(c, "checkpoint", q.shape, dev)
+    x = out
+    if x is None:
+        x = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _on_device(x, "out", torch.bfloat16, q.shape, dev)
+    _check(lib().act8_unpack(q.data_ptr(), e.data_ptr(), x.data_ptr(), rows, d, _stream()),
+           "act8_unpack")
     return x
 
 
+@functools.lru_cache(maxsize=256)
 def act8_wgrad_workspace_bytes(rows, d, n) -> int:
     return int(lib().act8_wgrad_workspace_bytes(rows, d, n))
 
@@ -499,44 +527,58 @@ def act8_wgrad_workspace_bytes(rows, d, n) -> int:
 def act8_wgrad(c, dy, row_scale=None, dw=None, workspace=None):
     """Weight gradient dw fp32 [d, n] = diag(row_scale) x^T dy from the 8-bit
     checkpoint of the layer input x [..., d] and dy bf16 [..., n]."""
-    rows, d = _rows(c[0], "q")
+    q, e = c
+    rows, d = _rows(q, "q")
     rows_dy, n = _rows(dy, "dy")
-    _need_act8(c, "checkpoint", tuple(c[0].shape))
-    _need(dy, "dy", torch.bfloat16, dy.shape)
-    _need_current(dy, "dy")
+    dev = _current(dy, "dy")
+    _need_act8(c, "checkpoint", q.shape, dev)
+    _on_device(dy, "dy", torch.bfloat16, dy.shape, dev)
     if rows != rows_dy:
         raise ValueError(f"the checkpoint has {rows} rows, dy {rows_dy}")
     if row_scale is not None:
-        _need(row_scale, "row_scale", torch.float32, (d,))
-    dw = torch.empty((d, n), dtype=torch.float32, device=dy.device) if dw is None else dw
-    _need(dw, "dw", torch.float32, (d, n))
+        _on_device(row_scale, "row_scale", torch.float32, (d,), dev)
+    if dw is None:
+        dw = torch.empty((d, n), dtype=torch.float32, device=dy.device)
+    else:
+        _on_device(dw, "dw", torch.float32, (d, n), dev)
+    size = 0
     if workspace is None:
         size = act8_wgrad_workspace_bytes(rows, d, n)
         if size:
             workspace = torch.empty((size,), dtype=torch.uint8, device=dy.device)
-    _check(lib().act8_wgrad(_ptr(c[0]), _ptr(c[1]), _ptr(dy), _ptr(row_scale), _ptr(dw),
-                            _ptr(workspace), 0 if workspace is None else workspace.numel(), rows, d,
-                            n, _stream()), "act8_wgrad")
+    else:
+        size = _workspace_size(workspace, dev)
+    _check(lib().act8_wgrad(q.data_ptr(), e.data_ptr(), dy.data_ptr(), _addr(row_scale),
+                            dw.data_ptr(), _addr(workspace), size, rows, d, n, _stream()),
+           "act8_wgrad")
     return dw
+
+
+def _workspace_size(w, dev):
+    _on_device(w, "workspace", torch.uint8, (w.numel(),), dev)
+    return w.numel()
 
 
 def swiglu_fwd(u, keep8=False, out=None):
     """h = a sigma(a) b for u = [a | b], bf16 [..., 2 f]; with keep8 returns
     (h, the 8-bit checkpoint of u)."""
     rows, f2 = _rows(u, "u")
-    _need(u, "u", torch.bfloat16, u.shape)
-    _need_current(u, "u")
+    dev = _current(u, "u")
+    _on_device(u, "u", torch.bfloat16, u.shape, dev)
     if f2 % 2:
         raise ValueError(f"u has {f2} columns, needs 2 f")
     f = f2 // 2
     if keep8 and f % 32:
         raise ValueError(f"an 8-bit checkpoint of u needs f a multiple of 32, got {f}")
-    shape = tuple(u.shape[:-1]) + (f,)
-    h = torch.empty(shape, dtype=torch.bfloat16, device=u.device) if out is None else out
-    _need(h, "out", torch.bfloat16, shape)
+    shape = u.shape[:-1] + (f,)
+    h = out
+    if h is None:
+        h = torch.empty(shape, dtype=torch.bfloat16, device=u.device)
+    else:
+        _on_device(h, "out", torch.bfloat16, shape, dev)
     c = _new_act8(u.shape, u.device) if keep8 else (None, None)
-    _check(lib().swiglu_fwd(_ptr(u), _ptr(h), _ptr(c[0]), _ptr(c[1]), rows, f, _stream()),
-           "swiglu_fwd")
+    _check(lib().swiglu_fwd(u.data_ptr(), h.data_ptr(), _addr(c[0]), _addr(c[1]), rows, f,
+                            _stream()), "swiglu_fwd")
     return (h, c) if keep8 else h
 
 
@@ -544,37 +586,38 @@ def swiglu_bwd(dh, u, with_h=False, du=None):
     """du bf16 [..., 2 f] from dh [..., f] and u, bf16 [..., 2 f] or its 8-bit
     checkpoint; with_h: (du, h), h recomputed from the same u."""
     rows, f = _rows(dh, "dh")
-    _need(dh, "dh", torch.bfloat16, dh.shape)
-    _need_current(dh, "dh")
-    shape = tuple(dh.shape[:-1]) + (2 * f,)
+    dev = _current(dh, "dh")
+    _on_device(dh, "dh", torch.bfloat16, dh.shape, dev)
+    shape = dh.shape[:-1] + (2 * f,)
+    q = e = None
     if isinstance(u, torch.Tensor):
-        _need(u, "u", torch.bfloat16, shape)
-        src = (u, None, None)
+        _on_device(u, "u", torch.bfloat16, shape, dev)
     else:
-        _need_act8(u, "u", shape)
-        src = (None, u[0], u[1])
-    du = torch.empty(shape, dtype=torch.bfloat16, device=dh.device) if du is None else du
-    _need(du, "du", torch.bfloat16, shape)
+        _need_act8(u, "u", shape, dev)
+        (q, e), u = u, None
+    if du is None:
+        du = torch.empty(shape, dtype=torch.bfloat16, device=dh.device)
+    else:
+        _on_device(du, "du", torch.bfloat16, shape, dev)
     h = torch.empty(dh.shape, dtype=torch.bfloat16, device=dh.device) if with_h else None
-    _check(lib().swiglu_bwd(_ptr(dh), _ptr(src[0]), _ptr(src[1]), _ptr(src[2]), _ptr(du), _ptr(h),
+    _check(lib().swiglu_bwd(dh.data_ptr(), _addr(u), _addr(q), _addr(e), du.data_ptr(), _addr(h),
                             rows, f, _stream()), "swiglu_bwd")
     return (du, h) if with_h else du
 
 
-def _need_stream(x, name, shape=None):
+def _need_stream(x, name, shape, dev):
+    """A tensor of the residual stream's kind: bf16 or fp32."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    _need(x, name, x.dtype, x.shape if shape is None else shape)
+    _on_device(x, name, x.dtype, shape, dev)
 
 
-def _gate_rows(gate, rows, d):
+def _gate_rows(gate, rows, d, dev):
     """G of a gate [d], [..., d] whose rows divide the stream's."""
-    if gate is None:
-        return 1
-    _need_stream(gate, "gate")
     g, dg = _rows(gate, "gate")
+    _need_stream(gate, "gate", gate.shape, dev)
     if dg != d or g < 1 or (rows and (g > rows or rows % g)):
         raise ValueError(f"gate has shape {tuple(gate.shape)}: needs d = {d} columns and a number "
                          f"of rows that divides {rows}")
@@ -590,41 +633,49 @@ def block_norm_fwd(x, y=None, gate=None, w_post=None, w_pre=None, res_scale=1.0,
     with gate_sigmoid), w_post and w_pre fp32 [d] or None.  kept is what
     block_norm_bwd takes: the row statistics with x' and y, or, with keep8,
     with their normed values in 8 bits."""
-    _need_stream(x, "x")
-    _need_current(x, "x")
     rows, d = _rows(x, "x")
-    dev, f32 = x.device, torch.float32
+    device = x.device
+    dev = _current(x, "x")
+    shape, f32, bf = x.shape, torch.float32, torch.bfloat16
+    _need_stream(x, "x", shape, dev)
+    G, out = 1, x
     if y is not None:
-        _need(y, "y", torch.bfloat16, x.shape)
-    elif gate is not None or w_post is not None:
-        raise ValueError("gate and w_post belong to a block output y")
-    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            _need(w, name, f32, (d,))
-    G = _gate_rows(gate, rows, d)
-    out = x
-    if y is not None:
-        out = torch.empty_like(x) if x_out is None else x_out
-        _need(out, "x_out", x.dtype, x.shape)
-    pre, post = w_pre is not None, w_post is not None
-    h = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if pre else None
-    rp = torch.empty(x.shape[:-1], dtype=f32, device=dev) if pre else None
-    ro = torch.empty(x.shape[:-1], dtype=f32, device=dev) if post else None
-    x8 = _new_act8(x.shape, dev) if keep8 and pre else None
-    y8 = _new_act8(x.shape, dev) if keep8 and y is not None else None
-    xq, xe = x8 if x8 is not None else (None, None)
-    yq, ye = y8 if y8 is not None else (None, None)
-    _check(lib().block_norm_fwd(_ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
-                                _ptr(out) if y is not None else None, _ptr(h), _ptr(ro), _ptr(rp),
-                                _ptr(yq), _ptr(ye), _ptr(xq), _ptr(xe), rows, d, G,
-                                int(x.dtype == f32), int(gate is not None and gate.dtype == f32),
-                                int(bool(gate_sigmoid)), float(res_scale), float(block_scale),
-                                float(eps), _stream()), "block_norm_fwd")
+        _on_device(y, "y", bf, shape, dev)
+        if gate is not None:
+            G = _gate_rows(gate, rows, d, dev)
+        if x_out is None:
+            out = torch.empty_like(x)
+        else:
+            out = x_out
+            _on_device(out, "x_out", x.dtype, shape, dev)
+    elif gate is not None or w_post is not None or x_out is not None:
+        raise ValueError("gate, w_post and x_out belong to a block output y")
+    h = rp = ro = None
+    if w_pre is not None:
+        _on_device(w_pre, "w_pre", f32, (d,), dev)
+        h = torch.empty(shape, dtype=bf, device=device)
+        rp = torch.empty(shape[:-1], dtype=f32, device=device)
+    if w_post is not None:
+        _on_device(w_post, "w_post", f32, (d,), dev)
+        ro = torch.empty(shape[:-1], dtype=f32, device=device)
+    xq = xe = yq = ye = None
     if keep8:
-        return out, h, BlockNormKept(rp, ro, None, None, x8, y8)
-    return out, h, BlockNormKept(rp, ro, out, y, None, None)
+        if w_pre is not None:
+            xq, xe = _new_act8(shape, device)
+        if y is not None:
+            yq, ye = _new_act8(shape, device)
+    _check(lib().block_norm_fwd(
+        x.data_ptr(), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre),
+        None if y is None else out.data_ptr(), _addr(h), _addr(ro), _addr(rp), _addr(yq), _addr(ye),
+        _addr(xq), _addr(xe), rows, d, G, x.dtype is f32, gate is not None and gate.dtype is f32,
+        bool(gate_sigmoid), res_scale, block_scale, eps, _stream()), "block_norm_fwd")
+    if keep8:
+        return out, h, BlockNormKept(rp, ro, None, None, None if xq is None else Act8(xq, xe),
+                                     None if yq is None else Act8(yq, ye))
+    return out, h, BlockNormKept(rp, ro, out, y)
 
 
+@functools.lru_cache(maxsize=256)
 def block_norm_bwd_workspace_bytes(N, d, G=1) -> int:
     return int(lib().block_norm_bwd_workspace_bytes(N, d, G))
 
@@ -636,60 +687,71 @@ def block_norm_bwd(dx_out, dh, kept, gate=None, w_post=None, w_pre=None, res_sca
     otherwise), dh, the gradient of h (None with w_pre None), and what the
     forward kept.  has_block: whether the forward had a y (None: whether kept
     holds y or its checkpoint)."""
-    like = dx_out if dx_out is not None else dh
+    like, name = (dx_out, "dx_out") if dx_out is not None else (dh, "dh")
     if like is None:
         raise ValueError("dx_out and dh are both None: no gradient to carry back")
-    rows, d = _rows(like, "dx_out" if dx_out is not None else "dh")
-    shape, dev, f32, bf = tuple(like.shape), like.device, torch.float32, torch.bfloat16
-    _need_current(like, "dx_out" if dx_out is not None else "dh")
-    pre, post = w_pre is not None, w_post is not None
-    block = (kept.y is not None or kept.yhat8 is not None) if has_block is None else bool(has_block)
-    if pre != (dh is not None):
+    rows, d = _rows(like, name)
+    device = like.device
+    dev = _current(like, name)
+    shape, f32, bf = like.shape, torch.float32, torch.bfloat16
+    rstd_pre, rstd_post, kx, ky, x8, y8 = kept
+    block = (ky is not None or y8 is not None) if has_block is None else bool(has_block)
+    if (w_pre is None) != (dh is None):
         raise ValueError("dh and w_pre go together")
-    if not block and (post or gate is not None):
+    if not block and (w_post is not None or gate is not None):
         raise ValueError("gate and w_post belong to a block output y")
-    stream = dx_out.dtype if dx_out is not None else kept.x.dtype if kept.x is not None else bf
+    stream = bf
     if dx_out is not None:
-        _need_stream(dx_out, "dx_out")
-    xq = xe = yq = ye = x = y = rp = ro = None
-    if pre:
-        _need(dh, "dh", bf, shape)
-        _need(w_pre, "w_pre", f32, (d,))
-        rp = kept.rstd_pre
-        _need(rp, "kept.rstd_pre", f32, shape[:-1])
-        if kept.xhat8 is not None:
-            _need_act8(kept.xhat8, "kept.xhat8", shape)
-            xq, xe = kept.xhat8
+        _need_stream(dx_out, "dx_out", shape, dev)
+        stream = dx_out.dtype
+    elif kx is not None:
+        stream = kx.dtype
+    x = y = xq = xe = yq = ye = rp = ro = dy = dgate = dwo = dwp = None
+    if w_pre is not None:
+        _on_device(dh, "dh", bf, shape, dev)
+        _on_device(w_pre, "w_pre", f32, (d,), dev)
+        rp = rstd_pre
+        _on_device(rp, "kept.rstd_pre", f32, shape[:-1], dev)
+        if x8 is not None:
+            _need_act8(x8, "kept.xhat8", shape, dev)
+            xq, xe = x8
         else:
-            x = kept.x
-            _need(x, "kept.x", stream, shape)
-    if post:
-        _need(w_post, "w_post", f32, (d,))
-        ro = kept.rstd_post
-        _need(ro, "kept.rstd_post", f32, shape[:-1])
-    if post or gate is not None:
-        if kept.yhat8 is not None:
-            _need_act8(kept.yhat8, "kept.yhat8", shape)
-            yq, ye = kept.yhat8
+            x = kx
+            _on_device(x, "kept.x", stream, shape, dev)
+        dwp = torch.empty_like(w_pre)
+    if w_post is not None:
+        _on_device(w_post, "w_post", f32, (d,), dev)
+        ro = rstd_post
+        _on_device(ro, "kept.rstd_post", f32, shape[:-1], dev)
+        dwo = torch.empty_like(w_post)
+    G = 1
+    if gate is not None:
+        G = _gate_rows(gate, rows, d, dev)
+        dgate = torch.empty_like(gate)
+    if w_post is not None or gate is not None:
+        if y8 is not None:
+            _need_act8(y8, "kept.yhat8", shape, dev)
+            yq, ye = y8
         else:
-            y = kept.y
-            _need(y, "kept.y", bf, shape)
-    G = _gate_rows(gate, rows, d)
-    dx = torch.empty(shape, dtype=stream, device=dev) if dx is None else dx
-    _need(dx, "dx", stream, shape)
-    dy = torch.empty(shape, dtype=bf, device=dev) if block else None
-    dgate = torch.empty_like(gate) if gate is not None else None
-    dwo = torch.empty_like(w_post) if post else None
-    dwp = torch.empty_like(w_pre) if pre else None
+            y = ky
+            _on_device(y, "kept.y", bf, shape, dev)
+    if dx is None:
+        dx = torch.empty(shape, dtype=stream, device=device)
+    else:
+        _on_device(dx, "dx", stream, shape, dev)
+    if block:
+        dy = torch.empty(shape, dtype=bf, device=device)
     if workspace is None:
-        workspace = torch.empty((max(16, block_norm_bwd_workspace_bytes(rows, d, G)),),
-                                dtype=torch.uint8, device=dev)
-    _check(lib().block_norm_bwd(_ptr(dx_out), _ptr(dh), _ptr(x), _ptr(y), _ptr(xq), _ptr(xe),
-                                _ptr(yq), _ptr(ye), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(ro),
-                                _ptr(rp), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dwo), _ptr(dwp),
-                                _ptr(workspace), workspace.numel(), rows, d, G, int(stream == f32),
-                                int(gate is not None and gate.dtype == f32), int(bool(gate_sigmoid)),
-                                float(res_scale), float(block_scale), _stream()), "block_norm_bwd")
+        size = max(16, block_norm_bwd_workspace_bytes(rows, d, G))
+        workspace = torch.empty((size,), dtype=torch.uint8, device=device)
+    else:
+        size = _workspace_size(workspace, dev)
+    _check(lib().block_norm_bwd(
+        _addr(dx_out), _addr(dh), _addr(x), _addr(y), _addr(xq), _addr(xe), _addr(yq), _addr(ye),
+        _addr(gate), _addr(w_post), _addr(w_pre), _addr(ro), _addr(rp), dx.data_ptr(), _addr(dy),
+        _addr(dgate), _addr(dwo), _addr(dwp), workspace.data_ptr(), size, rows, d, G, stream is f32,
+        gate is not None and gate.dtype is f32, bool(gate_sigmoid), res_scale, block_scale,
+        _stream()), "block_norm_bwd")
     return BlockNormGrads(dx, dy, dgate, dwo, dwp)
 
 

@@ -172,7 +172,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_kinds(L):
     with pytest.raises(ValueError, match="CUDA"):
         da.block_norm_fwd(x, w_pre=w)
     with pytest.raises(TypeError):
-        da.block_norm_fwd(x.half(), w_pre=w)
+        da.block_norm_fwd([1.0], w_pre=w)
     with pytest.raises(ValueError, match="CUDA"):
         da.act8_wgrad(da.Act8(torch.zeros((4, 64), dtype=torch.int8), torch.zeros((4, 2), dtype=torch.uint8)), x)
     with pytest.raises(ValueError, match="no gradient"):
