@@ -12,6 +12,7 @@
 #pragma once
 #include <cstdint>
 
+#include "exp2_poly.cuh"
 #include "sm103_ptx.cuh"
 
 namespace detattn {
@@ -88,6 +89,66 @@ __device__ __forceinline__ void act8_values8(uint2 q, float scale, float (&v)[8]
     v[4 + i] = b[i] * scale;
   }
 }
+
+// ------------------------------------------------------------ eight values as four pairs
+// The norms' arithmetic runs on f32x2 instructions: two results an issue slot.
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_all(float x) { return f2_make(x, x); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
+}
+struct Vec8 {
+  uint64_t p[4];
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2_all(x);
+  }
+  __device__ __forceinline__ void from_bf16(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = f2_make(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void from_f32(const void* at) {
+    const ulonglong2* q = static_cast<const ulonglong2*>(at);
+    const ulonglong2 a = q[0], b = q[1];
+    p[0] = a.x;
+    p[1] = a.y;
+    p[2] = b.x;
+    p[3] = b.y;
+  }
+  // The whole numbers of eight int8 bytes (the low byte of 2^23's mantissa).
+  __device__ __forceinline__ void from_int8(uint2 q) {
+    const uint32_t u[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+    const uint64_t off = f2_all(-8388736.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = f2_add(f2_make(__uint_as_float(__byte_perm(u[i >> 1], 0x4B000000u, i & 1 ? 0x7442 : 0x7440)),
+                            __uint_as_float(__byte_perm(u[i >> 1], 0x4B000000u, i & 1 ? 0x7443 : 0x7441))),
+                    off);
+  }
+  __device__ __forceinline__ uint4 to_bf16() const {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_split(p[i], lo, hi);
+      w[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void to_f32(void* at) const {
+    ulonglong2* q = static_cast<ulonglong2*>(at);
+    q[0] = make_ulonglong2(p[0], p[1]);
+    q[1] = make_ulonglong2(p[2], p[3]);
+  }
+};
 
 // ------------------------------------------------------------ eight bf16 / fp32 values
 __device__ __forceinline__ void bf16x8_to_float(uint4 x, float (&f)[8]) {

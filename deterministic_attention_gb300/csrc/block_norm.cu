@@ -228,16 +228,16 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const
 }
 
 // ------------------------------------------------------------ backward
-// One persistent block per SM.  Every row team has a ring of stages in shared
-// memory that bulk copies fill a row ahead (each tensor's row is one
-// contiguous piece), so that loads are in flight at all times while the
-// registers hold the column sums.  The exponent bytes of the checkpoints
-// (rows of d / 32 bytes, not a multiple of 16) come by plain loads a row
-// ahead.
-constexpr int kBwdWarps = 12;       // warps per block
+// One persistent block per SM: row teams and one producer warp.  Every team
+// has a ring of stages in shared memory; lane i of the producer fills team
+// i's with bulk copies, rows ahead (each tensor's row is one contiguous
+// piece), so that loads are in flight at all times while the teams' registers
+// hold the column sums.  The exponent bytes of the checkpoints (rows of d / 32
+// bytes, not a multiple of 16) come by plain loads a row ahead.
+constexpr int kBwdWarps = 11;       // warps in row teams; one more fills the rings
 constexpr int kBwdCols = 768;       // columns per warp (three vectors of eight per thread)
 constexpr int kBwdBlocks = 152;     // one block per SM of the GB300
-constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdThreads = (kBwdWarps + 1) * 32;
 constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 226 * 1024;  // dynamic shared memory at most (1 KB is left for the static part)
 
@@ -269,104 +269,183 @@ struct BwdCursor {
   }
 };
 
-// Adds the teams' column sums in team order and writes them out.
-template <int CH>
-__device__ void block_columns(const float (&acc)[CH][8], float* sums, int d, int W, int teams, int team,
-                              int t, float* out_f32, __nv_bfloat16* out_bf16) {
+// All threads of the row teams.
+__device__ __forceinline__ void teams_sync(int threads) {
+  asm volatile("bar.sync 15, %0;" ::"r"(threads) : "memory");
+}
+
+// Adds the teams' column sums in team order and hands each eight columns to
+// `out(column, sums)`.  With `wide`, through [teams][d] words of scratch;
+// without, through [d], one team after the other.
+template <int CH, class Out>
+__device__ __forceinline__ void block_columns(const Vec8 (&acc)[CH], float* scratch, bool wide, int d,
+                                              int W, int teams, int team, int t, Out out) {
+  const int n_vec = d >> 3, threads = teams * W * 32;
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int v = c * W * 32 + t;
+      if (v < n_vec) acc[c].to_f32(scratch + team * d + v * 8);
+    }
+    teams_sync(threads);
+    for (int v = team * W * 32 + t; v < n_vec; v += threads) {
+      Vec8 f;
+      f.from_f32(scratch + v * 8);
+      for (int k = 1; k < teams; ++k) {
+        Vec8 g;
+        g.from_f32(scratch + k * d + v * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = f2_add(f.p[i], g.p[i]);
+      }
+      out(v * 8, f);
+    }
+    return;
+  }
   for (int k = 0; k < teams; ++k) {
     if (team == k) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int v = c * W * 32 + t;
-        if (v < (d >> 3)) {
-          float f[8];
+        if (v < n_vec) {
+          Vec8 f = acc[c];
           if (k > 0) {
-            const uint4* p = reinterpret_cast<const uint4*>(sums + v * 8);
-            f32x8_to_float(p[0], p[1], f);
+            Vec8 before;
+            before.from_f32(scratch + v * 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += acc[c][i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = acc[c][i];
+            for (int i = 0; i < 4; ++i) f.p[i] = f2_add(before.p[i], f.p[i]);
           }
           if (k < teams - 1)
-            store8<true>(sums, v * 8, f);
-          else if (out_f32)
-            store8<true>(out_f32, v * 8, f);
+            f.to_f32(scratch + v * 8);
           else
-            store8<false>(out_bf16, v * 8, f);
+            out(v * 8, f);
         }
       }
     }
-    if (k < teams - 1) __syncthreads();
+    if (k < teams - 1) teams_sync(threads);
   }
 }
 
-template <int CH, bool MULTI, bool F32, bool FROM8>
+// Eight gate values as pairs, and their slopes by the stored value.
+__device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at, Vec8& g, Vec8& slope) {
+  if (a.gate_fp32)
+    g.from_f32(static_cast<const float*>(a.gate) + at);
+  else
+    g.from_bf16(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.gate) + at));
+  slope.fill(1.0f);
+  if (a.gate_sigmoid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      f2_split(g.p[i], x, y);
+      x = __fdividef(1.0f, 1.0f + __expf(-x));
+      y = __fdividef(1.0f, 1.0f + __expf(-y));
+      g.p[i] = f2_make(x, y);
+      slope.p[i] = f2_make(x * (1.0f - x), y * (1.0f - y));
+    }
+  }
+}
+
+// FULL: every input is there and no gate of its own for every row (the flags
+// below are then known to the compiler).
+template <int CH, bool MULTI, bool F32, bool FROM8, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float words[64];
-  __shared__ __align__(8) uint64_t bars[kBwdWarps * kBwdMaxStages];
-  __shared__ BwdCursor cursors[kBwdWarps];
-  __shared__ int issued[kBwdWarps];
+  __shared__ __align__(8) uint64_t bars[2 * kBwdWarps * kBwdMaxStages];  // full, empty
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = MULTI ? (a.d + kBwdCols - 1) / kBwdCols : 1;
-  const int teams = ring.teams;
-  const int team = warp / W, wt = warp - team * W;
-  const int t = wt * 32 + lane;
+  const int teams = ring.teams, team_threads = teams * W * 32;
   const int n_vec = a.d >> 3;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  const bool pre = a.dh != nullptr;
-  const bool per_row_gate = a.gate != nullptr && a.rows_per_gate == 1;
+  const bool pre = FULL || a.dh != nullptr;
+  const bool with_dx = FULL || a.dx_out != nullptr;
+  const bool post = FULL || a.w_post != nullptr;
+  const bool per_row_gate = !FULL && a.gate != nullptr && a.rows_per_gate == 1;
   const bool sum_gate = a.gate != nullptr && !per_row_gate;
-  const bool need_y = a.dy != nullptr && (a.w_post != nullptr || a.gate != nullptr);
+  const bool with_dy = FULL || a.dy != nullptr;
+  const bool need_y = FULL || (with_dy && (post || a.gate != nullptr));
   constexpr int kX = F32 ? 4 : 2;
-  float* sums = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);
+  float* cols = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);  // [d]
+  auto full = [&](int team, int s) { return smem_u32(&bars[team * kBwdMaxStages + s]); };
+  auto empty = [&](int team, int s) {
+    return smem_u32(&bars[(kBwdWarps + team) * kBwdMaxStages + s]);
+  };
+  if (threadIdx.x < teams) {
+    for (int s = 0; s < ring.stages; ++s) {
+      mbar_init(full(threadIdx.x, s), 1);
+      mbar_init(empty(threadIdx.x, s), W);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+
+  if (warp == teams * W) {
+    // The producer.
+    const uint32_t row_tx = (pre ? 2u * a.d : 0u) + (with_dx ? kX * a.d : 0u) +
+                            (pre ? (FROM8 ? 1u : kX) * a.d : 0u) + (need_y ? (FROM8 ? 1u : 2u) * a.d : 0u);
+    const int team = lane;
+    bool live = team < teams, gave_up = false;
+    BwdCursor cur{};
+    cur.item = blockIdx.x;
+    if (live) {
+      cur.open(a, team);
+      live = cur.settle(a, team);
+    }
+    int n = 0, s = 0;
+    uint32_t parity = 1;
+    uint64_t since = globaltimer_ns();
+    while (__any_sync(0xFFFFFFFFu, live)) {
+      bool idle = true;
+      if (live) {
+        if (n < ring.stages || mbar_test_wait(empty(team, s), parity)) {
+          idle = false;
+          const size_t at = static_cast<size_t>(cur.row) * a.d;
+          const uint32_t dst = smem_u32(smem) + (team * ring.stages + s) * ring.bytes, bar = full(team, s);
+          mbar_arrive_expect_tx(bar, row_tx);
+          if (pre) {
+            bulk_load(dst, static_cast<const uint8_t*>(a.dh) + at * 2, 2 * a.d, bar);
+            if constexpr (FROM8)
+              bulk_load(dst + ring.off_x, a.xhat_q + at, a.d, bar);
+            else
+              bulk_load(dst + ring.off_x, static_cast<const uint8_t*>(a.x) + at * kX, kX * a.d, bar);
+          }
+          if (with_dx)
+            bulk_load(dst + ring.off_d, static_cast<const uint8_t*>(a.dx_out) + at * kX, kX * a.d, bar);
+          if (need_y) {
+            if constexpr (FROM8)
+              bulk_load(dst + ring.off_y, a.yhat_q + at, a.d, bar);
+            else
+              bulk_load(dst + ring.off_y, static_cast<const uint8_t*>(a.y) + at * 2, 2 * a.d, bar);
+          }
+          ++n;
+          if (++s == ring.stages) {
+            s = 0;
+            parity ^= 1u;
+          }
+          cur.row += teams;
+          live = cur.settle(a, team);
+          since = globaltimer_ns();
+        } else if (globaltimer_ns() - since > a.wait_ns) {
+          live = false;
+          gave_up = true;
+        }
+      }
+      if (__all_sync(0xFFFFFFFFu, idle)) __nanosleep(40);
+    }
+    // The copies in flight, before the block can end.
+    for (int k = n > ring.stages ? n - ring.stages : 0; k < n; ++k)
+      if (!mbar_wait(full(team, k % ring.stages), (k / ring.stages) & 1, a.wait_ns)) gave_up = true;
+    if (gave_up) set_norm_status();
+    return;
+  }
+
+  const int team = warp / W, wt = warp - team * W;
+  const int t = wt * 32 + lane;
   uint8_t* mine = smem + team * ring.stages * ring.bytes;
-  const uint32_t bar0 = smem_u32(&bars[team * kBwdMaxStages]);
   int slot = 0;
   bool ok = true;
-
-  if (t == 0)
-    for (int s = 0; s < ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
-  if (t == 0) fence_barrier_init();
-  __syncthreads();
-
-  const uint32_t row_tx = (pre ? 2u * a.d : 0u) + (a.dx_out ? kX * a.d : 0u) +
-                          (pre ? (FROM8 ? 1u : kX) * a.d : 0u) + (need_y ? (FROM8 ? 1u : 2u) * a.d : 0u);
-  auto issue = [&](int row, int s) {
-    const size_t at = static_cast<size_t>(row) * a.d;
-    const uint32_t dst = smem_u32(mine + s * ring.bytes), bar = bar0 + 8 * s;
-    mbar_arrive_expect_tx(bar, row_tx);
-    if (pre) {
-      bulk_load(dst, static_cast<const uint8_t*>(a.dh) + at * 2, 2 * a.d, bar);
-      if constexpr (FROM8)
-        bulk_load(dst + ring.off_x, a.xhat_q + at, a.d, bar);
-      else
-        bulk_load(dst + ring.off_x, static_cast<const uint8_t*>(a.x) + at * kX, kX * a.d, bar);
-    }
-    if (a.dx_out)
-      bulk_load(dst + ring.off_d, static_cast<const uint8_t*>(a.dx_out) + at * kX, kX * a.d, bar);
-    if (need_y) {
-      if constexpr (FROM8)
-        bulk_load(dst + ring.off_y, a.yhat_q + at, a.d, bar);
-      else
-        bulk_load(dst + ring.off_y, static_cast<const uint8_t*>(a.y) + at * 2, 2 * a.d, bar);
-    }
-  };
-
-  // The team's first thread issues the copies; its cursor, which runs
-  // ring.stages rows ahead, lives in shared memory (the other threads need
-  // no registers for it).
-  BwdCursor* ahead = &cursors[team];
-  if (t == 0) {
-    int n = 0;
-    ahead->item = blockIdx.x;
-    ahead->open(a, team);
-    for (; n < ring.stages && ahead->settle(a, team); ++n, ahead->row += teams) issue(ahead->row, n);
-    issued[team] = n;
-  }
   // What plain loads bring, one row ahead.
   struct Small {
     float rx, ry;
@@ -375,7 +454,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto load_small = [&](int row) {
     Small m;
     m.rx = pre ? a.rstd_pre[row] : 0.0f;
-    m.ry = a.w_post ? a.rstd_post[row] : 1.0f;
+    m.ry = post ? a.rstd_post[row] : 1.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       m.e[c] = 0u;
@@ -391,17 +470,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return m;
   };
 
-  float acc_pre[CH][8], acc_post[CH][8], acc_gate[CH][8];
+  // Column sums of this thread: of dh xhat over all rows, and of D yhat (the
+  // gate left out where a whole item shares it) over the item's rows.  From
+  // the second follow both dgate and dw_post: what multiplies a column is
+  // applied where the item is written out.
+  Vec8 acc_pre[CH], acc_y[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc_pre[c][i] = acc_post[c][i] = acc_gate[c][i] = 0.0f;
+  for (int c = 0; c < CH; ++c) {
+    acc_pre[c].fill(0.0f);
+    acc_y[c].fill(0.0f);
+  }
 
   int s = 0;           // this row's stage
   uint32_t phase = 0;  // and the parity of its barrier
   BwdCursor cur;
   for (cur.item = blockIdx.x; cur.item < a.items; cur.item += gridDim.x) {
     cur.open(a, team);
+    const int group = cur.item / a.slices;
+    const size_t group_gate = static_cast<size_t>(group) * a.d;
+    if (need_y) {
+      // What multiplies a column on the way to y: the norm's weight times the
+      // gate that the item's rows share.  (The same words hold the teams'
+      // sums when an item that is not the block's last is written out.)
+      teams_sync(team_threads);
+      for (int v = threadIdx.x; v < n_vec; v += team_threads) {
+        Vec8 w, g, slope;
+        w.fill(1.0f);
+        if (post) w.from_f32(a.w_post + v * 8);
+        if (sum_gate) {
+          gate_pairs(a, group_gate + v * 8, g, slope);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w.p[i] = f2_mul(w.p[i], g.p[i]);
+        }
+        w.to_f32(cols + v * 8);
+      }
+      teams_sync(team_threads);
+    }
     Small next{};
     if (cur.row < cur.end) next = load_small(cur.row);
     for (; cur.row < cur.end; cur.row += teams) {
@@ -410,183 +514,196 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint8_t* st = mine + s * ring.bytes;
       const Small m = next;
       if (row + teams < cur.end) next = load_small(row + teams);
-      if (ok) ok = mbar_wait(bar0 + 8 * s, phase, a.wait_ns);
-      auto hat_x = [&](int c, int v, float (&f)[8]) {
-        if constexpr (FROM8) {
-          act8_values8(*reinterpret_cast<const uint2*>(st + ring.off_x + v * 8), act8_scale(m.e[c] & 255u), f);
-        } else {
-          Raw8<F32> r;
-          r.load(st + ring.off_x, v * 8);
-          r.get(f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= m.rx;
-        }
+      if (ok) ok = mbar_wait(full(team, s), phase, a.wait_ns);
+      // xhat = scale_x raw_x, yhat = scale_y raw_y: the row's 1 / rms and the
+      // stored number, or the group's power of two and the checkpoint's.
+      auto raw_x = [&](int v, Vec8& f) {
+        if constexpr (FROM8)
+          f.from_int8(*reinterpret_cast<const uint2*>(st + ring.off_x + v * 8));
+        else if constexpr (F32)
+          f.from_f32(st + ring.off_x + v * 32);
+        else
+          f.from_bf16(*reinterpret_cast<const uint4*>(st + ring.off_x + v * 16));
       };
-      auto hat_y = [&](int c, int v, float (&f)[8]) {
-        if constexpr (FROM8) {
-          act8_values8(*reinterpret_cast<const uint2*>(st + ring.off_y + v * 8), act8_scale(m.e[c] >> 8), f);
-        } else {
-          Raw8<false> r;
-          r.load(st + ring.off_y, v * 8);
-          r.get(f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= m.ry;
-        }
+      auto raw_y = [&](int v, Vec8& f) {
+        if constexpr (FROM8)
+          f.from_int8(*reinterpret_cast<const uint2*>(st + ring.off_y + v * 8));
+        else
+          f.from_bf16(*reinterpret_cast<const uint4*>(st + ring.off_y + v * 16));
       };
+      auto scale_x = [&](int c) { return FROM8 ? act8_scale(m.e[c] & 255u) : m.rx; };
+      auto scale_y = [&](int c) { return FROM8 ? act8_scale(m.e[c] >> 8) : m.ry; };
+      Vec8 keep[CH];  // dh w_pre, then D g w_post
       float s1 = 0.0f;
       if (pre) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int v = c * W * 32 + t;
           if (v < n_vec) {
-            float dh[8], xh[8], w[8];
-            bf16x8_to_float(*reinterpret_cast<const uint4*>(st + v * 16), dh);
-            hat_x(c, v, xh);
-            load_f32x8(a.w_pre + v * 8, w);
+            Vec8 dh, x, w;
+            dh.from_bf16(*reinterpret_cast<const uint4*>(st + v * 16));
+            raw_x(v, x);
+            w.from_f32(a.w_pre + v * 8);
+            const uint64_t sc = f2_all(scale_x(c));
+            uint64_t part = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float p = dh[i] * xh[i];
-              acc_pre[c][i] += p;
-              s1 = fmaf(p, w[i], s1);
+            for (int i = 0; i < 4; ++i) {
+              keep[c].p[i] = f2_mul(dh.p[i], w.p[i]);
+              acc_pre[c].p[i] = f2_fma(f2_mul(dh.p[i], x.p[i]), sc, acc_pre[c].p[i]);
+              part = f2_fma(keep[c].p[i], x.p[i], part);
             }
+            s1 = fmaf(f2_sum(part), scale_x(c), s1);
           }
         }
         s1 = team_sum<MULTI>(s1, words, W, team, wt, lane, slot) * inv_d;
       }
       float s2 = 0.0f;
-      float dz[CH][8];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int v = c * W * 32 + t;
         if (v < n_vec) {
           const size_t at = base + v * 8;
-          if (a.dx_out) {
-            Raw8<F32> r;
-            r.load(st + ring.off_d, v * 8);
-            r.get(dz[c]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dz[c][i] = 0.0f;
-          }
+          Vec8 D;
+          if (!with_dx)
+            D.fill(0.0f);
+          else if constexpr (F32)
+            D.from_f32(st + ring.off_d + v * 32);
+          else
+            D.from_bf16(*reinterpret_cast<const uint4*>(st + ring.off_d + v * 16));
           if (pre) {
-            float dh[8], xh[8], w[8];
-            bf16x8_to_float(*reinterpret_cast<const uint4*>(st + v * 16), dh);
-            hat_x(c, v, xh);
-            load_f32x8(a.w_pre + v * 8, w);
+            Vec8 x;
+            raw_x(v, x);
+            const uint64_t rx = f2_all(m.rx), k = f2_all(-m.rx * s1 * scale_x(c));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dz[c][i] = fmaf(m.rx, fmaf(dh[i], w[i], -xh[i] * s1), dz[c][i]);
+            for (int i = 0; i < 4; ++i) D.p[i] = f2_fma(keep[c].p[i], rx, f2_fma(x.p[i], k, D.p[i]));
           }
-          float o[8];
+          Vec8 o;
+          const uint64_t r = f2_all(a.res_scale);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = a.res_scale * dz[c][i];
-          store8<F32>(a.dx, at, o);
-          if (a.dy) {
-            float yh[8], w[8];
-            if (need_y) hat_y(c, v, yh);
+          for (int i = 0; i < 4; ++i) o.p[i] = f2_mul(r, D.p[i]);
+          if constexpr (F32)
+            o.to_f32(static_cast<float*>(a.dx) + at);
+          else
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dx) + at) = o.to_bf16();
+          if (need_y) {
+            Vec8 y, e, gw;
+            raw_y(v, y);
+            gw.from_f32(cols + v * 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dz[c][i] *= a.block_scale;
-              w[i] = 1.0f;
-            }
-            if (a.w_post) load_f32x8(a.w_post + v * 8, w);
-            if (a.gate) {
-              float g[8], slope[8];
-              load_gate8(a.gate, static_cast<size_t>(row / a.rows_per_gate) * a.d + v * 8, a.gate_fp32,
-                         a.gate_sigmoid, g, slope);
+            for (int i = 0; i < 4; ++i) e.p[i] = f2_mul(D.p[i], y.p[i]);
+            if (per_row_gate) {
+              Vec8 g, slope;
+              gate_pairs(a, at, g, slope);
+              const uint64_t k = f2_all(a.block_scale * scale_y(c));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float dg = dz[c][i] * (yh[i] * w[i]) * slope[i];
-                dz[c][i] *= g[i];
-                acc_gate[c][i] += dg;
-                slope[i] = dg;
+              for (int i = 0; i < 4; ++i) {
+                slope.p[i] = f2_mul(f2_mul(slope.p[i], gw.p[i]), f2_mul(e.p[i], k));
+                e.p[i] = f2_mul(e.p[i], g.p[i]);
+                gw.p[i] = f2_mul(gw.p[i], g.p[i]);
               }
-              if (per_row_gate) {
-                if (a.gate_fp32)
-                  store8<true>(a.dgate, at, slope);
-                else
-                  store8<false>(a.dgate, at, slope);
-              }
+              if (a.gate_fp32)
+                slope.to_f32(static_cast<float*>(a.dgate) + at);
+              else
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dgate) + at) = slope.to_bf16();
             }
-            if (a.w_post) {
+            const uint64_t sc = f2_all(scale_y(c));
+            uint64_t part = 0;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float p = dz[c][i] * yh[i];
-                acc_post[c][i] += p;
-                s2 = fmaf(p, w[i], s2);
-                dz[c][i] *= w[i];
-              }
+            for (int i = 0; i < 4; ++i) {
+              acc_y[c].p[i] = f2_fma(e.p[i], sc, acc_y[c].p[i]);
+              keep[c].p[i] = f2_mul(D.p[i], gw.p[i]);
+              part = f2_fma(keep[c].p[i], y.p[i], part);
             }
+            s2 = fmaf(f2_sum(part), scale_y(c), s2);
+          } else {
+            keep[c] = D;
           }
         }
       }
-      if (a.dy) {
-        if (a.w_post) s2 = team_sum<MULTI>(s2, words, W, team, wt, lane, slot) * inv_d;
+      if (with_dy) {
+        float k2 = 0.0f;
+        if (post) k2 = -m.ry * a.block_scale * (team_sum<MULTI>(s2, words, W, team, wt, lane, slot) * inv_d);
+        const uint64_t k1 = f2_all((post ? m.ry : 1.0f) * a.block_scale);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int v = c * W * 32 + t;
           if (v < n_vec) {
-            if (a.w_post) {
-              float yh[8];
-              hat_y(c, v, yh);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dz[c][i] = m.ry * fmaf(-yh[i], s2, dz[c][i]);
+            for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_mul(keep[c].p[i], k1);
+            if (post) {
+              Vec8 y;
+              raw_y(v, y);
+              const uint64_t k = f2_all(k2 * scale_y(c));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_fma(y.p[i], k, keep[c].p[i]);
             }
-            store8<false>(a.dy, base + v * 8, dz[c]);
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dy) + base + v * 8) = keep[c].to_bf16();
           }
         }
       }
-      // The whole team is past this stage: refill it.
-      if constexpr (MULTI)
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory");
-      else
-        __syncwarp();
-      if (t == 0 && ok && ahead->settle(a, team)) {
-        issue(ahead->row, s);
-        ahead->row += teams;
-        ++issued[team];
-      }
+      // This warp is past the stage.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(team, s));
       if (++s == ring.stages) {
         s = 0;
         phase ^= 1u;
       }
     }
-    if (sum_gate) {
-      // This item's share of its gate row, or all of it.
-      const int group = cur.item / a.slices;
-      float* f32 = a.part_gate ? a.part_gate + static_cast<size_t>(cur.item) * a.d
-                   : a.gate_fp32 ? static_cast<float*>(a.dgate) + static_cast<size_t>(group) * a.d
-                                 : nullptr;
-      __syncthreads();  // the sums of the item before have been read
-      block_columns<CH>(acc_gate, sums, a.d, W, teams, team, t, f32,
-                        f32 ? nullptr : static_cast<__nv_bfloat16*>(a.dgate) + static_cast<size_t>(group) * a.d);
+    if (post || sum_gate) {
+      // This item's sums: its share of dgate (all of it without a part), and
+      // of dw_post, which the block adds up over its items.
+      // After the last item the ring is free.
+      const bool last = cur.item + static_cast<int>(gridDim.x) >= a.items;
+      teams_sync(team_threads);
+      float* post_sums = a.part_post + static_cast<size_t>(blockIdx.x) * a.d;
+      const bool first = cur.item == blockIdx.x;
+      block_columns<CH>(acc_y, last ? reinterpret_cast<float*>(smem) : cols, last, a.d, W, teams, team, t, [&](int col, Vec8& f) {
+        const uint64_t k = f2_all(a.block_scale);
+        Vec8 g, slope;
+        g.fill(1.0f);
+        if (sum_gate) {
+          gate_pairs(a, group_gate + col, g, slope);
+          Vec8 w;
+          if (post)
+            w.from_f32(a.w_post + col);
+          else
+            w.fill(1.0f);
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+          for (int i = 0; i < 4; ++i) slope.p[i] = f2_mul(f2_mul(slope.p[i], w.p[i]), f2_mul(f.p[i], k));
+          if (a.part_gate)
+            slope.to_f32(a.part_gate + static_cast<size_t>(cur.item) * a.d + col);
+          else if (a.gate_fp32)
+            slope.to_f32(static_cast<float*>(a.dgate) + group_gate + col);
+          else
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dgate) + group_gate + col) = slope.to_bf16();
+        }
+        if (post) {
+          Vec8 sum;
+          if (first)
+            sum.fill(0.0f);
+          else
+            sum.from_f32(post_sums + col);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc_gate[c][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) sum.p[i] = f2_fma(f2_mul(f.p[i], k), g.p[i], sum.p[i]);
+          sum.to_f32(post_sums + col);
+        }
+      });
+#pragma unroll
+      for (int c = 0; c < CH; ++c) acc_y[c].fill(0.0f);
     }
   }
   if (pre) {
-    __syncthreads();
-    block_columns<CH>(acc_pre, sums, a.d, W, teams, team, t,
-                      a.part_pre + static_cast<size_t>(blockIdx.x) * a.d, nullptr);
+    teams_sync(team_threads);
+    float* out = a.part_pre + static_cast<size_t>(blockIdx.x) * a.d;
+    block_columns<CH>(acc_pre, reinterpret_cast<float*>(smem), true, a.d, W, teams, team, t,
+                      [&](int col, Vec8& f) { f.to_f32(out + col); });
   }
-  if (a.w_post) {
-    __syncthreads();
-    block_columns<CH>(acc_post, sums, a.d, W, teams, team, t,
-                      a.part_post + static_cast<size_t>(blockIdx.x) * a.d, nullptr);
-  }
-  if (!ok) {
-    // A wait ran out: the copies in flight, before the block ends.
-    if (t == 0)
-      for (int n = issued[team], k = n > ring.stages ? n - ring.stages : 0; k < n; ++k)
-        mbar_wait(bar0 + 8 * (k % ring.stages), (k / ring.stages) & 1, a.wait_ns);
-    set_norm_status();
-  }
+  if (!ok) set_norm_status();
 }
 
 // Adds the parts of a column sum in ascending order: 32 columns per block,
-// eight runs of parts each, then the runs in order.
+// sixteen runs of parts each, then the runs in order.
+constexpr int kSumRuns = 16;
 struct SumJob {
   const float* parts;  // [n][d]
   void* out;           // [d]
@@ -598,8 +715,8 @@ struct SumJobs {
   int n_pre, n_post;       // 1 or 0
   int d;
 };
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumJobs j) {
-  __shared__ float run[8][32];
+__global__ void __launch_bounds__(kSumRuns * 32) sum_parts_kernel(const SumJobs j) {
+  __shared__ float run[kSumRuns][32];
   const int z = blockIdx.y;
   SumJob s;
   size_t at = 0;
@@ -613,8 +730,9 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const SumJobs j) {
   }
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + tx;
+  griddep_wait();
   const float* p = s.parts + at * s.n * j.d + col;
-  const int per = (s.n + 7) / 8, lo = min(ty * per, s.n), hi = min(lo + per, s.n);
+  const int per = (s.n + kSumRuns - 1) / kSumRuns, lo = min(ty * per, s.n), hi = min(lo + per, s.n);
   float acc = 0.0f;
   if (col < j.d) {
 #pragma unroll 8
@@ -623,7 +741,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const SumJobs j) {
   run[ty][tx] = acc;
   __syncthreads();
   if (ty == 0 && col < j.d) {
-    for (int k = 1; k < 8; ++k) acc += run[k][tx];
+    for (int k = 1; k < kSumRuns; ++k) acc += run[k][tx];
     if (s.out_fp32)
       static_cast<float*>(s.out)[at * j.d + col] = acc;
     else
@@ -650,10 +768,10 @@ cudaError_t fwd_of(const BlockNormFwdArgs& a, bool f32, int W, cudaStream_t st) 
   return cudaGetLastError();
 }
 
-template <int CH, bool MULTI, bool F32, bool FROM8>
-cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
+template <int CH, bool MULTI, bool F32, bool FROM8, bool FULL>
+cudaError_t bwd_full(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   static unsigned long long attr_ctx[64] = {};
-  auto kernel = block_norm_bwd_kernel<CH, MULTI, F32, FROM8>;
+  auto kernel = block_norm_bwd_kernel<CH, MULTI, F32, FROM8, FULL>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -672,14 +790,21 @@ cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   r.off_y = r.off_x + (pre ? (FROM8 ? 1 : x_bytes) * a.d : 0);
   r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
   r.teams = kBwdWarps / W;
-  auto sums = [&](int teams) { return teams > 1 ? 4 * a.d : 0; };
-  while (r.teams > 1 && r.teams * 2 * r.bytes + sums(r.teams) > kBwdSmem) --r.teams;
+  while (r.teams > 1 && r.teams * 2 * r.bytes + 4 * a.d > kBwdSmem) --r.teams;
   r.stages = 2;
-  while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + sums(r.teams) <= kBwdSmem)
+  while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + 4 * a.d <= kBwdSmem)
     ++r.stages;
-  const int smem = r.teams * r.stages * r.bytes + sums(r.teams);
-  kernel<<<a.blocks, r.teams * W * 32, smem, st>>>(a, r);
+  const int smem = r.teams * r.stages * r.bytes + 4 * a.d;
+  kernel<<<a.blocks, (r.teams * W + 1) * 32, smem, st>>>(a, r);
   return cudaGetLastError();
+}
+
+template <int CH, bool MULTI, bool F32, bool FROM8>
+cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
+  const bool full = a.dh != nullptr && a.dx_out != nullptr && a.dy != nullptr && a.w_post != nullptr &&
+                    (a.gate == nullptr || a.rows_per_gate > 1);
+  return full ? bwd_full<CH, MULTI, F32, FROM8, true>(a, W, st)
+              : bwd_full<CH, MULTI, F32, FROM8, false>(a, W, st);
 }
 
 template <int CH, bool MULTI>
@@ -747,8 +872,18 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool x_fp32, cudaSt
   j.gate = {a.part_gate, a.dgate, a.slices, a.gate_fp32};
   const int rows = j.n_pre + j.n_post + (a.part_gate ? a.items / a.slices : 0);
   if (rows == 0) return cudaSuccess;
-  sum_parts_kernel<<<dim3((a.d + 31) / 32, rows), 256, 0, st>>>(j);
-  return cudaGetLastError();
+  // A programmatic dependent: launched while the rows are at work, it waits
+  // for them before it reads.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.d + 31) / 32, rows);
+  cfg.blockDim = kSumRuns * 32;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_parts_kernel, j);
 }
 
 cudaError_t take_norm_status(cudaStream_t st, unsigned* out) {
