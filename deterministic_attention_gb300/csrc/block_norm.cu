@@ -234,10 +234,11 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const
 // piece), so that loads are in flight at all times while the teams' registers
 // hold the column sums.  The exponent bytes of the checkpoints (rows of d / 32
 // bytes, not a multiple of 16) come by plain loads a row ahead.
-constexpr int kBwdWarps = 11;       // warps in row teams; one more fills the rings
-constexpr int kBwdCols = 768;       // columns per warp (three vectors of eight per thread)
+// Warps in row teams (one more fills the rings) by the vectors of eight
+// columns that a thread holds: with three, 11 warps' registers fit; with two, 15.
+constexpr int bwd_warps(int ch, bool multi) { return multi && ch == 2 ? 15 : 11; }
+constexpr int kBwdMaxTeams = 11;
 constexpr int kBwdBlocks = 152;     // one block per SM of the GB300
-constexpr int kBwdThreads = (kBwdWarps + 1) * 32;
 constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 226 * 1024;  // dynamic shared memory at most (1 KB is left for the static part)
 
@@ -245,6 +246,7 @@ constexpr int kBwdSmem = 226 * 1024;  // dynamic shared memory at most (1 KB is 
 struct BwdRing {
   int off_d, off_x, off_y, bytes;  // dh at 0
   int teams, stages;
+  int W;             // warps per team
 };
 
 // This team's rows, in order: rows team, team + teams, ... of each item.
@@ -348,13 +350,13 @@ __device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at,
 // FULL: every input is there and no gate of its own for every row (the flags
 // below are then known to the compiler).
 template <int CH, bool MULTI, bool F32, bool FROM8, bool FULL>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__((bwd_warps(CH, MULTI) + 1) * 32, 1)
     block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float words[64];
-  __shared__ __align__(8) uint64_t bars[2 * kBwdWarps * kBwdMaxStages];  // full, empty
+  __shared__ __align__(8) uint64_t bars[2 * kBwdMaxTeams * kBwdMaxStages];  // full, empty
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = MULTI ? (a.d + kBwdCols - 1) / kBwdCols : 1;
+  const int W = MULTI ? ring.W : 1;
   const int teams = ring.teams, team_threads = teams * W * 32;
   const int n_vec = a.d >> 3;
   const float inv_d = 1.0f / static_cast<float>(a.d);
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* cols = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);  // [d]
   auto full = [&](int team, int s) { return smem_u32(&bars[team * kBwdMaxStages + s]); };
   auto empty = [&](int team, int s) {
-    return smem_u32(&bars[(kBwdWarps + team) * kBwdMaxStages + s]);
+    return smem_u32(&bars[(kBwdMaxTeams + team) * kBwdMaxStages + s]);
   };
   if (threadIdx.x < teams) {
     for (int s = 0; s < ring.stages; ++s) {
@@ -789,7 +791,8 @@ cudaError_t bwd_full(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   r.off_x = r.off_d + (a.dx_out ? x_bytes * a.d : 0);
   r.off_y = r.off_x + (pre ? (FROM8 ? 1 : x_bytes) * a.d : 0);
   r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
-  r.teams = kBwdWarps / W;
+  r.W = W;
+  r.teams = bwd_warps(CH, MULTI) / W;
   while (r.teams > 1 && r.teams * 2 * r.bytes + 4 * a.d > kBwdSmem) --r.teams;
   r.stages = 2;
   while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + 4 * a.d <= kBwdSmem)
@@ -830,9 +833,29 @@ cudaError_t launch_block_norm_fwd(const BlockNormFwdArgs& a, bool x_fp32, cudaSt
   return fwd_of<4, true>(a, x_fp32, W, st);
 }
 
+namespace {
+
+// Warps per row and vectors per thread.  Up to 768 columns a row is one
+// warp's; beyond, two vectors per thread keep more warps at work than three
+// where their teams fill the block as well (32768 x 1536: five teams of three
+// against five of two).
+struct BwdShape {
+  int W, ch;
+};
+BwdShape bwd_shape(int d) {
+  if (d <= 768) return {1, (d + 255) / 256};
+  const int w3 = (d + 767) / 768, w2 = (d + 511) / 512;
+  if (w2 <= bwd_warps(2, true) && bwd_warps(2, true) / w2 * w2 > bwd_warps(3, true) / w3 * w3)
+    return {w2, 2};
+  return {w3, 3};
+}
+
+}  // namespace
+
 BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
   BlockNormBwdPlan p{};
-  const int W = (d + kBwdCols - 1) / kBwdCols, teams = kBwdWarps / W;
+  const BwdShape sh = bwd_shape(d);
+  const int teams = bwd_warps(sh.ch, sh.W > 1) / sh.W;
   const bool shared = G > 1 && G < N;
   if (!shared) {
     const int want = (N + teams - 1) / teams;
@@ -854,14 +877,14 @@ BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool x_fp32, cudaStream_t st) {
-  const int W = (a.d + kBwdCols - 1) / kBwdCols, ch = (a.d + 256 * W - 1) / (256 * W);
+  const auto [W, ch] = bwd_shape(a.d);
   cudaError_t e;
   if (W == 1)
     e = ch == 1   ? bwd_of<1, false>(a, x_fp32, W, st)
         : ch == 2 ? bwd_of<2, false>(a, x_fp32, W, st)
                   : bwd_of<3, false>(a, x_fp32, W, st);
   else
-    e = ch <= 2 ? bwd_of<2, true>(a, x_fp32, W, st) : bwd_of<3, true>(a, x_fp32, W, st);
+    e = ch == 2 ? bwd_of<2, true>(a, x_fp32, W, st) : bwd_of<3, true>(a, x_fp32, W, st);
   if (e != cudaSuccess) return e;
   SumJobs j{};
   j.d = a.d;

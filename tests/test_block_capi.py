@@ -154,7 +154,7 @@ def test_block_norm_bwd_valid_forms(L):
 
 def test_block_norm_workspace(L):
     up = lambda x: (x + 255) // 256 * 256
-    # 4096 rows of 768 columns: twelve rows at a time in each of 152 blocks.
+    # 4096 rows of 768 columns: eleven rows at a time in each of 152 blocks.
     assert L.block_norm_bwd_workspace_bytes(4096, 768, 1) == 3 * up(152 * 768 * 4)
     assert L.block_norm_bwd_workspace_bytes(0, 768, 1) == 0
     assert L.block_norm_bwd_workspace_bytes(8, 768, 3) == 0
