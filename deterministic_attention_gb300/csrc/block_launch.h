@@ -93,22 +93,28 @@ cudaError_t launch_swiglu_bwd(const void* dh, const void* u, const int8_t* q, co
                               void* du, void* h, long rows, int f, cudaStream_t st);
 
 // ------------------------------------------------------------ weight gradient from a checkpoint
-constexpr int kWgradBM = 128;   // columns of the checkpoint (rows of dw) per tile
-constexpr int kWgradBN = 256;   // columns of dy per tile
-constexpr int kWgradBK = 64;    // tokens per step
-// Persistent blocks, one per SM of the GB300.  A constant, so that the deal
-// of the work, and with it every bit, follows from the shape alone (no block
-// waits for another, so any SM count is correct).
-constexpr int kWgradBlocks = 152;
+// A pair of blocks works on a tile of 256 columns of the checkpoint (rows of
+// dw, half of them each) by 256 columns of dy, 64 tokens a step.
+constexpr int kWgradBM = 256;
+constexpr int kWgradBN = 256;
+constexpr int kWgradBK = 64;
+// Steps that one accumulator takes before it is added to the tile's sum in
+// fp32 registers: the tensor core's own additions lose about 6e-7 of a sum of
+// 1024 tokens, and in proportion to their number.
+constexpr int kWgradChunk = 16;
+// Persistent pairs, one block per SM of the GB300.  A constant, so that the
+// deal of the work, and with it every bit, follows from the shape alone (no
+// pair waits for another, so any SM count is correct).
+constexpr int kWgradPairs = 76;
 
 struct Act8WgradArgs {
   const uint8_t* e;       // [rows, d / 32]
   const float* row_scale; // [d] or null
   float* dw;              // [d, n]
-  float* partial;         // [rem_tiles * splits][128][256]
+  float* partial;         // [tiles that are cut * splits][256][256]
   int rows, d, n;
   int tiles_m, tiles_n;
-  int whole_tiles;        // tiles computed by one block each
+  int whole_tiles;        // tiles computed by one pair each
   int splits;             // row ranges of each of the other tiles (1: none split)
   unsigned long long wait_ns;
 };
@@ -116,7 +122,7 @@ struct Act8WgradPlan {
   int tiles_m, tiles_n, whole_tiles, splits;
 };
 Act8WgradPlan act8_wgrad_plan(int rows, int d, int n);
-// mq: uint8 map {d, rows}, box {128, 64}, no swizzle; mdy: bf16 map {n,
+// mq: uint8 map {d, rows}, box {kWgradBM / 2, 64}, no swizzle; mdy: bf16 map {n,
 // rows}, box {64, 64}, 128-byte swizzle.
 cudaError_t launch_act8_wgrad(const CUtensorMap& mq, const CUtensorMap& mdy,
                               const Act8WgradArgs& a, cudaStream_t st);

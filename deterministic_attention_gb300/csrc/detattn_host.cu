@@ -1692,7 +1692,7 @@ int act8_wgrad(const void* q, const void* e, const void* dy, const float* row_sc
   CUtensorMap mq, mdy;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
-  const cuuint32_t box[2] = {kWgradBM, kWgradBK};
+  const cuuint32_t box[2] = {kWgradBM / 2, kWgradBK};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = g_encode(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims,
                               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

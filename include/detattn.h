@@ -354,7 +354,7 @@ int act8_pack(const void* x, void* q, void* e, int rows, int d, void* stream);
  * (all that act8_pack and the calls below write, besides 255). */
 int act8_unpack(const void* q, const void* e, void* x, int rows, int d, void* stream);
 
-/* Bytes of workspace act8_wgrad needs: fp32 128 x 256 tiles of partial sums,
+/* Bytes of workspace act8_wgrad needs: fp32 256 x 256 tiles of partial sums,
  * one for every token range of every tile that is cut (fixed by the shape).
  * 0 for an invalid shape, and where no tile is cut. */
 size_t act8_wgrad_workspace_bytes(int rows, int d, int n);
@@ -363,8 +363,9 @@ size_t act8_wgrad_workspace_bytes(int rows, int d, int n);
  *   dw[i, j] = row_scale[i] * sum_t x[t, i] dy[t, j],   x the checkpoint's values
  * dy bf16 [rows, n]; dw fp32 [d, n], fully overwritten (zeros for rows = 0);
  * row_scale fp32 [d] or NULL (1): the norm's weight where the checkpoint
- * holds the normed input before it (block_norm_fwd).  bf16 tensor cores, fp32
- * accumulation; each element's sum has a fixed order.  rows in [0, 2^24], d a
+ * holds the normed input before it (block_norm_fwd).  bf16 tensor cores; runs
+ * of at most 1024 tokens are summed there and the runs in fp32 registers, all
+ * in a fixed order.  rows in [0, 2^24], d a
  * multiple of 32 and n of 8, both up to 2^20, rows * d, rows * n and d * n
  * at most 4e9.  q, dy, dw, row_scale and workspace 16-byte aligned. */
 int act8_wgrad(const void* q, const void* e, const void* dy, const float* row_scale, float* dw,

@@ -53,10 +53,10 @@ def test_wgrad_rejects(L, kw, code):
 
 
 def test_wgrad_workspace_follows_the_shape(L):
-    tile = 128 * 256 * 4
-    assert L.act8_wgrad_workspace_bytes(4096, 768, 1280) == 30 * 5 * tile   # 30 tiles, five ranges each
+    tile = 256 * 256 * 4
+    assert L.act8_wgrad_workspace_bytes(4096, 768, 1280) == 15 * 5 * tile   # 15 tiles, five ranges each
     assert L.act8_wgrad_workspace_bytes(64, 768, 1280) == 0                 # one step: nothing to cut
-    assert L.act8_wgrad_workspace_bytes(4096, 128 * 8, 256 * 19) == 0       # 152 tiles
+    assert L.act8_wgrad_workspace_bytes(4096, 128 * 8, 256 * 19) == 0       # 76 tiles
     assert L.act8_wgrad_workspace_bytes(0, 768, 1280) == 0
     assert L.act8_wgrad_workspace_bytes(4096, 768, 1281) == 0
 

@@ -113,9 +113,10 @@ def test_act8_empty():
 @pytest.mark.parametrize("rows,d,n", [
     (1, 32, 8), (63, 64, 256), (64, 128, 264), (65, 160, 8), (500, 96, 1000), (1777, 1184, 504),
     (4096, 768, 1280),       # every tile cut
-    (192, 19 * 128, 8 * 256),  # exactly one whole tile for each block, nothing cut
+    (192, 19 * 256, 4 * 256),  # exactly one whole tile for each pair of blocks, nothing cut
     (700, 2496, 2200),       # whole tiles and cut ones, ragged both ways
-    (200, 2432, 5000),       # a block walks several whole tiles
+    (200, 2432, 5000),       # a pair walks several whole tiles
+    (2600, 4864, 1024),      # a whole tile takes its tokens in three runs
 ])
 @pytest.mark.parametrize("scaled", [False, True])
 def test_wgrad_matches_product(rows, d, n, scaled):
@@ -142,9 +143,9 @@ def test_wgrad_matches_product(rows, d, n, scaled):
 @pytest.mark.gpu
 def test_wgrad_plan_cases_are_what_they_say():
     """The shapes above reach whole tiles only, cut tiles only, and both."""
-    assert da.act8_wgrad_workspace_bytes(192, 19 * 128, 8 * 256) == 0
-    assert da.act8_wgrad_workspace_bytes(4096, 768, 1280) == 30 * 5 * 128 * 256 * 4
-    assert da.act8_wgrad_workspace_bytes(700, 2496, 2200) % (28 * 128 * 256 * 4) == 0
+    assert da.act8_wgrad_workspace_bytes(192, 19 * 256, 4 * 256) == 0
+    assert da.act8_wgrad_workspace_bytes(4096, 768, 1280) == 15 * 5 * 256 * 256 * 4
+    assert da.act8_wgrad_workspace_bytes(700, 2496, 2200) % (14 * 256 * 256 * 4) == 0
 
 
 @pytest.mark.gpu
