@@ -17,11 +17,15 @@
 // dY in and out 64), 875 clocks at 128 bytes a clock for 512 clocks of MMA.  A
 // pair of blocks (cta_group::2) on a 256 x 256 tile shares dY: 80 KB each, 625
 // clocks.  So blocks work in pairs, one persistent block per SM:
-//   warp 0       TMA producer: int8 and dY tiles of 64 tokens, five stages
-//   warp 1       (even block) tcgen05.mma issuer, M = 256, N = 256, K = 16
-//   warps 2, 3   (odd block) tell the issuer what that block has ready
-//   warps 4-11   int8 -> bf16
+//   warp 0       TMA producer of the int8 tiles (64 tokens each)
+//   warp 1       (even block) tcgen05.mma issuer, M = N = 256, K = 16
+//   warp 2       TMA producer of the dY tiles
+//   warps 4-11   int8 -> bf16, two groups of four taking turns
 //   warps 12-19  epilogue: accumulators -> fp32 sums in registers -> dw
+// The three tiles have rings of their own: a step is 0.31 us of MMA, a load
+// answers after one to two, and a stage that held all three from the load to
+// the end of its products was held too long (five such stages: 687 us for
+// 8192 x 4096 x 6144, with the products alone 221).
 // Two accumulators in TMEM take turns: one is added to the tile's sum in
 // registers after every 1024 tokens while the other fills.
 // Tiles left over when all pairs have taken an equal number of whole ones
@@ -40,32 +44,45 @@ __device__ unsigned int g_wgrad_status;
 
 namespace {
 
-constexpr int kStages = 5;
 constexpr int kHalfM = kWgradBM / 2, kHalfN = kWgradBN / 2;
-constexpr int kRawBytes = kWgradBK * kHalfM;         // 8 KB
+constexpr int kRawBytes = kWgradBK * kHalfM;         // 8 KB: int8
 constexpr int kABytes = kWgradBK * kHalfM * 2;       // 16 KB: two atoms of 64 columns
 constexpr int kBBytes = kWgradBK * kHalfN * 2;       // 16 KB: two atoms
-constexpr int kStageBytes = kRawBytes + kABytes + kBBytes;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kRawStages = 8, kAStages = 4, kBStages = 6;
+constexpr int kSmemBytes = kRawStages * kRawBytes + kAStages * kABytes + kBStages * kBBytes + 1024;
 static_assert(kSmemBytes <= 226 * 1024, "shared memory");
 static_assert(kRawBytes % 1024 == 0 && kABytes % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
 constexpr int kCtrlWarps = 4, kConvWarps = 8, kEpiWarps = 8;
+constexpr int kConvGroups = 2, kGroupWarps = kConvWarps / kConvGroups;
+static_assert(2 * kGroupWarps == 8 && kRawStages % kConvGroups == 0 && kAStages % kConvGroups == 0, "turns");
 constexpr int kThreads = 32 * (kCtrlWarps + kConvWarps + kEpiWarps);
 // Registers per thread after reallocation: an epilogue thread holds 128 sums.
 constexpr int kCtrlRegs = 48, kConvRegs = 64, kEpiRegs = 152;
 constexpr int kRegBudget = 32 * (kCtrlWarps * kCtrlRegs + kConvWarps * kConvRegs + kEpiWarps * kEpiRegs);
 
 enum : int {
-  kBarRaw = 0,               // int8 tile here (each block's own)
-  kBarB = kStages,           // both dY halves (the even block's)
-  kBarConv = 2 * kStages,    // bf16 operand written here (each block's own)
-  kBarPeer = 3 * kStages,    // ... and in the odd block (the even block's)
-  kBarEmpty = 4 * kStages,   // the stage's products are done (each block's)
-  kBarAcc = 5 * kStages,     // an accumulator is complete (each block's)
-  kBarAccFree = kBarAcc + 2, // it has been read here (each block's own)
-  kBarPeerFree = kBarAcc + 4,  // ... and in the odd block (the even block's)
-  kBarDrain = kBarAcc + 6,
-  kNumBars = kBarAcc + 7
+  kBarRaw = 0,                          // int8 tile is here (each block's own)
+  kBarRawFree = kBarRaw + kRawStages,   // it has been converted (each block's own)
+  kBarB = kBarRawFree + kRawStages,     // both dY halves are there (the even block's)
+  kBarBFree = kBarB + kBStages,         // their products are done (each block's)
+  kBarA = kBarBFree + kBStages,         // both bf16 operands are written (the even block's)
+  kBarAFree = kBarA + kAStages,         // their products are done (each block's)
+  kBarAcc = kBarAFree + kAStages,       // an accumulator is complete (each block's)
+  kBarAccFree = kBarAcc + 2,            // it has been read by both blocks (the even block's)
+  kBarDrain = kBarAccFree + 2,
+  kNumBars
+};
+
+// Position in a ring: stage and parity of the phase to wait for.
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
 };
 
 __device__ __forceinline__ void gave_up() { atomicOr(&g_wgrad_status, 1u); }
@@ -125,9 +142,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // The same offsets in both blocks (the products read both at one address).
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  auto sRaw = [&](int s) { return s0 + s * kStageBytes; };
-  auto sA = [&](int s) { return s0 + s * kStageBytes + kRawBytes; };
-  auto sB = [&](int s) { return s0 + s * kStageBytes + kRawBytes + kABytes; };
+  auto sRaw = [&](int s) { return s0 + s * kRawBytes; };
+  const uint32_t sA0 = s0 + kRawStages * kRawBytes, sB0 = sA0 + kAStages * kABytes;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto lead_bar = [&](int i) { return map_shared_rank(smem_u32(&bars[i]), 0); };
   if (warp == 1) {
@@ -136,17 +152,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kRawStages; ++s) {
       mbar_init(bar(kBarRaw + s), 1);
+      mbar_init(bar(kBarRawFree + s), kGroupWarps);
+    }
+    for (int s = 0; s < kBStages; ++s) {
       mbar_init(bar(kBarB + s), 1);
-      mbar_init(bar(kBarConv + s), kConvWarps);
-      mbar_init(bar(kBarPeer + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
+      mbar_init(bar(kBarBFree + s), 1);
+    }
+    for (int s = 0; s < kAStages; ++s) {
+      mbar_init(bar(kBarA + s), 2 * kGroupWarps);
+      mbar_init(bar(kBarAFree + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarAcc + i), 1);
-      mbar_init(bar(kBarAccFree + i), kEpiWarps);
-      mbar_init(bar(kBarPeerFree + i), 1);
+      mbar_init(bar(kBarAccFree + i), 2 * kEpiWarps);
     }
     mbar_init(bar(kBarDrain), 1);
     fence_barrier_init();
@@ -166,120 +186,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kCtrlWarps) {
     setmaxnreg_dec<kCtrlRegs>();
     if (warp == 0) {
+      // int8 tiles.
       if (lane == 0) {
-        int s = 0, it = 0;  // stage; steps so far, over all units
-        uint32_t parity = 1;
+        Ring r;
+        int it = 0;  // steps so far, over all units
         for (int u = pair; u < n_units && ok; u += pairs) {
           const Unit w = unit_at(a, u);
           int m0, n0;
           tile_origin(a, w.tile, &m0, &n0);
-          m0 += rank * kHalfM;
-          n0 += rank * kHalfN;
           for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-            if (it >= kStages && !(ok = mbar_wait(bar(kBarEmpty + s), parity, a.wait_ns))) break;
-            mbar_arrive_expect_tx(bar(kBarRaw + s), kRawBytes);
-            tma_load_2d(sRaw(s), &mq, bar(kBarRaw + s), m0, kb * kWgradBK);
-            if (rank == 0) mbar_arrive_expect_tx(bar(kBarB + s), 2 * kBBytes);
-            const uint32_t to = lead_bar(kBarB + s);
-            tma_load_2d_pair(sB(s), &mdy, to, n0, kb * kWgradBK);
-            tma_load_2d_pair(sB(s) + 8192, &mdy, to, n0 + 64, kb * kWgradBK);
-            if (++s == kStages) {
-              s = 0;
-              parity ^= 1u;
-            }
+            if (it >= kRawStages && !(ok = mbar_wait(bar(kBarRawFree + r.s), r.parity ^ 1u, a.wait_ns)))
+              break;
+            mbar_arrive_expect_tx(bar(kBarRaw + r.s), kRawBytes);
+            tma_load_2d(sRaw(r.s), &mq, bar(kBarRaw + r.s), m0 + rank * kHalfM, kb * kWgradBK);
+            r.next(kRawStages);
           }
         }
-        // After a wait that ran out: the copies in flight, before the block ends.
-        if (!ok)
-          for (int k = it > kStages ? it - kStages : 0; k < it; ++k) {
-            mbar_wait(bar(kBarRaw + k % kStages), (k / kStages) & 1, a.wait_ns);
-            if (rank == 0) mbar_wait(bar(kBarB + k % kStages), (k / kStages) & 1, a.wait_ns);
-          }
+        if (!ok) {
+          // The copies in flight, before the block ends.
+          for (int k = it > kRawStages ? it - kRawStages : 0; k < it; ++k)
+            mbar_wait(bar(kBarRaw + k % kRawStages), (k / kRawStages) & 1, a.wait_ns);
+          gave_up();
+        }
       }
-      if (!ok) gave_up();
+      __syncwarp();
+    } else if (warp == 2) {
+      // dY tiles: this block's half of the columns, on the even block's barrier.
+      if (lane == 0) {
+        Ring r;
+        int it = 0;
+        for (int u = pair; u < n_units && ok; u += pairs) {
+          const Unit w = unit_at(a, u);
+          int m0, n0;
+          tile_origin(a, w.tile, &m0, &n0);
+          n0 += rank * kHalfN;
+          for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+            if (it >= kBStages && !(ok = mbar_wait(bar(kBarBFree + r.s), r.parity ^ 1u, a.wait_ns)))
+              break;
+            if (rank == 0) mbar_arrive_expect_tx(bar(kBarB + r.s), 2 * kBBytes);
+            const uint32_t to = lead_bar(kBarB + r.s), dst = sB0 + r.s * kBBytes;
+            tma_load_2d_pair(dst, &mdy, to, n0, kb * kWgradBK);
+            tma_load_2d_pair(dst + 8192, &mdy, to, n0 + 64, kb * kWgradBK);
+            r.next(kBStages);
+          }
+        }
+        if (!ok) {
+          // The odd block's copies complete here too; it leaves no earlier
+          // than this block.
+          if (rank == 0)
+            for (int k = it > kBStages ? it - kBStages : 0; k < it; ++k)
+              mbar_wait(bar(kBarB + k % kBStages), (k / kBStages) & 1, a.wait_ns);
+          gave_up();
+        }
+      }
       __syncwarp();
     } else if (warp == 1 && rank == 0) {
       constexpr uint32_t kId = idesc_bf16(kWgradBM, kWgradBN, true, true);
       // MN-major tiles: 16 tokens are 16 rows of 128 bytes; atoms lie 8 KB apart.
-      const uint64_t dA0 = sdesc_sw128(sA(0), 8192, 1024);
-      const uint64_t dB0 = sdesc_sw128(sB(0), 8192, 1024);
-      int s = 0, n = 0;  // n: accumulators filled
-      uint32_t parity = 0;
+      const uint64_t dA0 = sdesc_sw128(sA0, 8192, 1024);
+      const uint64_t dB0 = sdesc_sw128(sB0, 8192, 1024);
+      Ring ra, rb;
+      int n = 0;  // accumulators filled
       for (int u = pair; u < n_units && ok; u += pairs) {
         const Unit w = unit_at(a, u);
         for (int c = w.kb0; c < w.kb1 && ok; c += kWgradChunk, ++n) {
           const int acc = n & 1, end = min(c + kWgradChunk, w.kb1);
-          if (n >= 2) {
-            const uint32_t p = ((n >> 1) & 1) ^ 1;
-            if (!(ok = warp_all(mbar_wait(bar(kBarAccFree + acc), p, a.wait_ns)))) break;
-            if (!(ok = warp_all(mbar_wait_cluster(bar(kBarPeerFree + acc), p, a.wait_ns)))) break;
-          }
+          if (n >= 2 &&
+              !(ok = warp_all(mbar_wait_cluster(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, a.wait_ns))))
+            break;
           tc_fence_after();
           for (int kb = c; kb < end; ++kb) {
-            if (!(ok = warp_all(mbar_wait(bar(kBarB + s), parity, a.wait_ns)))) break;
-            if (!(ok = warp_all(mbar_wait(bar(kBarConv + s), parity, a.wait_ns)))) break;
-            if (!(ok = warp_all(mbar_wait_cluster(bar(kBarPeer + s), parity, a.wait_ns)))) break;
+            if (!(ok = warp_all(mbar_wait(bar(kBarB + rb.s), rb.parity, a.wait_ns)))) break;
+            if (!(ok = warp_all(mbar_wait_cluster(bar(kBarA + ra.s), ra.parity, a.wait_ns)))) break;
             tc_fence_after();
-            const uint64_t da = desc_add(dA0, s * kStageBytes), db = desc_add(dB0, s * kStageBytes);
+            const uint64_t da = desc_add(dA0, ra.s * kABytes), db = desc_add(dB0, rb.s * kBBytes);
             mma_ss_x4_pair(tmem + acc * kWgradBN, da, desc_add(da, 2048), desc_add(da, 4096),
                            desc_add(da, 6144), db, desc_add(db, 2048), desc_add(db, 4096),
                            desc_add(db, 6144), kId, kb > c ? 1u : 0u);
-            mma_commit_pair(bar(kBarEmpty + s));
-            if (++s == kStages) {
-              s = 0;
-              parity ^= 1u;
-            }
+            mma_commit_pair(bar(kBarAFree + ra.s));
+            mma_commit_pair(bar(kBarBFree + rb.s));
+            ra.next(kAStages);
+            rb.next(kBStages);
           }
           if (ok) mma_commit_pair(bar(kBarAcc + acc));
         }
       }
       mma_commit_pair(bar(kBarDrain));
       if (!warp_all(mbar_wait(bar(kBarDrain), 0, a.wait_ns)) || !ok) gave_up();
-    } else if (warp == 2 && rank == 1) {
-      // The odd block's operands, passed on to the issuer.  (One thread with
-      // no loads or stores of its own in flight does it: an arrival that
-      // releases to the cluster waits for all that its thread has begun, and
-      // the converting warps always have exponent loads under way.  With
-      // their own arrivals there a step took 2500 clocks.)
-      if (lane == 0) {
-        const int total = total_steps(a, pair, pairs);
-        const uint32_t to = lead_bar(kBarPeer);
-        int s = 0;
-        uint32_t parity = 0;
-        for (int it = 0; it < total; ++it) {
-          if (!(ok = mbar_wait(bar(kBarConv + s), parity, a.wait_ns))) break;
-          mbar_arrive_remote(to + 8 * s);
-          if (++s == kStages) {
-            s = 0;
-            parity ^= 1u;
-          }
-        }
-        if (!ok) gave_up();
-      }
-      __syncwarp();
-    } else if (warp == 3 && rank == 1) {
-      // Its accumulators read, likewise.
-      if (lane == 0) {
-        const uint32_t to = lead_bar(kBarPeerFree);
-        int n = 0;
-        for (int u = pair; u < n_units && ok; u += pairs)
-          for (int chunks = unit_chunks(a, u); chunks > 0; --chunks, ++n) {
-            if (!(ok = mbar_wait(bar(kBarAccFree + (n & 1)), (n >> 1) & 1, a.wait_ns))) break;
-            mbar_arrive_remote(to + 8 * (n & 1));
-          }
-        if (!ok) gave_up();
-      }
-      __syncwarp();
     }
   } else if (warp < kCtrlWarps + kConvWarps) {
     // int8 -> bf16: thread (warp, lane) turns columns 8 j .. 8 j + 7, j =
-    // lane % 16, of every 16th token row.  Half a warp reads one 128-byte
+    // lane % 16, of every eighth token row.  Half a warp reads one 128-byte
     // row, and eight lanes write one 128-byte row of an atom, the 16-byte
     // pieces exchanged as the swizzle wants: no bank conflicts either way.
+    // The two groups take steps in turn, so that one group's waits and fences
+    // run beside the other's arithmetic.
     setmaxnreg_dec<kConvRegs>();
-    const int cw = warp - kCtrlWarps, j = lane & 15, r0 = cw * 2 + (lane >> 4);
-    constexpr int kRows = kWgradBK / (2 * kConvWarps);  // rows per thread and step
-    constexpr int kAhead = 4;                           // steps that exponents are fetched ahead
+    const int cw = warp - kCtrlWarps, group = cw / kGroupWarps, j = lane & 15;
+    const int r0 = (cw % kGroupWarps) * 2 + (lane >> 4);
+    constexpr int kRowStep = 2 * kGroupWarps, kRows = kWgradBK / kRowStep;  // eight rows per thread
+    constexpr int kAhead = 2;  // of its steps that a group fetches exponents ahead
     const int groups = a.d / kAct8Group;
     // The exponents' cursor: the step whose bytes are fetched next.
     int fu = pair, fkb = 0, fend = 0;
@@ -295,54 +301,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       fkb = w.kb0;
       fend = w.kb1;
     };
-    open();
-    auto fetch = [&](uint32_t (&e)[kRows]) {
-      if (fu >= n_units) return;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = fkb * kWgradBK + r0 + 2 * kConvWarps * i;
-        e[i] = fat[static_cast<size_t>(min(row, a.rows - 1)) * groups];
-      }
-      if (++fkb == fend) {
+    auto step = [&]() {
+      if (++fkb >= fend) {
         fu += pairs;
         open();
       }
     };
+    auto fetch = [&](uint32_t (&e)[kRows]) {
+      if (fu >= n_units) return;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        e[i] = fat[static_cast<size_t>(min(fkb * kWgradBK + r0 + kRowStep * i, a.rows - 1)) * groups];
+#pragma unroll
+      for (int i = 0; i < kConvGroups; ++i)
+        if (fu < n_units) step();
+    };
+    open();
+    if (group == 1) step();
     uint32_t e[kAhead][kRows];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(e[i]);
     const int total = total_steps(a, pair, pairs);
-    int s = 0;
-    uint32_t parity = 0;
-    for (int it = 0; it < total && ok; it += kAhead) {
+    Ring rr, ra;
+    if (group == 1) {
+      rr.next(kRawStages);
+      ra.next(kAStages);
+    }
+    for (int it = group; it < total && ok; it += kConvGroups * kAhead) {
 #pragma unroll
       for (int h = 0; h < kAhead; ++h) {
-        if (it + h < total && ok) {
-          ok = warp_all(mbar_wait(bar(kBarRaw + s), parity, a.wait_ns));
-          uint2 q[kRows];
+        if (it + kConvGroups * h < total && ok) {
+          ok = warp_all(mbar_wait(bar(kBarRaw + rr.s), rr.parity, a.wait_ns));
+          if (ok && it + kConvGroups * h >= kAStages)
+            ok = warp_all(mbar_wait(bar(kBarAFree + ra.s), ra.parity ^ 1u, a.wait_ns));
+          const uint32_t raw = sRaw(rr.s) + r0 * 128 + j * 8;
+          const uint32_t out = sA0 + ra.s * kABytes + (j >> 3) * 8192 + r0 * 128 + (((j & 7) ^ r0) << 4);
+          // Eight rows down, the swizzle (row % 8) is the same.
 #pragma unroll
-          for (int i = 0; i < kRows; ++i)
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(q[i].x), "=r"(q[i].y)
-                         : "r"(sRaw(s) + (r0 + 2 * kConvWarps * i) * 128 + j * 8)
-                         : "memory");
+          for (int i0 = 0; i0 < kRows; i0 += 4) {
+            uint2 q[4];
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + 2 * kConvWarps * i;
-            Vec8 v;
-            v.from_int8(q[i]);
-            const uint64_t sc = f2_all(act8_scale(e[h][i]));
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                           : "=r"(q[i].x), "=r"(q[i].y)
+                           : "r"(raw + kRowStep * (i0 + i) * 128));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v.p[k] = f2_mul(v.p[k], sc);
-            st_shared_u4(sA(s) + (j >> 3) * 8192 + r * 128 + (((j & 7) ^ (r & 7)) << 4), v.to_bf16());
+            for (int i = 0; i < 4; ++i) {
+              Vec8 v;
+              v.from_int8(q[i]);
+              const uint64_t sc = f2_all(act8_scale(e[h][i0 + i]));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v.p[k] = f2_mul(v.p[k], sc);
+              st_shared_u4(out + kRowStep * (i0 + i) * 128, v.to_bf16());
+            }
           }
           fetch(e[h]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(bar(kBarConv + s));
-          if (++s == kStages) {
-            s = 0;
-            parity ^= 1u;
+          if (lane == 0 && ok) {
+            mbar_arrive(bar(kBarRawFree + rr.s));
+            mbar_arrive_pair(lead_bar(kBarA + ra.s));
+          }
+#pragma unroll
+          for (int k = 0; k < kConvGroups; ++k) {
+            rr.next(kRawStages);
+            ra.next(kAStages);
           }
         }
       }
@@ -386,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarAccFree + acc));
+        if (lane == 0) mbar_arrive_pair(lead_bar(kBarAccFree + acc));
       }
       if (!ok) {
         gave_up();
