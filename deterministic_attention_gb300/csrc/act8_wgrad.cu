@@ -8,7 +8,7 @@
 //
 // Every checkpointed value is a bf16 number, so the product runs on the bf16
 // tensor cores with no further rounding of X: TMA brings the int8 tile and
-// the dY tile, eight warps turn the int8 tile into the swizzled bf16 operand
+// the dY tile, twelve warps turn the int8 tile into the swizzled bf16 operand
 // next to it, and one warp issues tcgen05.mma.  Tokens are the K dimension of
 // both operands, which are read MN-major as they lie in memory.
 //
@@ -20,8 +20,8 @@
 //   warp 0       TMA producer of the int8 tiles (64 tokens each)
 //   warp 1       (even block) tcgen05.mma issuer, M = N = 256, K = 16
 //   warp 2       TMA producer of the dY tiles
-//   warps 4-11   int8 -> bf16, two groups of four taking turns
-//   warps 12-19  epilogue: accumulators -> fp32 sums in registers -> dw
+//   warps 4-15   int8 -> bf16, three groups of four taking turns
+//   warps 16-23  epilogue: accumulators -> fp32 sums in registers -> dw
 // The three tiles have rings of their own: a step is 0.31 us of MMA, a load
 // answers after one to two, and a stage that held all three from the load to
 // the end of its products was held too long (five such stages: 687 us for
@@ -52,12 +52,12 @@ constexpr int kRawStages = 8, kAStages = 4, kBStages = 6;
 constexpr int kSmemBytes = kRawStages * kRawBytes + kAStages * kABytes + kBStages * kBBytes + 1024;
 static_assert(kSmemBytes <= 226 * 1024, "shared memory");
 static_assert(kRawBytes % 1024 == 0 && kABytes % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
-constexpr int kCtrlWarps = 4, kConvWarps = 8, kEpiWarps = 8;
-constexpr int kConvGroups = 2, kGroupWarps = kConvWarps / kConvGroups;
-static_assert(2 * kGroupWarps == 8 && kRawStages % kConvGroups == 0 && kAStages % kConvGroups == 0, "turns");
+constexpr int kCtrlWarps = 4, kConvWarps = 12, kEpiWarps = 8;
+constexpr int kConvGroups = 3, kGroupWarps = kConvWarps / kConvGroups;
+static_assert(2 * kGroupWarps == 8, "a group's row step keeps the swizzle");
 constexpr int kThreads = 32 * (kCtrlWarps + kConvWarps + kEpiWarps);
 // Registers per thread after reallocation: an epilogue thread holds 128 sums.
-constexpr int kCtrlRegs = 48, kConvRegs = 64, kEpiRegs = 152;
+constexpr int kCtrlRegs = 48, kConvRegs = 48, kEpiRegs = 144;
 constexpr int kRegBudget = 32 * (kCtrlWarps * kCtrlRegs + kConvWarps * kConvRegs + kEpiWarps * kEpiRegs);
 
 enum : int {
@@ -86,6 +86,27 @@ struct Ring {
 };
 
 __device__ __forceinline__ void gave_up() { atomicOr(&g_wgrad_status, 1u); }
+// Four int8 bytes times a power of two (`scale`: its bf16 bits in both halves)
+// as bf16, in the order 0, 2, 1, 3: masks then leave the bytes where they are.
+// With m the low seven bits and s the sign bit, a value is (128 + m) - 128 (1 +
+// s): both terms are bf16 numbers that take one LOP3 from the bytes (0x4300 |
+// m and 0xC300 | s << 7), and every step is exact.  (Ten ALU instructions
+// for eight values; through fp32 and its packing conversion it takes
+// fourteen, and the ALU is what these warps wait for.)
+__device__ __forceinline__ uint32_t bf16x2_of_bytes(uint32_t x, uint32_t scale) {
+  const uint32_t m = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0xC300C300u;
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\t"
+      "add.rn.bf16x2 t, %1, %2;\n\t"
+      "mul.rn.bf16x2 %0, t, %3;\n\t}"
+      : "=r"(r)
+      : "r"(m), "r"(c), "r"(scale));
+  return r;
+}
+// Where the column at position p of a tile lies in the checkpoint: the order
+// above, i.e. the two low bits of p exchanged.
+__device__ __forceinline__ int column_of(int p) { return (p & ~3) | ((p & 1) << 1) | ((p >> 1) & 1); }
+
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 
 // Work of one pair, in order: whole tiles pair, pair + pairs, ..., then
@@ -195,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int m0, n0;
           tile_origin(a, w.tile, &m0, &n0);
           for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-            if (it >= kRawStages && !(ok = mbar_wait(bar(kBarRawFree + r.s), r.parity ^ 1u, a.wait_ns)))
+            if (it >= kRawStages && !(ok = mbar_wait_hint(bar(kBarRawFree + r.s), r.parity ^ 1u, a.wait_ns)))
               break;
             mbar_arrive_expect_tx(bar(kBarRaw + r.s), kRawBytes);
             tma_load_2d(sRaw(r.s), &mq, bar(kBarRaw + r.s), m0 + rank * kHalfM, kb * kWgradBK);
@@ -205,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) {
           // The copies in flight, before the block ends.
           for (int k = it > kRawStages ? it - kRawStages : 0; k < it; ++k)
-            mbar_wait(bar(kBarRaw + k % kRawStages), (k / kRawStages) & 1, a.wait_ns);
+            mbar_wait_hint(bar(kBarRaw + k % kRawStages), (k / kRawStages) & 1, a.wait_ns);
           gave_up();
         }
       }
@@ -221,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tile_origin(a, w.tile, &m0, &n0);
           n0 += rank * kHalfN;
           for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-            if (it >= kBStages && !(ok = mbar_wait(bar(kBarBFree + r.s), r.parity ^ 1u, a.wait_ns)))
+            if (it >= kBStages && !(ok = mbar_wait_hint(bar(kBarBFree + r.s), r.parity ^ 1u, a.wait_ns)))
               break;
             if (rank == 0) mbar_arrive_expect_tx(bar(kBarB + r.s), 2 * kBBytes);
             const uint32_t to = lead_bar(kBarB + r.s), dst = sB0 + r.s * kBBytes;
@@ -235,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // than this block.
           if (rank == 0)
             for (int k = it > kBStages ? it - kBStages : 0; k < it; ++k)
-              mbar_wait(bar(kBarB + k % kBStages), (k / kBStages) & 1, a.wait_ns);
+              mbar_wait_hint(bar(kBarB + k % kBStages), (k / kBStages) & 1, a.wait_ns);
           gave_up();
         }
       }
@@ -252,12 +273,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = w.kb0; c < w.kb1 && ok; c += kWgradChunk, ++n) {
           const int acc = n & 1, end = min(c + kWgradChunk, w.kb1);
           if (n >= 2 &&
-              !(ok = warp_all(mbar_wait_cluster(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, a.wait_ns))))
+              !(ok = warp_all(mbar_wait_hint<true>(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, a.wait_ns))))
             break;
           tc_fence_after();
           for (int kb = c; kb < end; ++kb) {
-            if (!(ok = warp_all(mbar_wait(bar(kBarB + rb.s), rb.parity, a.wait_ns)))) break;
-            if (!(ok = warp_all(mbar_wait_cluster(bar(kBarA + ra.s), ra.parity, a.wait_ns)))) break;
+            if (!(ok = warp_all(mbar_wait_hint(bar(kBarB + rb.s), rb.parity, a.wait_ns)))) break;
+            if (!(ok = warp_all(mbar_wait_hint<true>(bar(kBarA + ra.s), ra.parity, a.wait_ns)))) break;
             tc_fence_after();
             const uint64_t da = desc_add(dA0, ra.s * kABytes), db = desc_add(dB0, rb.s * kBBytes);
             mma_ss_x4_pair(tmem + acc * kWgradBN, da, desc_add(da, 2048), desc_add(da, 4096),
@@ -272,20 +293,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit_pair(bar(kBarDrain));
-      if (!warp_all(mbar_wait(bar(kBarDrain), 0, a.wait_ns)) || !ok) gave_up();
+      if (!warp_all(mbar_wait_hint(bar(kBarDrain), 0, a.wait_ns)) || !ok) gave_up();
     }
   } else if (warp < kCtrlWarps + kConvWarps) {
     // int8 -> bf16: thread (warp, lane) turns columns 8 j .. 8 j + 7, j =
     // lane % 16, of every eighth token row.  Half a warp reads one 128-byte
     // row, and eight lanes write one 128-byte row of an atom, the 16-byte
     // pieces exchanged as the swizzle wants: no bank conflicts either way.
-    // The two groups take steps in turn, so that one group's waits and fences
-    // run beside the other's arithmetic.
+    // The groups take steps in turn, so that one group's waits and fences run
+    // beside the others' arithmetic.
     setmaxnreg_dec<kConvRegs>();
     const int cw = warp - kCtrlWarps, group = cw / kGroupWarps, j = lane & 15;
     const int r0 = (cw % kGroupWarps) * 2 + (lane >> 4);
     constexpr int kRowStep = 2 * kGroupWarps, kRows = kWgradBK / kRowStep;  // eight rows per thread
-    constexpr int kAhead = 2;  // of its steps that a group fetches exponents ahead
+    constexpr int kAhead = 1;  // of its steps that a group fetches exponents ahead
     const int groups = a.d / kAct8Group;
     // The exponents' cursor: the step whose bytes are fetched next.
     int fu = pair, fkb = 0, fend = 0;
@@ -311,19 +332,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (fu >= n_units) return;
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
-        e[i] = fat[static_cast<size_t>(min(fkb * kWgradBK + r0 + kRowStep * i, a.rows - 1)) * groups];
+        asm volatile("ld.global.nc.u8 %0, [%1];"
+                     : "=r"(e[i])
+                     : "l"(fat + static_cast<size_t>(min(fkb * kWgradBK + r0 + kRowStep * i, a.rows - 1)) * groups));
 #pragma unroll
       for (int i = 0; i < kConvGroups; ++i)
         if (fu < n_units) step();
     };
     open();
-    if (group == 1) step();
+    for (int i = 0; i < group; ++i)
+      if (fu < n_units) step();
     uint32_t e[kAhead][kRows];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(e[i]);
     const int total = total_steps(a, pair, pairs);
     Ring rr, ra;
-    if (group == 1) {
+    for (int i = 0; i < group; ++i) {
       rr.next(kRawStages);
       ra.next(kAStages);
     }
@@ -331,9 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < kAhead; ++h) {
         if (it + kConvGroups * h < total && ok) {
-          ok = warp_all(mbar_wait(bar(kBarRaw + rr.s), rr.parity, a.wait_ns));
+          ok = warp_all(mbar_wait_hint(bar(kBarRaw + rr.s), rr.parity, a.wait_ns));
           if (ok && it + kConvGroups * h >= kAStages)
-            ok = warp_all(mbar_wait(bar(kBarAFree + ra.s), ra.parity ^ 1u, a.wait_ns));
+            ok = warp_all(mbar_wait_hint(bar(kBarAFree + ra.s), ra.parity ^ 1u, a.wait_ns));
           const uint32_t raw = sRaw(rr.s) + r0 * 128 + j * 8;
           const uint32_t out = sA0 + ra.s * kABytes + (j >> 3) * 8192 + r0 * 128 + (((j & 7) ^ r0) << 4);
           // Eight rows down, the swizzle (row % 8) is the same.
@@ -347,12 +371,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            : "r"(raw + kRowStep * (i0 + i) * 128));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              Vec8 v;
-              v.from_int8(q[i]);
-              const uint64_t sc = f2_all(act8_scale(e[h][i0 + i]));
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v.p[k] = f2_mul(v.p[k], sc);
-              st_shared_u4(out + kRowStep * (i0 + i) * 128, v.to_bf16());
+              // 2^(e - 127), twice.  (Volatile: formed here, not where the byte
+              // is loaded, or the load would be waited for there.)
+              uint32_t sc;
+              asm volatile("mul.lo.u32 %0, %1, 0x00800080;" : "=r"(sc) : "r"(e[h][i0 + i]));
+              st_shared_u4(out + kRowStep * (i0 + i) * 128,
+                           make_uint4(bf16x2_of_bytes(q[i].x, sc), bf16x2_of_bytes(q[i].x >> 8, sc),
+                                      bf16x2_of_bytes(q[i].y, sc), bf16x2_of_bytes(q[i].y >> 8, sc)));
             }
           }
           fetch(e[h]);
@@ -392,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) sum[h][g][i] = 0;
       for (int chunks = unit_chunks(a, u); chunks > 0; --chunks, ++n) {
         const int acc = n & 1;
-        if (!(ok = warp_all(mbar_wait(bar(kBarAcc + acc), (n >> 1) & 1, a.wait_ns)))) break;
+        if (!(ok = warp_all(mbar_wait_hint(bar(kBarAcc + acc), (n >> 1) & 1, a.wait_ns)))) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -419,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int m0, n0;
       tile_origin(a, w.tile, &m0, &n0);
       const bool part = w.part >= 0;
-      const int r0 = static_cast<int>(cluster_ctarank()) * kHalfM + (warp & 3) * 32 + (lane >> 2);
+      const int r0 = static_cast<int>(cluster_ctarank()) * kHalfM + (warp & 3) * 32 + column_of(lane >> 2);
       const int c0 = half * kHalfN + 2 * (lane & 3);
       const int left = part ? kWgradBN : a.n - n0;  // columns to write
 #pragma unroll

@@ -89,26 +89,39 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   return false;
 }
 
-// The same for a barrier that threads of another block of the cluster arrive
-// on: what they wrote before is visible after the wait.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+// The same with a hint that lets the hardware suspend the thread for up to 20
+// us at a time (it wakes when the phase completes), so that warps that wait
+// long take no issue slots from those at work; and for a barrier that threads
+// of another block of the cluster arrive on, whose earlier writes are visible
+// after the wait.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait_hint<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
+    if (mbar_try_wait_hint<CLUSTER>(bar, parity)) return true;
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
   return false;
