@@ -33,23 +33,24 @@ __device__ __forceinline__ uint32_t act8_exponent(uint32_t m) {
   return static_cast<uint32_t>(e > 1 ? e : 1);
 }
 
-// Eight values of one lane; the four lanes of an aligned quad hold one group.
-// Returns the exponent byte and writes the eight int8 values.  Every lane of
-// the warp takes part.
-__device__ __forceinline__ uint32_t act8_quantise8(const float (&v)[8], uint2* q) {
+// Eight values v times `mult` >= 0 of one lane; the four lanes of an aligned
+// quad hold one group.  Returns the exponent byte and writes the eight int8
+// values.  Every lane of the warp takes part.  (v mult 2^-k is rounded once,
+// to a whole number: 2^-k mult is exact.)
+__device__ __forceinline__ uint32_t act8_quantise8(const float (&v)[8], float mult, uint2* q) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, act8_abs_bits(v[i]));
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  const uint32_t e = act8_exponent(m);
+  const uint32_t e = act8_exponent(act8_abs_bits(__uint_as_float(m) * mult));
   if (e == 255u) {
     *q = make_uint2(0u, 0u);
     return e;
   }
   // x 2^-k + 1.5 2^23: the sum's low byte is the rounded value in two's
   // complement.
-  const float inv = __uint_as_float((254u - e) << 23);
+  const float inv = __uint_as_float((254u - e) << 23) * mult;
   float r[8];
   uint32_t b[8];
 #pragma unroll
@@ -133,6 +134,37 @@ struct Vec8 {
                             __uint_as_float(__byte_perm(u[i >> 1], 0x4B000000u, i & 1 ? 0x7443 : 0x7441))),
                     off);
   }
+  __device__ __forceinline__ void to_float(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_split(p[i], f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ void mul(const Vec8& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2_mul(p[i], b.p[i]);
+  }
+  __device__ __forceinline__ void scale(float x) {
+    const uint64_t k = f2_all(x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2_mul(p[i], k);
+  }
+  // Adds the squares to a pair of sums.
+  __device__ __forceinline__ void squares(uint64_t& sum) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = f2_fma(p[i], p[i], sum);
+  }
+  // Logistic function 1 / (1 + 2^(-x log2 e)), within a few units of 2^-23 for
+  // |x| up to about 8 (what the rounded exponent leaves, |x| 2^-24, shrinks
+  // with 1 - sigma for x > 0).  An infinite power gives 0.
+  __device__ __forceinline__ void sigmoid() {
+    const uint64_t k = f2_all(-1.44269504f), one = f2_all(1.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      f2_split(f2_mul(p[i], k), x, y);
+      f2_split(f2_add(f2_make(ex2_approx(x), ex2_approx(y)), one), x, y);
+      p[i] = f2_make(__fdividef(1.0f, x), __fdividef(1.0f, y));
+    }
+  }
   __device__ __forceinline__ uint4 to_bf16() const {
     uint32_t w[4];
 #pragma unroll
@@ -150,7 +182,7 @@ struct Vec8 {
   }
 };
 
-// ------------------------------------------------------------ eight bf16 / fp32 values
+// Eight separate values.
 __device__ __forceinline__ void bf16x8_to_float(uint4 x, float (&f)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -162,16 +194,6 @@ __device__ __forceinline__ void bf16x8_to_float(uint4 x, float (&f)[8]) {
 __device__ __forceinline__ uint4 float_to_bf16x8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void f32x8_to_float(uint4 a, uint4 b, float (&f)[8]) {
-  f[0] = __uint_as_float(a.x);
-  f[1] = __uint_as_float(a.y);
-  f[2] = __uint_as_float(a.z);
-  f[3] = __uint_as_float(a.w);
-  f[4] = __uint_as_float(b.x);
-  f[5] = __uint_as_float(b.y);
-  f[6] = __uint_as_float(b.z);
-  f[7] = __uint_as_float(b.w);
 }
 
 }  // namespace detattn

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads)
     float f[8];
     uint2 out;
     bf16x8_to_float(raw[j], f);
-    const uint32_t ex = act8_quantise8(f, &out);
+    const uint32_t ex = act8_quantise8(f, 1.0f, &out);
     if (v < n_vec) {
       q[v] = out;
       if ((v & 3) == 0) e[v >> 2] = static_cast<uint8_t>(ex);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
   if (in) h[v] = float_to_bf16x8(o);
   if constexpr (KEEP8) {
     uint2 qa, qb;
-    const uint32_t ea = act8_quantise8(a, &qa), eb = act8_quantise8(b, &qb);
+    const uint32_t ea = act8_quantise8(a, 1.0f, &qa), eb = act8_quantise8(b, 1.0f, &qb);
     if (in) {
       q[ia] = qa;
       q[ib] = qb;

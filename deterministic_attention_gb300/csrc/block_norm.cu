@@ -59,27 +59,12 @@ __device__ __forceinline__ float team_sum(float v, float* words, int W, int team
   return v;
 }
 
-__device__ __forceinline__ void load_f32x8(const float* p, float (&f)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-  f32x8_to_float(a, b, f);
-}
-// Eight gate values of one gate row, and (for the backward) their slopes by
-// the stored value.
-__device__ __forceinline__ void load_gate8(const void* gate, size_t at, bool fp32, bool sigmoid,
-                                           float (&g)[8], float (&slope)[8]) {
+// Eight gate values of the bf16 or fp32 gate from element `at` on.
+__device__ __forceinline__ void load_gate(const void* gate, size_t at, bool fp32, Vec8& g) {
   if (fp32)
-    load_f32x8(static_cast<const float*>(gate) + at, g);
+    g.from_f32(static_cast<const float*>(gate) + at);
   else
-    bf16x8_to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gate) + at)), g);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    slope[i] = 1.0f;
-    if (sigmoid) {
-      g[i] = 1.0f / (1.0f + __expf(-g[i]));
-      slope[i] = g[i] * (1.0f - g[i]);
-    }
-  }
+    g.from_bf16(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gate) + at));
 }
 
 // Eight stream values (bf16 or fp32) as raw words.
@@ -99,29 +84,31 @@ struct Raw8 {
       a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (F32)
-      f32x8_to_float(a, b, f);
-    else
-      bf16x8_to_float(a, f);
+  __device__ __forceinline__ void get(Vec8& v) const {
+    if constexpr (F32) {
+      v.p[0] = f2_make(__uint_as_float(a.x), __uint_as_float(a.y));
+      v.p[1] = f2_make(__uint_as_float(a.z), __uint_as_float(a.w));
+      v.p[2] = f2_make(__uint_as_float(b.x), __uint_as_float(b.y));
+      v.p[3] = f2_make(__uint_as_float(b.z), __uint_as_float(b.w));
+    } else {
+      v.from_bf16(a);
+    }
   }
 };
 template <bool F32>
-__device__ __forceinline__ void store8(void* p, size_t at, const float (&f)[8]) {
-  if constexpr (F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) = float_to_bf16x8(f);
-  }
+__device__ __forceinline__ void store8(void* p, size_t at, const Vec8& v) {
+  if constexpr (F32)
+    v.to_f32(static_cast<float*>(p) + at);
+  else
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) = v.to_bf16();
 }
-// Eight checkpointed values; lanes past the row (`in` false) take part in the
-// group's shuffles and store nothing.
-__device__ __forceinline__ void keep8(const float (&v)[8], bool in, size_t at, int8_t* q,
-                                      uint8_t* e) {
+// Eight checkpointed values v mult; lanes past the row (`in` false) take part
+// in the group's shuffles and store nothing.
+__device__ __forceinline__ void keep8(const Vec8& v, float mult, bool in, size_t at, int8_t* q, uint8_t* e) {
   uint2 out;
-  const uint32_t ex = act8_quantise8(v, &out);
+  float f[8];
+  v.to_float(f);
+  const uint32_t ex = act8_quantise8(f, mult, &out);
   if (in) {
     *reinterpret_cast<uint2*>(q + at) = out;
     if ((at & 31) == 0) e[at >> 5] = static_cast<uint8_t>(ex);
@@ -132,7 +119,8 @@ __device__ __forceinline__ void keep8(const float (&v)[8], bool in, size_t at, i
 constexpr int kFwdWarps = 4;  // warps per block where a row takes one warp
 
 template <int CH, bool MULTI, bool F32, bool KEEP8>
-__global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const BlockNormFwdArgs a) {
+__global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? 2 : 6)
+    block_norm_fwd_kernel(const BlockNormFwdArgs a) {
   __shared__ float words[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = MULTI ? blockDim.x >> 5 : 1;
@@ -141,7 +129,6 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const
   const int row = MULTI ? blockIdx.x : blockIdx.x * kFwdWarps + warp;
   if (row >= a.N) return;
   const int n_vec = a.d >> 3;
-  const float inv_d = 1.0f / static_cast<float>(a.d);
   const size_t base = static_cast<size_t>(row) * a.d;
   int slot = 0;
 
@@ -159,69 +146,64 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128) block_norm_fwd_kernel(const
   }
   float rstd_y = 1.0f;
   if (a.w_post) {
-    float ss = 0.0f;
+    uint64_t sum = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float f[8];
-      bf16x8_to_float(yr[c], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+      Vec8 f;
+      f.from_bf16(yr[c]);
+      f.squares(sum);
     }
-    ss = team_sum<MULTI>(ss, words, W, team, wt, lane, slot);
-    rstd_y = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
+    const float ss = team_sum<MULTI>(f2_sum(sum), words, W, team, wt, lane, slot);
+    rstd_y = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
     if (t == 0) a.rstd_post[row] = rstd_y;
   }
-  float xf[CH][8];
-  float ss = 0.0f;
+  Vec8 x[CH];
+  uint64_t sum = 0;
   const size_t gate_row = a.gate ? static_cast<size_t>(row / a.rows_per_gate) * a.d : 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int v = c * W * 32 + t;
     const bool in = v < n_vec;
-    xr[c].get(xf[c]);
+    xr[c].get(x[c]);
     if (a.y) {
-      float z[8];
-      bf16x8_to_float(yr[c], z);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] *= rstd_y;
-      if constexpr (KEEP8) keep8(z, in, base + v * 8, a.yhat_q, a.yhat_e);
+      Vec8 z;
+      z.from_bf16(yr[c]);
+      if constexpr (KEEP8) keep8(z, rstd_y, in, base + v * 8, a.yhat_q, a.yhat_e);
       if (in) {
         if (a.w_post) {
-          float w[8];
-          load_f32x8(a.w_post + v * 8, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] *= w[i];
+          Vec8 w;
+          w.from_f32(a.w_post + v * 8);
+          z.scale(rstd_y);
+          z.mul(w);
         }
         if (a.gate) {
-          float g[8], slope[8];
-          load_gate8(a.gate, gate_row + v * 8, a.gate_fp32, a.gate_sigmoid, g, slope);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] *= g[i];
+          Vec8 g;
+          load_gate(a.gate, gate_row + v * 8, a.gate_fp32, g);
+          if (a.gate_sigmoid) g.sigmoid();
+          z.mul(g);
         }
+        const uint64_t r = f2_all(a.res_scale), s = f2_all(a.block_scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xf[c][i] = fmaf(a.block_scale, z[i], a.res_scale * xf[c][i]);
-        store8<F32>(a.x_out, base + v * 8, xf[c]);
+        for (int i = 0; i < 4; ++i) x[c].p[i] = f2_fma(s, z.p[i], f2_mul(r, x[c].p[i]));
+        store8<F32>(a.x_out, base + v * 8, x[c]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(xf[c][i], xf[c][i], ss);
+    x[c].squares(sum);
   }
   if (!a.w_pre) return;
-  ss = team_sum<MULTI>(ss, words, W, team, wt, lane, slot);
-  const float rstd_x = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
+  const float ss = team_sum<MULTI>(f2_sum(sum), words, W, team, wt, lane, slot);
+  const float rstd_x = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
   if (t == 0) a.rstd_pre[row] = rstd_x;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int v = c * W * 32 + t;
     const bool in = v < n_vec;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) xf[c][i] *= rstd_x;
-    if constexpr (KEEP8) keep8(xf[c], in, base + v * 8, a.xhat_q, a.xhat_e);
+    if constexpr (KEEP8) keep8(x[c], rstd_x, in, base + v * 8, a.xhat_q, a.xhat_e);
     if (in) {
-      float w[8];
-      load_f32x8(a.w_pre + v * 8, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= xf[c][i];
+      Vec8 w;
+      w.from_f32(a.w_pre + v * 8);
+      x[c].scale(rstd_x);
+      w.mul(x[c]);
       store8<false>(a.h, base + v * 8, w);
     }
   }
@@ -327,23 +309,14 @@ __device__ __forceinline__ void block_columns(const Vec8 (&acc)[CH], float* scra
   }
 }
 
-// Eight gate values as pairs, and their slopes by the stored value.
+// Eight gate values and their slopes by the stored value.
 __device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at, Vec8& g, Vec8& slope) {
-  if (a.gate_fp32)
-    g.from_f32(static_cast<const float*>(a.gate) + at);
-  else
-    g.from_bf16(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.gate) + at));
+  load_gate(a.gate, at, a.gate_fp32, g);
   slope.fill(1.0f);
   if (a.gate_sigmoid) {
+    g.sigmoid();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x, y;
-      f2_split(g.p[i], x, y);
-      x = __fdividef(1.0f, 1.0f + __expf(-x));
-      y = __fdividef(1.0f, 1.0f + __expf(-y));
-      g.p[i] = f2_make(x, y);
-      slope.p[i] = f2_make(x * (1.0f - x), y * (1.0f - y));
-    }
+    for (int i = 0; i < 4; ++i) slope.p[i] = f2_fma(f2_mul(g.p[i], f2_all(-1.0f)), g.p[i], g.p[i]);
   }
 }
 

@@ -1227,7 +1227,7 @@ int check_flags(std::initializer_list<int> flags) {
 struct NormPtr {
   const void* p;
   bool must;
-  bool aligned;
+  int align;  // bytes
   const char* name;
 };
 int check_norm_ptrs(std::initializer_list<NormPtr> ps) {
@@ -1237,7 +1237,8 @@ int check_norm_ptrs(std::initializer_list<NormPtr> ps) {
       return fail(DETATTN_ERR_NULL, "%s is given, but what it belongs to is not", p.name);
   }
   for (const NormPtr& p : ps)
-    if (p.aligned && !aligned16(p.p)) return fail(DETATTN_ERR_ALIGN, "%s is not 16-byte aligned", p.name);
+    if (reinterpret_cast<uintptr_t>(p.p) % p.align != 0)
+      return fail(DETATTN_ERR_ALIGN, "%s is not %d-byte aligned", p.name, p.align);
   return DETATTN_OK;
 }
 
@@ -1709,7 +1710,7 @@ int swiglu_fwd(const void* u, void* h, void* u_q, void* u_e, int rows, int f, vo
   if (rows == 0) return ok_status();
   if ((rc = check_ptrs({{u, "u"}, {h, "h"}})) != DETATTN_OK) return rc;
   const bool kept = u_q != nullptr || u_e != nullptr;
-  if ((rc = check_norm_ptrs({{u_q, kept, true, "u_q"}, {u_e, kept, false, "u_e"}})) != DETATTN_OK)
+  if ((rc = check_norm_ptrs({{u_q, kept, 16, "u_q"}, {u_e, kept, 1, "u_e"}})) != DETATTN_OK)
     return rc;
   if ((rc = check_device()) != DETATTN_OK) return rc;
   return launched(launch_swiglu_fwd(u, h, static_cast<int8_t*>(u_q), static_cast<uint8_t*>(u_e),
@@ -1724,10 +1725,10 @@ int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, 
   if ((rc = check_swiglu(rows, f, kept)) != DETATTN_OK) return rc;
   if (rows == 0) return ok_status();
   if ((rc = check_ptrs({{dh, "dh"}, {du, "du"}})) != DETATTN_OK) return rc;
-  if ((rc = check_norm_ptrs({{u, !kept, true, "u"},
-                             {u_q, kept, true, "u_q"},
-                             {u_e, kept, false, "u_e"},
-                             {h, h != nullptr, true, "h"}})) != DETATTN_OK)
+  if ((rc = check_norm_ptrs({{u, !kept, 16, "u"},
+                             {u_q, kept, 16, "u_q"},
+                             {u_e, kept, 1, "u_e"},
+                             {h, h != nullptr, 16, "h"}})) != DETATTN_OK)
     return rc;
   if ((rc = check_device()) != DETATTN_OK) return rc;
   return launched(launch_swiglu_bwd(dh, u, static_cast<const int8_t*>(u_q),
@@ -1752,19 +1753,19 @@ int block_norm_fwd(const void* x, const void* y, const void* gate, const float* 
   if (N == 0) return ok_status();
   const bool block = y != nullptr, pre = w_pre != nullptr, post = w_post != nullptr;
   if (!block && !pre) return fail(DETATTN_ERR_NULL, "y and w_pre are both NULL: nothing to do");
-  if ((rc = check_norm_ptrs({{x, true, true, "x"},
-                             {y, block, true, "y"},
-                             {gate, block && gate != nullptr, true, "gate"},
-                             {w_post, block && post, true, "w_post"},
-                             {w_pre, pre, true, "w_pre"},
-                             {x_out, block, true, "x_out"},
-                             {h, pre, true, "h"},
-                             {rstd_post, post, true, "rstd_post"},
-                             {rstd_pre, pre, true, "rstd_pre"},
-                             {yhat_q, block && keep_y, true, "yhat_q"},
-                             {yhat_e, block && keep_y, false, "yhat_e"},
-                             {xhat_q, pre && keep_x, true, "xhat_q"},
-                             {xhat_e, pre && keep_x, false, "xhat_e"}})) != DETATTN_OK)
+  if ((rc = check_norm_ptrs({{x, true, 16, "x"},
+                             {y, block, 16, "y"},
+                             {gate, block && gate != nullptr, 16, "gate"},
+                             {w_post, block && post, 16, "w_post"},
+                             {w_pre, pre, 16, "w_pre"},
+                             {x_out, block, 16, "x_out"},
+                             {h, pre, 16, "h"},
+                             {rstd_post, post, 4, "rstd_post"},
+                             {rstd_pre, pre, 4, "rstd_pre"},
+                             {yhat_q, block && keep_y, 16, "yhat_q"},
+                             {yhat_e, block && keep_y, 1, "yhat_e"},
+                             {xhat_q, pre && keep_x, 16, "xhat_q"},
+                             {xhat_e, pre && keep_x, 1, "xhat_e"}})) != DETATTN_OK)
     return rc;
   if (block && pre && keep_x != keep_y)
     return fail(DETATTN_ERR_NULL, "the checkpoints of yhat and xhat are kept both or neither");
@@ -1824,27 +1825,27 @@ int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void
       return fail(DETATTN_ERR_NULL, "xhat comes from a checkpoint and yhat from a tensor: one kind for both");
     if (from_y8 && x != nullptr && pre)
       return fail(DETATTN_ERR_NULL, "yhat comes from a checkpoint and xhat from a tensor: one kind for both");
-    if ((rc = check_norm_ptrs({{dx_out, dx_out != nullptr, true, "dx_out"},
-                               {dh, pre, true, "dh"},
-                               {x, pre && !from_x8, true, "x"},
-                               {xhat_q, pre && from_x8, true, "xhat_q"},
-                               {xhat_e, pre && from_x8, false, "xhat_e"},
-                               {y, need_y && !from_y8, true, "y"},
-                               {yhat_q, need_y && from_y8, true, "yhat_q"},
-                               {yhat_e, need_y && from_y8, false, "yhat_e"},
-                               {gate, block && gated, true, "gate"},
-                               {w_post, block && post, true, "w_post"},
-                               {rstd_post, block && post, true, "rstd_post"},
-                               {rstd_pre, pre, true, "rstd_pre"},
-                               {dx, true, true, "dx"},
-                               {dgate, block && gated, true, "dgate"},
-                               {dw_post, block && post, true, "dw_post"},
-                               {dw_pre, pre, true, "dw_pre"}})) != DETATTN_OK)
+    if ((rc = check_norm_ptrs({{dx_out, dx_out != nullptr, 16, "dx_out"},
+                               {dh, pre, 16, "dh"},
+                               {x, pre && !from_x8, 16, "x"},
+                               {xhat_q, pre && from_x8, 16, "xhat_q"},
+                               {xhat_e, pre && from_x8, 1, "xhat_e"},
+                               {y, need_y && !from_y8, 16, "y"},
+                               {yhat_q, need_y && from_y8, 16, "yhat_q"},
+                               {yhat_e, need_y && from_y8, 1, "yhat_e"},
+                               {gate, block && gated, 16, "gate"},
+                               {w_post, block && post, 16, "w_post"},
+                               {rstd_post, block && post, 4, "rstd_post"},
+                               {rstd_pre, pre, 4, "rstd_pre"},
+                               {dx, true, 16, "dx"},
+                               {dgate, block && gated, 16, "dgate"},
+                               {dw_post, block && post, 16, "dw_post"},
+                               {dw_pre, pre, 16, "dw_pre"}})) != DETATTN_OK)
       return rc;
     if (!aligned16(dy)) return fail(DETATTN_ERR_ALIGN, "dy is not 16-byte aligned");
-  } else if ((rc = check_norm_ptrs({{dgate, gate != nullptr, true, "dgate"},
-                                    {dw_post, post, true, "dw_post"},
-                                    {dw_pre, pre, true, "dw_pre"}})) != DETATTN_OK) {
+  } else if ((rc = check_norm_ptrs({{dgate, gate != nullptr, 16, "dgate"},
+                                    {dw_post, post, 16, "dw_post"},
+                                    {dw_pre, pre, 16, "dw_pre"}})) != DETATTN_OK) {
     return rc;
   }
   const BlockNormBwdPlan p = block_norm_bwd_plan(N, d, G);

@@ -407,7 +407,7 @@ int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, 
  * yhat_q: y; rstd_post: w_post; h, rstd_pre, xhat_q: w_pre), and outputs named here with "(with ...)" must be given.
  * N in [0, 2^30], d a multiple of 8 (of 32 with checkpoints) in [8, 8192],
  * N * d at most 2^36.  eps > 0; the scales finite.  16-byte aligned pointers
- * (yhat_e and xhat_e need none). */
+ * (rstd_post and rstd_pre: 4-byte; yhat_e and xhat_e need no alignment). */
 int block_norm_fwd(const void* x, const void* y, const void* gate, const float* w_post,
                    const float* w_pre, void* x_out, void* h, float* rstd_post, float* rstd_pre,
                    void* yhat_q, void* yhat_e, void* xhat_q, void* xhat_e, int N, int d, int G,

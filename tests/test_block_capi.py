@@ -177,3 +177,10 @@ def test_binding_refuses_cpu_tensors_and_wrong_kinds(L):
         da.act8_wgrad(da.Act8(torch.zeros((4, 64), dtype=torch.int8), torch.zeros((4, 2), dtype=torch.uint8)), x)
     with pytest.raises(ValueError, match="no gradient"):
         da.block_norm_bwd(None, None, da.BlockNormKept())
+
+
+def test_statistics_need_four_byte_alignment(L):
+    assert _fwd(L, rstd_pre=ctypes.c_void_p(0x10002)) == -2
+    assert _bwd(L, rstd_post=ctypes.c_void_p(0x10001)) == -2
+    if not torch.cuda.is_available():
+        assert _fwd(L, rstd_pre=ctypes.c_void_p(0x10004)) == -6
