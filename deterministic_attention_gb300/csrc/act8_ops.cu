@@ -50,19 +50,34 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Unpack: sixteen values (half a group) per thread.
+// Unpack: likewise, kUnpackVecs vectors of eight per thread.  (Sixteen values
+// per thread, loaded as one 16-byte word, leave a warp's stores 32 bytes
+// apart: 8192 x 4096 took 18.1 us against 13.2.)
+constexpr int kUnpackVecs = 4;
 __global__ void __launch_bounds__(kThreads)
-    act8_unpack_kernel(const uint4* __restrict__ q, const uint8_t* __restrict__ e,
-                       uint4* __restrict__ x, long n_half) {
-  const long v = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (v >= n_half) return;
-  const uint4 raw = q[v];
-  const float s = act8_scale(e[v >> 1]);
-  float f[8];
-  act8_values8(make_uint2(raw.x, raw.y), s, f);
-  x[2 * v] = float_to_bf16x8(f);
-  act8_values8(make_uint2(raw.z, raw.w), s, f);
-  x[2 * v + 1] = float_to_bf16x8(f);
+    act8_unpack_kernel(const uint2* __restrict__ q, const uint8_t* __restrict__ e,
+                       uint4* __restrict__ x, long n_vec) {
+  const long v0 = static_cast<long>(blockIdx.x) * (kThreads * kUnpackVecs) + threadIdx.x;
+  uint2 raw[kUnpackVecs];
+  uint32_t ex[kUnpackVecs];
+#pragma unroll
+  for (int j = 0; j < kUnpackVecs; ++j) {
+    const long v = v0 + j * kThreads;
+    if (v < n_vec) {
+      raw[j] = q[v];
+      ex[j] = e[v >> 2];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kUnpackVecs; ++j) {
+    const long v = v0 + j * kThreads;
+    if (v < n_vec) {
+      Vec8 f;
+      f.from_int8(raw[j]);
+      f.scale(act8_scale(ex[j]));
+      x[v] = f.to_bf16();
+    }
+  }
 }
 
 // sigma(a); exp of a large -a is infinity and gives 0.
@@ -146,9 +161,9 @@ cudaError_t launch_act8_pack(const void* x, int8_t* q, uint8_t* e, long rows, in
 
 cudaError_t launch_act8_unpack(const int8_t* q, const uint8_t* e, void* x, long rows, int d,
                                cudaStream_t st) {
-  const long n_half = rows * (d / 16);
-  act8_unpack_kernel<<<blocks_of(n_half, kThreads), kThreads, 0, st>>>(
-      reinterpret_cast<const uint4*>(q), e, static_cast<uint4*>(x), n_half);
+  const long n_vec = rows * (d / 8);
+  act8_unpack_kernel<<<blocks_of(n_vec, kThreads * kUnpackVecs), kThreads, 0, st>>>(
+      reinterpret_cast<const uint2*>(q), e, static_cast<uint4*>(x), n_vec);
   return cudaGetLastError();
 }
 

@@ -126,8 +126,8 @@ __device__ __forceinline__ Unit unit_at(const Act8WgradArgs& a, int u) {
   } else {
     const int r = u - a.whole_tiles, z = r % a.splits;
     w.tile = a.whole_tiles + r / a.splits;
-    w.kb0 = static_cast<int>(static_cast<long>(n_k) * z / a.splits);
-    w.kb1 = static_cast<int>(static_cast<long>(n_k) * (z + 1) / a.splits);
+    w.kb0 = n_k * z / a.splits;  // (n_k is at most 2^18, splits 32)
+    w.kb1 = n_k * (z + 1) / a.splits;
     w.part = a.splits > 1 ? r : -1;
   }
   return w;

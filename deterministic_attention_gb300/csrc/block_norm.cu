@@ -119,7 +119,7 @@ __device__ __forceinline__ void keep8(const Vec8& v, float mult, bool in, size_t
 constexpr int kFwdWarps = 4;  // warps per block where a row takes one warp
 
 template <int CH, bool MULTI, bool F32, bool KEEP8>
-__global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? 2 : 6)
+__global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? (CH == 3 ? 4 : 3) : 6)
     block_norm_fwd_kernel(const BlockNormFwdArgs a) {
   __shared__ float words[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
