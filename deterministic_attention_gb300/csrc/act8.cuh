@@ -50,11 +50,18 @@ __device__ __forceinline__ uint32_t act8_quantise8(const float (&v)[8], float mu
   }
   // x 2^-k + 1.5 2^23: the sum's low byte is the rounded value in two's
   // complement.
-  const float inv = __uint_as_float((254u - e) << 23) * mult;
+  const float inv = __uint_as_float((254u - e) << 23);
   float r[8];
   uint32_t b[8];
+  if (e >= 64u && mult < 0x1p60f) {
+    const float k = inv * mult;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = fmaf(v[i], inv, 12582912.0f);
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(v[i], k, 12582912.0f);
+  } else {
+    // Groups of (near) zeros, where 2^-k mult may pass the largest float.
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(v[i] * mult, inv, 12582912.0f);
+  }
   // k = 122: 64 2^122 would be infinity, so what rounds there stays at 63.
   if (e == 249u) {
 #pragma unroll

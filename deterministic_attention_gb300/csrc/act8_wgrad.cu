@@ -512,15 +512,18 @@ Act8WgradPlan act8_wgrad_plan(int rows, int d, int n) {
   const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n;
   p.whole_tiles = static_cast<int>(tiles / kWgradPairs * kWgradPairs);
   const int rem = static_cast<int>(tiles - p.whole_tiles);
-  // The cut that leaves the busiest pair the fewest steps, a range costing
-  // about two steps of its own (writing the partial tile and adding it up).
+  // The cut that leaves the busiest pair the fewest steps.  Cutting at all
+  // costs about twelve (the partial tiles written and added up, a second
+  // launch): 1000 x 768 x 1280 takes 17.5 us a call cut in five and 16.4
+  // whole, 500 rows 17.0 and 12.7; 1777 x 1184 x 1000 17.1 cut in three and
+  // 20.5 whole.
   const int n_k = (rows + kWgradBK - 1) / kWgradBK;
   p.splits = 1;
   if (rem == 0) return p;
   double best = 0.0;
   for (int s = 1; s <= 32 && s <= n_k; ++s) {
     const int rounds = (rem * s + kWgradPairs - 1) / kWgradPairs;
-    const double cost = rounds * (static_cast<double>((n_k + s - 1) / s) + (s > 1 ? 4.0 : 0.0));
+    const double cost = rounds * (static_cast<double>((n_k + s - 1) / s) + (s > 1 ? 12.0 : 0.0));
     if (s == 1 || cost < best) {
       best = cost;
       p.splits = s;

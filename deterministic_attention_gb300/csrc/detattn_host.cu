@@ -1254,7 +1254,7 @@ NormLayout norm_layout(const BlockNormBwdPlan& p, int d) {
   l.pre = 0;
   l.post = up(row * p.blocks);
   l.gate = l.post + up(row * p.blocks);
-  l.total = l.gate + up(row * p.items);
+  l.total = l.gate + (p.gate_parts ? up(row * p.items) : 0);
   return l;
 }
 

@@ -158,6 +158,8 @@ def test_block_norm_workspace(L):
     assert L.block_norm_bwd_workspace_bytes(4096, 768, 1) == 3 * up(152 * 768 * 4)
     assert L.block_norm_bwd_workspace_bytes(0, 768, 1) == 0
     assert L.block_norm_bwd_workspace_bytes(8, 768, 3) == 0
+    # A gate row for every two rows: each is one block's, no parts to add up.
+    assert L.block_norm_bwd_workspace_bytes(1 << 20, 256, 1 << 19) == 2 * up(152 * 256 * 4)
     # 32 sequences: 19 slices each.
     assert L.block_norm_bwd_workspace_bytes(32768, 1536, 32) == 2 * up(152 * 1536 * 4) + up(608 * 1536 * 4)
 

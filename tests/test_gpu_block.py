@@ -114,7 +114,7 @@ def test_act8_empty():
     (1, 32, 8), (63, 64, 256), (64, 128, 264), (65, 160, 8), (500, 96, 1000), (1777, 1184, 504),
     (4096, 768, 1280),       # every tile cut
     (192, 19 * 256, 4 * 256),  # exactly one whole tile for each pair of blocks, nothing cut
-    (700, 2496, 2200),       # whole tiles and cut ones, ragged both ways
+    (2500, 2496, 2200),      # whole tiles and cut ones, ragged both ways
     (200, 2432, 5000),       # a pair walks several whole tiles
     (2600, 4864, 1024),      # a whole tile takes its tokens in three runs
 ])
@@ -145,7 +145,7 @@ def test_wgrad_plan_cases_are_what_they_say():
     """The shapes above reach whole tiles only, cut tiles only, and both."""
     assert da.act8_wgrad_workspace_bytes(192, 19 * 256, 4 * 256) == 0
     assert da.act8_wgrad_workspace_bytes(4096, 768, 1280) == 15 * 5 * 256 * 256 * 4
-    assert da.act8_wgrad_workspace_bytes(700, 2496, 2200) % (14 * 256 * 256 * 4) == 0
+    assert da.act8_wgrad_workspace_bytes(2500, 2496, 2200) == 14 * 5 * 256 * 256 * 4
 
 
 @pytest.mark.gpu
@@ -425,6 +425,40 @@ def test_block_norm_rows_do_not_touch_each_other():
     for a, b in ((grads.dx, ref.dx), (grads.dy, ref.dy), (grads.dgate, ref.dgate)):
         assert torch.equal(a[rest], b[rest])
     assert grads.dx[5].isnan().all() and grads.dw_pre.isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_block_norm_rows_of_zeros_and_tiny_values(stream):
+    """Padding rows: everything they give is zero, in their checkpoints too
+    (1 / rms is then 1 / sqrt(eps)); groups far below 1 keep their values."""
+    i = _norm_inputs(12, 256, (1, F32), True, True, stream, 43)
+    i["x"][3:6], i["y"][3:6] = 0, 0
+    i["x"][7, 64:128] = 2.0 ** -100
+    i["y"][7, 64:128] = -(2.0 ** -120)
+    i["x"][9], i["y"][9] = 2.0 ** -110, 2.0 ** -126
+    c = _cuda(i)
+    kw = dict(gate=c["gate"], w_post=c["w_post"], w_pre=c["w_pre"])
+    x_out, h, kept = da.block_norm_fwd(c["x"], c["y"], eps=EPS, keep8=True, **kw)
+    o = ob.norm_fwd(_np(i["x"]), _np(i["y"]), _np(i["gate"]), _np(i["w_post"]), _np(i["w_pre"]), eps=EPS)
+    _check_kept("yhat", kept.yhat8, o["yhat"])
+    _check_kept("xhat", kept.xhat8, o["xhat"])
+    for t in (x_out, h, kept.xhat8.q, kept.yhat8.q):
+        assert not t[3:6].any()
+    assert (kept.xhat8.e[3:6] == 1).all() and (kept.yhat8.e[3:6] == 1).all()
+    kw = dict(gate=c["gate"], w_post=c["w_post"], w_pre=c["w_pre"])
+    _check_bwd(da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw), _bwd_refs(i, kept, 1.0, 1.0, False), 12)
+
+
+@pytest.mark.gpu
+def test_block_norm_smallest_eps():
+    """1 / sqrt(eps) near the largest fp32 powers: a row of zeros stays zero."""
+    x = torch.zeros((2, 64), dtype=BF, device="cuda")
+    x[1] = 1.0
+    _, h, kept = da.block_norm_fwd(x, w_pre=torch.ones(64, device="cuda"), eps=1e-44, keep8=True)
+    assert not h[0].any() and not kept.xhat8.q[0].any() and (kept.xhat8.e[0] == 1).all()
+    assert torch.equal(h[1].float(), torch.ones(64, device="cuda"))
+    assert torch.equal(da.act8_unpack(kept.xhat8)[1], h[1])
 
 
 # ------------------------------------------------------------ identity, streams, graphs
