@@ -115,6 +115,27 @@ __device__ __forceinline__ void keep8(const Vec8& v, float mult, bool in, size_t
   }
 }
 
+// Three sums at once.
+template <bool MULTI>
+__device__ __forceinline__ void team_sum3(float (&v)[3], float* words, int W, int team, int warp_in_team,
+                                          int lane, int& slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  if constexpr (MULTI) {
+    float* w = words + slot * 48 + team * W * 3;
+    if (lane < 3) w[warp_in_team * 3 + lane] = lane == 0 ? v[0] : lane == 1 ? v[1] : v[2];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory");
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      v[k] = 0.0f;
+      for (int i = 0; i < W; ++i) v[k] += w[i * 3 + k];
+    }
+    slot ^= 1;
+  }
+}
+
 // ------------------------------------------------------------ forward
 constexpr int kFwdWarps = 4;  // warps per block where a row takes one warp
 
@@ -217,12 +238,15 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? (CH == 3 ? 4 : 3) :
 // hold the column sums.  The exponent bytes of the checkpoints (rows of d / 32
 // bytes, not a multiple of 16) come by plain loads a row ahead.
 // Warps in row teams (one more fills the rings) by the vectors of eight
-// columns that a thread holds: with three, 11 warps' registers fit; with two, 15.
-constexpr int bwd_warps(int ch, bool multi) { return multi && ch == 2 ? 15 : 11; }
+// columns that a thread holds: with three, 11 warps' registers fit; with two, 15,
+// unless a gate of each row's own takes registers too.
+constexpr int bwd_warps(int ch, bool multi, bool row_gate) {
+  return multi && ch == 2 && !row_gate ? 15 : 11;
+}
 constexpr int kBwdMaxTeams = 11;
 constexpr int kBwdBlocks = 152;     // one block per SM of the GB300
 constexpr int kBwdMaxStages = 4;
-constexpr int kBwdSmem = 226 * 1024;  // dynamic shared memory at most (1 KB is left for the static part)
+constexpr int kBwdSmem = 225 * 1024;  // dynamic shared memory at most (2 KB are left for the static part)
 
 // Where the pieces of a row lie in a stage, and the ring's shape.
 struct BwdRing {
@@ -320,14 +344,22 @@ __device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at,
   }
 }
 
-// FULL: every input is there and no gate of its own for every row (the flags
-// below are then known to the compiler).
-template <int CH, bool MULTI, bool F32, bool FROM8, bool FULL>
-__global__ void __launch_bounds__((bwd_warps(CH, MULTI) + 1) * 32, 1)
+// Eight gate values of a row's own gate.
+__device__ __forceinline__ void row_gate(const BlockNormBwdArgs& a, size_t at, Vec8& g) {
+  load_gate(a.gate, at, a.gate_fp32, g);
+  if (a.gate_sigmoid) g.sigmoid();
+}
+
+// What the compiler knows of a call: that every input is there and no row has
+// a gate of its own; only the latter; that every row has one.
+enum BwdMode { kBwdFull, kBwdPlain, kBwdRowGate };
+template <int CH, bool MULTI, bool F32, bool FROM8, BwdMode MODE>
+__global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1) * 32, 1)
     block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float words[64];
+  __shared__ float words[96];
   __shared__ __align__(8) uint64_t bars[2 * kBwdMaxTeams * kBwdMaxStages];  // full, empty
+  constexpr bool FULL = MODE == kBwdFull, per_row_gate = MODE == kBwdRowGate;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = MULTI ? ring.W : 1;
   const int teams = ring.teams, team_threads = teams * W * 32;
@@ -336,10 +368,9 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI) + 1) * 32, 1)
   const bool pre = FULL || a.dh != nullptr;
   const bool with_dx = FULL || a.dx_out != nullptr;
   const bool post = FULL || a.w_post != nullptr;
-  const bool per_row_gate = !FULL && a.gate != nullptr && a.rows_per_gate == 1;
-  const bool sum_gate = a.gate != nullptr && !per_row_gate;
-  const bool with_dy = FULL || a.dy != nullptr;
-  const bool need_y = FULL || (with_dy && (post || a.gate != nullptr));
+  const bool sum_gate = !per_row_gate && a.gate != nullptr;
+  const bool with_dy = FULL || per_row_gate || a.dy != nullptr;
+  const bool need_y = FULL || per_row_gate || (with_dy && (post || a.gate != nullptr));
   constexpr int kX = F32 ? 4 : 2;
   float* cols = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);  // [d]
   auto full = [&](int team, int s) { return smem_u32(&bars[team * kBwdMaxStages + s]); };
@@ -508,111 +539,117 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI) + 1) * 32, 1)
       };
       auto scale_x = [&](int c) { return FROM8 ? act8_scale(m.e[c] & 255u) : m.rx; };
       auto scale_y = [&](int c) { return FROM8 ? act8_scale(m.e[c] >> 8) : m.ry; };
-      Vec8 keep[CH];  // dh w_pre, then D g w_post
-      float s1 = 0.0f;
-      if (pre) {
+      // D = p - x k1, p = dx' + rstd dh w_pre, needs a sum over the row, and
+      // dy one over D; but with D the second is linear in k1:
+      //   sum D gw y = sum p gw y - k1 sum x gw y
+      // so that all sums come from one pass and one exchange.
+      Vec8 keep[CH];  // p
+      float sums[3] = {0.0f, 0.0f, 0.0f};  // dh w_pre xhat; p gw yhat; xhat gw yhat
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int v = c * W * 32 + t;
-          if (v < n_vec) {
-            Vec8 dh, x, w;
+      for (int c = 0; c < CH; ++c) {
+        const int v = c * W * 32 + t;
+        if (v < n_vec) {
+          if (!with_dx)
+            keep[c].fill(0.0f);
+          else if constexpr (F32)
+            keep[c].from_f32(st + ring.off_d + v * 32);
+          else
+            keep[c].from_bf16(*reinterpret_cast<const uint4*>(st + ring.off_d + v * 16));
+          Vec8 x;
+          if (pre) {
+            Vec8 dh, w;
             dh.from_bf16(*reinterpret_cast<const uint4*>(st + v * 16));
             raw_x(v, x);
             w.from_f32(a.w_pre + v * 8);
-            const uint64_t sc = f2_all(scale_x(c));
+            const uint64_t sc = f2_all(scale_x(c)), rx = f2_all(m.rx);
             uint64_t part = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              keep[c].p[i] = f2_mul(dh.p[i], w.p[i]);
+              const uint64_t q = f2_mul(dh.p[i], w.p[i]);
               acc_pre[c].p[i] = f2_fma(f2_mul(dh.p[i], x.p[i]), sc, acc_pre[c].p[i]);
-              part = f2_fma(keep[c].p[i], x.p[i], part);
+              part = f2_fma(q, x.p[i], part);
+              keep[c].p[i] = f2_fma(q, rx, keep[c].p[i]);
             }
-            s1 = fmaf(f2_sum(part), scale_x(c), s1);
+            sums[0] = fmaf(f2_sum(part), scale_x(c), sums[0]);
+          }
+          if (post) {
+            Vec8 gw, f;
+            gw.from_f32(cols + v * 8);
+            raw_y(v, f);
+            gw.mul(f);
+            if constexpr (per_row_gate) {
+              row_gate(a, base + v * 8, f);
+              gw.mul(f);
+            }
+            uint64_t part = 0, cross = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              part = f2_fma(keep[c].p[i], gw.p[i], part);
+              if (pre) cross = f2_fma(x.p[i], gw.p[i], cross);
+            }
+            sums[1] = fmaf(f2_sum(part), scale_y(c), sums[1]);
+            if (pre) sums[2] = fmaf(f2_sum(cross), scale_x(c) * scale_y(c), sums[2]);
           }
         }
-        s1 = team_sum<MULTI>(s1, words, W, team, wt, lane, slot) * inv_d;
       }
-      float s2 = 0.0f;
+      if (pre || post) team_sum3<MULTI>(sums, words, W, team, wt, lane, slot);
+      const float kx = -m.rx * sums[0] * inv_d;  // D = p + kx xhat
+      const float ky = -m.ry * a.block_scale * inv_d * (pre ? fmaf(kx, sums[2], sums[1]) : sums[1]);
+      const float kd = (post ? m.ry : 1.0f) * a.block_scale;  // dy = kd D gw + ky yhat
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int v = c * W * 32 + t;
         if (v < n_vec) {
           const size_t at = base + v * 8;
-          Vec8 D;
-          if (!with_dx)
-            D.fill(0.0f);
-          else if constexpr (F32)
-            D.from_f32(st + ring.off_d + v * 32);
-          else
-            D.from_bf16(*reinterpret_cast<const uint4*>(st + ring.off_d + v * 16));
           if (pre) {
             Vec8 x;
             raw_x(v, x);
-            const uint64_t rx = f2_all(m.rx), k = f2_all(-m.rx * s1 * scale_x(c));
+            const uint64_t k = f2_all(kx * scale_x(c));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) D.p[i] = f2_fma(keep[c].p[i], rx, f2_fma(x.p[i], k, D.p[i]));
+            for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_fma(x.p[i], k, keep[c].p[i]);
           }
-          Vec8 o;
-          const uint64_t r = f2_all(a.res_scale);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o.p[i] = f2_mul(r, D.p[i]);
-          if constexpr (F32)
-            o.to_f32(static_cast<float*>(a.dx) + at);
-          else
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dx) + at) = o.to_bf16();
-          if (need_y) {
-            Vec8 y, e, gw;
-            raw_y(v, y);
-            gw.from_f32(cols + v * 8);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e.p[i] = f2_mul(D.p[i], y.p[i]);
-            if (per_row_gate) {
-              Vec8 g, slope;
-              gate_pairs(a, at, g, slope);
-              const uint64_t k = f2_all(a.block_scale * scale_y(c));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                slope.p[i] = f2_mul(f2_mul(slope.p[i], gw.p[i]), f2_mul(e.p[i], k));
-                e.p[i] = f2_mul(e.p[i], g.p[i]);
-                gw.p[i] = f2_mul(gw.p[i], g.p[i]);
-              }
-              if (a.gate_fp32)
-                slope.to_f32(static_cast<float*>(a.dgate) + at);
-              else
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dgate) + at) = slope.to_bf16();
-            }
-            const uint64_t sc = f2_all(scale_y(c));
-            uint64_t part = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc_y[c].p[i] = f2_fma(e.p[i], sc, acc_y[c].p[i]);
-              keep[c].p[i] = f2_mul(D.p[i], gw.p[i]);
-              part = f2_fma(keep[c].p[i], y.p[i], part);
-            }
-            s2 = fmaf(f2_sum(part), scale_y(c), s2);
-          } else {
-            keep[c] = D;
-          }
-        }
-      }
-      if (with_dy) {
-        float k2 = 0.0f;
-        if (post) k2 = -m.ry * a.block_scale * (team_sum<MULTI>(s2, words, W, team, wt, lane, slot) * inv_d);
-        const uint64_t k1 = f2_all((post ? m.ry : 1.0f) * a.block_scale);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int v = c * W * 32 + t;
-          if (v < n_vec) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_mul(keep[c].p[i], k1);
-            if (post) {
-              Vec8 y;
+          Vec8 o = keep[c];
+          o.scale(a.res_scale);
+          store8<F32>(a.dx, at, o);
+          if (with_dy) {
+            if (need_y) {
+              Vec8 y, e, gw;
               raw_y(v, y);
-              const uint64_t k = f2_all(k2 * scale_y(c));
+              gw.from_f32(cols + v * 8);
+              e = keep[c];
+              e.mul(y);
+              keep[c].scale(kd);
+              keep[c].mul(gw);
+              if constexpr (per_row_gate) {
+                // dgate = block_scale D yhat w_post slope, slope = 1 or g - g^2.
+                Vec8 g;
+                row_gate(a, at, g);
+                gw.mul(e);
+                gw.scale(a.block_scale * scale_y(c));
+                e.mul(g);
+                keep[c].mul(g);
+                if (a.gate_sigmoid) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_fma(y.p[i], k, keep[c].p[i]);
+                  for (int i = 0; i < 4; ++i)
+                    gw.p[i] = f2_mul(gw.p[i], f2_fma(f2_mul(g.p[i], f2_all(-1.0f)), g.p[i], g.p[i]));
+                }
+                if (a.gate_fp32)
+                  store8<true>(a.dgate, at, gw);
+                else
+                  store8<false>(a.dgate, at, gw);
+              }
+              const uint64_t sc = f2_all(scale_y(c));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc_y[c].p[i] = f2_fma(e.p[i], sc, acc_y[c].p[i]);
+              if (post) {
+                const uint64_t k = f2_all(ky * scale_y(c));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) keep[c].p[i] = f2_fma(y.p[i], k, keep[c].p[i]);
+              }
+            } else {
+              keep[c].scale(kd);
             }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dy) + base + v * 8) = keep[c].to_bf16();
+            store8<false>(a.dy, at, keep[c]);
           }
         }
       }
@@ -743,10 +780,10 @@ cudaError_t fwd_of(const BlockNormFwdArgs& a, bool f32, int W, cudaStream_t st) 
   return cudaGetLastError();
 }
 
-template <int CH, bool MULTI, bool F32, bool FROM8, bool FULL>
-cudaError_t bwd_full(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
+template <int CH, bool MULTI, bool F32, bool FROM8, BwdMode MODE>
+cudaError_t bwd_mode(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   static unsigned long long attr_ctx[64] = {};
-  auto kernel = block_norm_bwd_kernel<CH, MULTI, F32, FROM8, FULL>;
+  auto kernel = block_norm_bwd_kernel<CH, MULTI, F32, FROM8, MODE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -765,7 +802,7 @@ cudaError_t bwd_full(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   r.off_y = r.off_x + (pre ? (FROM8 ? 1 : x_bytes) * a.d : 0);
   r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
   r.W = W;
-  r.teams = bwd_warps(CH, MULTI) / W;
+  r.teams = bwd_warps(CH, MULTI, MODE == kBwdRowGate) / W;
   while (r.teams > 1 && r.teams * 2 * r.bytes + 4 * a.d > kBwdSmem) --r.teams;
   r.stages = 2;
   while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + 4 * a.d <= kBwdSmem)
@@ -777,10 +814,11 @@ cudaError_t bwd_full(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
 
 template <int CH, bool MULTI, bool F32, bool FROM8>
 cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
-  const bool full = a.dh != nullptr && a.dx_out != nullptr && a.dy != nullptr && a.w_post != nullptr &&
-                    (a.gate == nullptr || a.rows_per_gate > 1);
-  return full ? bwd_full<CH, MULTI, F32, FROM8, true>(a, W, st)
-              : bwd_full<CH, MULTI, F32, FROM8, false>(a, W, st);
+  if (a.gate != nullptr && a.rows_per_gate == 1)
+    return bwd_mode<CH, MULTI, F32, FROM8, kBwdRowGate>(a, W, st);
+  if (a.dh != nullptr && a.dx_out != nullptr && a.dy != nullptr && a.w_post != nullptr)
+    return bwd_mode<CH, MULTI, F32, FROM8, kBwdFull>(a, W, st);
+  return bwd_mode<CH, MULTI, F32, FROM8, kBwdPlain>(a, W, st);
 }
 
 template <int CH, bool MULTI>
@@ -815,11 +853,11 @@ namespace {
 struct BwdShape {
   int W, ch;
 };
-BwdShape bwd_shape(int d) {
+BwdShape bwd_shape(int d, bool row_gate) {
   if (d <= 768) return {1, (d + 255) / 256};
   const int w3 = (d + 767) / 768, w2 = (d + 511) / 512;
-  if (w2 <= bwd_warps(2, true) && bwd_warps(2, true) / w2 * w2 > bwd_warps(3, true) / w3 * w3)
-    return {w2, 2};
+  const int n3 = bwd_warps(3, true, row_gate), n2 = bwd_warps(2, true, row_gate);
+  if (w2 <= n2 && n2 / w2 * w2 > n3 / w3 * w3) return {w2, 2};
   return {w3, 3};
 }
 
@@ -827,8 +865,8 @@ BwdShape bwd_shape(int d) {
 
 BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
   BlockNormBwdPlan p{};
-  const BwdShape sh = bwd_shape(d);
-  const int teams = bwd_warps(sh.ch, sh.W > 1) / sh.W;
+  const BwdShape sh = bwd_shape(d, false);
+  const int teams = bwd_warps(sh.ch, sh.W > 1, false) / sh.W;
   const bool shared = G > 1 && G < N;
   if (!shared) {
     const int want = (N + teams - 1) / teams;
@@ -850,7 +888,7 @@ BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool x_fp32, cudaStream_t st) {
-  const auto [W, ch] = bwd_shape(a.d);
+  const auto [W, ch] = bwd_shape(a.d, a.gate != nullptr && a.rows_per_gate == 1);
   cudaError_t e;
   if (W == 1)
     e = ch == 1   ? bwd_of<1, false>(a, x_fp32, W, st)
