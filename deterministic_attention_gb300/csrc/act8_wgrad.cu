@@ -93,8 +93,21 @@ __device__ __forceinline__ void gave_up() { atomicOr(&g_wgrad_status, 1u); }
 // m and 0xC300 | s << 7), and every step is exact.  (Ten ALU instructions
 // for eight values; through fp32 and its packing conversion it takes
 // fourteen, and the ALU is what these warps wait for.)
-__device__ __forceinline__ uint32_t bf16x2_of_bytes(uint32_t x, uint32_t scale) {
-  const uint32_t m = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0xC300C300u;
+// The masks are held in registers: an instruction takes one of them as an
+// immediate, and the compiler otherwise makes two of each.
+struct ByteMasks {
+  uint32_t low = 0x007F007Fu, m = 0x43004300u, sign = 0x00800080u, c = 0xC300C300u;
+  __device__ __forceinline__ ByteMasks() {
+    asm volatile("" : "+r"(low), "+r"(m), "+r"(sign), "+r"(c));
+  }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_of_bytes(uint32_t x, uint32_t scale, const ByteMasks& k) {
+  const uint32_t m = and_or(x, k.low, k.m), c = and_or(x, k.sign, k.c);
   uint32_t r;
   asm("{\n\t.reg .b32 t;\n\t"
       "add.rn.bf16x2 t, %1, %2;\n\t"
@@ -345,6 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t e[kAhead][kRows];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(e[i]);
+    const ByteMasks masks;
     const int total = total_steps(a, pair, pairs);
     Ring rr, ra;
     for (int i = 0; i < group; ++i) {
@@ -376,8 +390,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t sc;
               asm volatile("mul.lo.u32 %0, %1, 0x00800080;" : "=r"(sc) : "r"(e[h][i0 + i]));
               st_shared_u4(out + kRowStep * (i0 + i) * 128,
-                           make_uint4(bf16x2_of_bytes(q[i].x, sc), bf16x2_of_bytes(q[i].x >> 8, sc),
-                                      bf16x2_of_bytes(q[i].y, sc), bf16x2_of_bytes(q[i].y >> 8, sc)));
+                           make_uint4(bf16x2_of_bytes(q[i].x, sc, masks), bf16x2_of_bytes(q[i].x >> 8, sc, masks),
+                                      bf16x2_of_bytes(q[i].y, sc, masks), bf16x2_of_bytes(q[i].y >> 8, sc, masks)));
             }
           }
           fetch(e[h]);
