@@ -33,6 +33,7 @@
 // ranges in ascending order.  Every element's sum has one fixed order.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "act8.cuh"
@@ -319,45 +320,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cw = warp - kCtrlWarps, group = cw / kGroupWarps, j = lane & 15;
     const int r0 = (cw % kGroupWarps) * 2 + (lane >> 4);
     constexpr int kRowStep = 2 * kGroupWarps, kRows = kWgradBK / kRowStep;  // eight rows per thread
-    constexpr int kAhead = 1;  // of its steps that a group fetches exponents ahead
-    const int groups = a.d / kAct8Group;
-    // The exponents' cursor: the step whose bytes are fetched next.
+    const uint32_t groups = a.d / kAct8Group;
+    // The exponents' cursor: the step whose bytes are fetched next, which is
+    // the group's own next one (three steps before it is turned).
     int fu = pair, fkb = 0, fend = 0;
     const uint8_t* fat = a.e;
     auto open = [&]() {
-      if (fu >= n_units) return;
+      if (fu >= n_units) {  // past the last: what is fetched is not used
+        fkb = 0;
+        fend = INT_MAX;
+        return;
+      }
       const Unit w = unit_at(a, fu);
       int m0, n0;
       tile_origin(a, w.tile, &m0, &n0);
       // Columns past the checkpoint's last group read as zero; any exponent
       // byte that exists will do for them, as for rows past the last.
-      fat = a.e + min((m0 + rank * kHalfM) / kAct8Group + (j >> 2), groups - 1);
+      fat = a.e + min(static_cast<uint32_t>((m0 + rank * kHalfM) / kAct8Group + (j >> 2)), groups - 1);
       fkb = w.kb0;
       fend = w.kb1;
     };
-    auto step = [&]() {
-      if (++fkb >= fend) {
+    auto skip = [&](int n) {
+      fkb += n;
+      while (fkb >= fend) {
+        const int over = fkb - fend;
         fu += pairs;
         open();
+        fkb += over;
       }
     };
+    // Volatile: the loads are issued here and waited for where the bytes are
+    // used.
     auto fetch = [&](uint32_t (&e)[kRows]) {
-      if (fu >= n_units) return;
+      const int row = fkb * kWgradBK + r0;
+      if (fkb * kWgradBK + kWgradBK <= a.rows) {
+        const uint8_t* p = fat + static_cast<size_t>(row) * groups;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        asm volatile("ld.global.nc.u8 %0, [%1];"
-                     : "=r"(e[i])
-                     : "l"(fat + static_cast<size_t>(min(fkb * kWgradBK + r0 + kRowStep * i, a.rows - 1)) * groups));
+        for (int i = 0; i < kRows; ++i)
+          asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(e[i]) : "l"(p + i * kRowStep * groups));
+      } else {
 #pragma unroll
-      for (int i = 0; i < kConvGroups; ++i)
-        if (fu < n_units) step();
+        for (int i = 0; i < kRows; ++i)
+          asm volatile("ld.global.nc.u8 %0, [%1];"
+                       : "=r"(e[i])
+                       : "l"(fat + static_cast<size_t>(min(row + kRowStep * i, a.rows - 1)) * groups));
+      }
+      skip(kConvGroups);
     };
     open();
-    for (int i = 0; i < group; ++i)
-      if (fu < n_units) step();
-    uint32_t e[kAhead][kRows];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(e[i]);
+    if (group > 0) skip(group);
+    uint32_t e[kRows];
+    fetch(e);
     const ByteMasks masks;
     const int total = total_steps(a, pair, pairs);
     Ring rr, ra;
@@ -365,48 +378,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       rr.next(kRawStages);
       ra.next(kAStages);
     }
-    for (int it = group; it < total && ok; it += kConvGroups * kAhead) {
+    for (int it = group; it < total && ok; it += kConvGroups) {
+      ok = warp_all(mbar_wait_hint(bar(kBarRaw + rr.s), rr.parity, a.wait_ns));
+      if (ok && it >= kAStages)
+        ok = warp_all(mbar_wait_hint(bar(kBarAFree + ra.s), ra.parity ^ 1u, a.wait_ns));
+      const uint32_t raw = sRaw(rr.s) + r0 * 128 + j * 8;
+      const uint32_t out = sA0 + ra.s * kABytes + (j >> 3) * 8192 + r0 * 128 + (((j & 7) ^ r0) << 4);
+      // Eight rows down, the swizzle (row % 8) is the same.
 #pragma unroll
-      for (int h = 0; h < kAhead; ++h) {
-        if (it + kConvGroups * h < total && ok) {
-          ok = warp_all(mbar_wait_hint(bar(kBarRaw + rr.s), rr.parity, a.wait_ns));
-          if (ok && it + kConvGroups * h >= kAStages)
-            ok = warp_all(mbar_wait_hint(bar(kBarAFree + ra.s), ra.parity ^ 1u, a.wait_ns));
-          const uint32_t raw = sRaw(rr.s) + r0 * 128 + j * 8;
-          const uint32_t out = sA0 + ra.s * kABytes + (j >> 3) * 8192 + r0 * 128 + (((j & 7) ^ r0) << 4);
-          // Eight rows down, the swizzle (row % 8) is the same.
+      for (int i0 = 0; i0 < kRows; i0 += 4) {
+        uint2 q[4];
 #pragma unroll
-          for (int i0 = 0; i0 < kRows; i0 += 4) {
-            uint2 q[4];
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(q[i].x), "=r"(q[i].y)
+                       : "r"(raw + kRowStep * (i0 + i) * 128));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                           : "=r"(q[i].x), "=r"(q[i].y)
-                           : "r"(raw + kRowStep * (i0 + i) * 128));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // 2^(e - 127), twice.  (Volatile: formed here, not where the byte
-              // is loaded, or the load would be waited for there.)
-              uint32_t sc;
-              asm volatile("mul.lo.u32 %0, %1, 0x00800080;" : "=r"(sc) : "r"(e[h][i0 + i]));
-              st_shared_u4(out + kRowStep * (i0 + i) * 128,
-                           make_uint4(bf16x2_of_bytes(q[i].x, sc, masks), bf16x2_of_bytes(q[i].x >> 8, sc, masks),
-                                      bf16x2_of_bytes(q[i].y, sc, masks), bf16x2_of_bytes(q[i].y >> 8, sc, masks)));
-            }
-          }
-          fetch(e[h]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && ok) {
-            mbar_arrive(bar(kBarRawFree + rr.s));
-            mbar_arrive_pair(lead_bar(kBarA + ra.s));
-          }
-#pragma unroll
-          for (int k = 0; k < kConvGroups; ++k) {
-            rr.next(kRawStages);
-            ra.next(kAStages);
-          }
+        for (int i = 0; i < 4; ++i) {
+          // 2^(e - 127), twice.  (Volatile: formed here, not where the byte
+          // is loaded, or the load would be waited for there.)
+          uint32_t sc;
+          asm volatile("mul.lo.u32 %0, %1, 0x00800080;" : "=r"(sc) : "r"(e[i0 + i]));
+          st_shared_u4(out + kRowStep * (i0 + i) * 128,
+                       make_uint4(bf16x2_of_bytes(q[i].x, sc, masks), bf16x2_of_bytes(q[i].x >> 8, sc, masks),
+                                  bf16x2_of_bytes(q[i].y, sc, masks), bf16x2_of_bytes(q[i].y >> 8, sc, masks)));
         }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && ok) {
+        mbar_arrive(bar(kBarRawFree + rr.s));
+        mbar_arrive_pair(lead_bar(kBarA + ra.s));
+      }
+      fetch(e);
+#pragma unroll
+      for (int k = 0; k < kConvGroups; ++k) {
+        rr.next(kRawStages);
+        ra.next(kAStages);
       }
     }
     if (!ok) gave_up();
