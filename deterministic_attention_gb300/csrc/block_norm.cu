@@ -20,6 +20,15 @@
 // fixed columns and add their rows in ascending order in registers, the teams
 // of a block are added in team order, and a second kernel adds the blocks in
 // block order.  The deal of rows follows from the shape alone.
+//
+// Both move each tensor once and should be bound by memory.  The forward is:
+// 32768 x 1536 with an fp32 stream and a gate for every element, 705 MB, takes
+// 111 us, 6.3 TB/s or 93 % of the measured copy rate.  The backward is not
+// quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 118 us (75 %);
+// it issues 42 instructions an element, of which about half are a row's own
+// (its sums, waits and addresses), at 0.42 of the issue rate.  4096 x 768 from
+// checkpoints, 32 MB, takes 14 us with the second kernel, of which two to
+// three rows per team and the two launches' ramps are most.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

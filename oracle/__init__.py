@@ -12,7 +12,8 @@ gradient of an embedding lookup summed in ascending token order (oxide-train
 README, "The trainer is not bit-identical to itself after step 1").
 ``oracle.layer`` (numpy around the attention functions here) is one attention
 layer of a training step: QKV projection, rotary positions, attention, output
-projection, and its closed-form backward.
+projection, and its closed-form backward.  ``oracle.block`` (numpy alone) is
+what surrounds it: block norms, 8-bit activation checkpoints, the gated unit.
 
 The arithmetic lives in ``attn_oracle.c`` (plain C, fp64, OpenMP over
 independent heads); this module compiles it with gcc, loads it with ctypes and
