@@ -705,6 +705,7 @@ def block_norm_bwd(dx_out, dh, kept, gate=None, w_post=None, w_pre=None, res_sca
         _need_stream(dx_out, "dx_out", shape, dev)
         stream = dx_out.dtype
     elif kx is not None:
+        _need_stream(kx, "kept.x", shape, dev)
         stream = kx.dtype
     x = y = xq = xe = yq = ye = rp = ro = dy = dgate = dwo = dwp = None
     if w_pre is not None:

@@ -594,6 +594,57 @@ def test_two_graphs_share_a_workspace():
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows equal, bit for bit,
+    the same rows on their own."""
+    tail, d = 37, 2048
+    rows = (1 << 20) + 5
+    x = torch.zeros((rows, d), dtype=BF, device="cuda")
+    x[-tail:] = torch.randn((tail, d), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(BF)
+    end = x[-tail:].clone()
+    c, ce = da.act8_pack(x), da.act8_pack(end)
+    assert torch.equal(c.q[-tail:], ce.q) and torch.equal(c.e[-tail:], ce.e)
+    assert torch.equal(da.act8_unpack(c)[-tail:], da.act8_unpack(ce))
+    h, u8 = da.swiglu_fwd(x, keep8=True)
+    he, _ = da.swiglu_fwd(end, keep8=True)
+    assert torch.equal(h[-tail:], he) and torch.equal(u8.q[-tail:], ce.q) and torch.equal(u8.e[-tail:], ce.e)
+    for u, ue in ((x, end), (c, ce)):
+        assert torch.equal(da.swiglu_bwd(h, u)[-tail:], da.swiglu_bwd(he, ue))
+    del h, he, u8, u
+    w = torch.ones(d, device="cuda")
+    for keep8 in (False, True):
+        kw = dict(gate=w, w_post=w, w_pre=w)
+        got = da.block_norm_fwd(x, x, keep8=keep8, **kw)
+        ref = da.block_norm_fwd(end, end, keep8=keep8, **kw)
+        for a, b in zip(got[:2], ref[:2]):
+            assert torch.equal(a[-tail:], b)
+        got = da.block_norm_bwd(x, x, got[2], **kw)
+        ref = da.block_norm_bwd(end, end, ref[2], **kw)
+        for a, b in zip(got[:2], ref[:2]):
+            assert torch.equal(a[-tail:], b)
+        # Rows of zeros add nothing; the sums' order differs between the two:
+        # 37 terms and as many roundings of at most 2^-24 of the sum of magnitudes.
+        for a, b in zip(got[2:], ref[2:]):
+            assert (a - b).abs().max() <= 37 * 2.0 ** -23 * 37 * 25
+        del got, ref
+    # Whole numbers, so every order of summing gives the same bits.
+    del x
+    dy = torch.zeros((rows, 8), dtype=BF, device="cuda")
+    dy[-tail:] = torch.randint(-4, 5, (tail, 8), device="cuda").to(BF)
+    q = torch.zeros((rows, d), dtype=torch.int8, device="cuda")
+    q[-tail:] = torch.randint(-127, 128, (tail, d), device="cuda").to(torch.int8)
+    e = torch.full((rows, d // 32), 127, dtype=torch.uint8, device="cuda")
+    assert torch.equal(da.act8_wgrad(da.Act8(q, e), dy), q[-tail:].double().T.matmul(dy[-tail:].double()).float())
+    del q, e, dy, c
+    q = torch.randint(-127, 128, (40, 1 << 16), device="cuda").to(torch.int8)
+    dy = torch.randint(-4, 5, (40, (1 << 15) + 8), device="cuda").to(BF)
+    e = torch.full((40, 1 << 11), 127, dtype=torch.uint8, device="cuda")
+    dw = da.act8_wgrad(da.Act8(q, e), dy)
+    assert torch.equal(dw[-300:, -300:], q[:, -300:].double().T.matmul(dy[:, -300:].double()).float())
+    assert torch.equal(dw[:300, :300], q[:, :300].double().T.matmul(dy[:, :300].double()).float())
+
+
+@pytest.mark.gpu
 def test_binding_refuses_what_does_not_fit():
     x = torch.zeros((8, 64), dtype=BF, device="cuda")
     w, gate = torch.ones(64, device="cuda"), torch.ones((3, 64), device="cuda")
@@ -623,6 +674,8 @@ def test_binding_refuses_what_does_not_fit():
         da.block_norm_bwd(x, None, kept, w_post=w, w_pre=w)
     with pytest.raises(TypeError):
         da.block_norm_bwd(x.float(), h, kept, w_post=w, w_pre=w)   # kept.x is bf16
+    with pytest.raises(TypeError, match="kept.x"):                # without dx_out, kept.x says the type
+        da.block_norm_bwd(None, h, kept._replace(x=x.half(), y=None), w_pre=w)
     with pytest.raises(ValueError, match="rows"):
         da.act8_wgrad(da.act8_pack(x), torch.zeros((7, 64), dtype=BF, device="cuda"))
     with pytest.raises(ValueError, match="shape"):
