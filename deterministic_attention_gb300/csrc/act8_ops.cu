@@ -11,8 +11,8 @@
 // ones for checkpoints) and written once, and memory bounds them.  A thread
 // holds eight consecutive columns and an aligned quad of lanes one group of
 // 32, so a group's largest magnitude takes two shuffles.  Measured: a round
-// trip of 8192 x 4096 (203 MB) in 31 us, the gated unit's backward at 32768 x
-// 4096 from 8 bits (1.35 GB) in 192 us, 7.0 TB/s (part of what the pass before
+// trip of 8192 x 4096 (203 MB) in 32 us, the gated unit's backward at 32768 x
+// 4096 from 8 bits (1.35 GB) in 194 us, 7.0 TB/s (part of what the pass before
 // left is still in L2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

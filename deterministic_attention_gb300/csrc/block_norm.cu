@@ -25,8 +25,8 @@
 // 32768 x 1536 with an fp32 stream and a gate for every element, 705 MB, takes
 // 111 us, 6.3 TB/s or 93 % of the measured copy rate.  The backward is not
 // quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 118 us (75 %);
-// it issues 42 instructions an element, of which about half are a row's own
-// (its sums, waits and addresses), at 0.42 of the issue rate.  4096 x 768 from
+// it issues 42 instructions an element, of which two fifths are a row's own
+// (its sums, waits and addresses), at 0.47 of the issue rate.  4096 x 768 from
 // checkpoints, 32 MB, takes 14 us with the second kernel, of which two to
 // three rows per team and the two launches' ramps are most.
 #include <cuda_bf16.h>

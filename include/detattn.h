@@ -398,7 +398,8 @@ int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, 
  * gate_fp32, else bf16: row t takes gate row t / (N / G) (G = 1: one for
  * every channel; G = the sequences of a batch; G = N: one for every
  * element).  The norm before the block takes x' before its rounding to the
- * stream's type.
+ * stream's type.  Squares are summed in fp32: a row with a magnitude beyond
+ * about 1e19 has 1 / rms = 0, and one with an infinity or NaN gives NaN there.
  * Outputs: x_out = x' (with y; may be x itself), h (with w_pre), rstd_post
  * and rstd_pre fp32 [N] = 1 / sqrt(mean + eps) (with w_post, w_pre), and,
  * where not NULL, the checkpoints of yhat (with y) and xhat (with w_pre), for
