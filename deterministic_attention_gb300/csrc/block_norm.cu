@@ -24,9 +24,9 @@
 // Both move each tensor once and should be bound by memory.  The forward is:
 // 32768 x 1536 with an fp32 stream and a gate for every element, 705 MB, takes
 // 111 us, 6.3 TB/s or 93 % of the measured copy rate.  The backward is not
-// quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 118 us (75 %);
-// it issues 42 instructions an element, of which two fifths are a row's own
-// (its sums, waits and addresses), at 0.47 of the issue rate.  4096 x 768 from
+// quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 113 us (79 %);
+// it issues 37 instructions an element, of which a third are a row's own
+// (its sums, waits and addresses), at 0.41 of the issue rate.  4096 x 768 from
 // checkpoints, 32 MB, takes 14 us with the second kernel, of which two to
 // three rows per team and the two launches' ramps are most.
 #include <cuda_bf16.h>
@@ -124,24 +124,34 @@ __device__ __forceinline__ void keep8(const Vec8& v, float mult, bool in, size_t
   }
 }
 
-// Three sums at once.
+// Three sums at once.  The first two exchanges of a warp halve the sums as
+// well as the lanes, so that six shuffles do, not fifteen: lanes 0 to 7 end
+// with the first sum, 8 to 15 with the second, 16 to 23 with the third.
 template <bool MULTI>
 __device__ __forceinline__ void team_sum3(float (&v)[3], float* words, int W, int team, int warp_in_team,
                                           int lane, int& slot) {
+  const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
+  float k0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+  const float k1 = v[1] + __shfl_xor_sync(0xFFFFFFFFu, v[1], 16);
+  k0 = (odd ? k1 : k0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? k0 : k1, 8);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  for (int o = 4; o > 0; o >>= 1) k0 += __shfl_xor_sync(0xFFFFFFFFu, k0, o);
   if constexpr (MULTI) {
-    float* w = words + slot * 48 + team * W * 3;
-    if (lane < 3) w[warp_in_team * 3 + lane] = lane == 0 ? v[0] : lane == 1 ? v[1] : v[2];
+    float* w = words + slot * 64 + team * W * 4;
+    if ((lane & 7) == 0) w[warp_in_team * 4 + (lane >> 3)] = k0;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory");
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      v[k] = 0.0f;
-      for (int i = 0; i < W; ++i) v[k] += w[i * 3 + k];
+    v[0] = v[1] = v[2] = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < W; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(w + i * 4);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
     }
     slot ^= 1;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, k0, 8 * k);
   }
 }
 
@@ -262,6 +272,7 @@ struct BwdRing {
   int off_d, off_x, off_y, bytes;  // dh at 0
   int teams, stages;
   int W;             // warps per team
+  bool w_near;       // w_pre has a copy behind the column multipliers (always, but for fp32 tensors)
 };
 
 // This team's rows, in order: rows team, team + teams, ... of each item.
@@ -366,7 +377,7 @@ template <int CH, bool MULTI, bool F32, bool FROM8, BwdMode MODE>
 __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1) * 32, 1)
     block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float words[96];
+  __shared__ __align__(16) float words[2 * 64];  // two sets of four per warp
   __shared__ __align__(8) uint64_t bars[2 * kBwdMaxTeams * kBwdMaxStages];  // full, empty
   constexpr bool FULL = MODE == kBwdFull, per_row_gate = MODE == kBwdRowGate;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -382,6 +393,7 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
   const bool need_y = FULL || per_row_gate || (with_dy && (post || a.gate != nullptr));
   constexpr int kX = F32 ? 4 : 2;
   float* cols = reinterpret_cast<float*>(smem + teams * ring.stages * ring.bytes);  // [d]
+  float* near_w = cols + a.d;                                                       // [d]: w_pre
   auto full = [&](int team, int s) { return smem_u32(&bars[team * kBwdMaxStages + s]); };
   auto empty = [&](int team, int s) {
     return smem_u32(&bars[(kBwdMaxTeams + team) * kBwdMaxStages + s]);
@@ -496,6 +508,16 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
     acc_y[c].fill(0.0f);
   }
 
+  const bool w_near = FROM8 || !F32 || ring.w_near;
+  if (pre && w_near) {
+    for (int v = threadIdx.x; v < n_vec; v += team_threads) {
+      Vec8 w;
+      w.from_f32(a.w_pre + v * 8);
+      w.to_f32(near_w + v * 8);
+    }
+    teams_sync(team_threads);
+  }
+
   int s = 0;           // this row's stage
   uint32_t phase = 0;  // and the parity of its barrier
   BwdCursor cur;
@@ -569,7 +591,10 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
             Vec8 dh, w;
             dh.from_bf16(*reinterpret_cast<const uint4*>(st + v * 16));
             raw_x(v, x);
-            w.from_f32(a.w_pre + v * 8);
+            if (w_near)
+              w.from_f32(near_w + v * 8);
+            else
+              w.from_f32(a.w_pre + v * 8);
             const uint64_t sc = f2_all(scale_x(c)), rx = f2_all(m.rx);
             uint64_t part = 0;
 #pragma unroll
@@ -812,11 +837,17 @@ cudaError_t bwd_mode(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
   r.W = W;
   r.teams = bwd_warps(CH, MULTI, MODE == kBwdRowGate) / W;
-  while (r.teams > 1 && r.teams * 2 * r.bytes + 4 * a.d > kBwdSmem) --r.teams;
+  // The rings leave no L1 to speak of, so w_pre would come from L2 for every
+  // row: it has a copy behind the column multipliers, for which only fp32 rows
+  // of more than 7200 columns leave no room (32768 x 1536: 118.5 us without,
+  // 117.0 with it).
+  int cols = (pre ? 8 : 4) * a.d;
+  while (r.teams > 1 && r.teams * 2 * r.bytes + cols > kBwdSmem) --r.teams;
+  r.w_near = pre && r.teams * 2 * r.bytes + cols <= kBwdSmem;
+  if (!r.w_near) cols = 4 * a.d;
   r.stages = 2;
-  while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + 4 * a.d <= kBwdSmem)
-    ++r.stages;
-  const int smem = r.teams * r.stages * r.bytes + 4 * a.d;
+  while (r.stages < kBwdMaxStages && r.teams * (r.stages + 1) * r.bytes + cols <= kBwdSmem) ++r.stages;
+  const int smem = r.teams * r.stages * r.bytes + cols;
   kernel<<<a.blocks, (r.teams * W + 1) * 32, smem, st>>>(a, r);
   return cudaGetLastError();
 }
