@@ -24,10 +24,13 @@
 //   warps 16-23  epilogue: accumulators -> fp32 sums in registers -> dw
 // Measured at 8192 x 4096 x 6144: single blocks 437 us, pairs with eight
 // converting warps and arithmetic through fp32 298 us, twelve warps and bytes
-// to bf16 by masks 255 us: 1.62 PFLOP/s, 84 % of the measured bf16 peak.
-// With the conversion left out it would be 207 us: the ALU and issue slots
-// that it takes are what bounds it now.  The rings are deep enough (six other
-// splits of the same shared memory were within 2 %).
+// to bf16 by masks 255 us (254 to 261 over three cards): 1.62 PFLOP/s, 84 % of the measured bf16 peak.
+// The conversion is what it pays for: 208 us without its stores, 232 without
+// its arithmetic, 238 without its loads of the bytes.  Shared memory is
+// nearest to its limit: copies (24 KB a step and block), conversion (24 KB)
+// and operands (at least 32 KB) take 640 cycles at 128 bytes a cycle of the
+// 810 that a step has, and the arithmetic holds the ALU for 330.  The rings
+// are deep enough (six other splits of the same shared memory were within 2 %).
 // Two accumulators in TMEM take turns: one is added to the tile's sum in
 // registers after every 1024 tokens while the other fills.
 // Tiles left over when all pairs have taken an equal number of whole ones
@@ -95,7 +98,7 @@ __device__ __forceinline__ void gave_up() { atomicOr(&g_wgrad_status, 1u); }
 // s): both terms are bf16 numbers that take one LOP3 from the bytes (0x4300 |
 // m and 0xC300 | s << 7), and every step is exact.  (Ten ALU instructions
 // for eight values; through fp32 and its packing conversion it takes
-// fourteen, and the ALU is what these warps wait for.)
+// fourteen.)
 // The masks are held in registers: an instruction takes one of them as an
 // immediate, and the compiler otherwise makes two of each.
 struct ByteMasks {

@@ -26,7 +26,7 @@
 // 111 us, 6.3 TB/s or 93 % of the measured copy rate.  The backward is not
 // quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 113 us (79 %);
 // it issues 37 instructions an element, of which a third are a row's own
-// (its sums, waits and addresses), at 0.41 of the issue rate.  4096 x 768 from
+// (its sums, waits and addresses), at 0.45 of the issue rate.  4096 x 768 from
 // checkpoints, 32 MB, takes 14 us with the second kernel, of which two to
 // three rows per team and the two launches' ramps are most.
 #include <cuda_bf16.h>

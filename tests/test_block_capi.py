@@ -20,7 +20,7 @@ def L():
 
 
 def _ok(rc):
-    """Valid: done on a GPU machine (nothing to do), stopped by the missing device here."""
+    """Valid: done where there is a GPU (nothing to do), stopped by the missing device here."""
     assert rc in (0, -6)
 
 
