@@ -872,7 +872,9 @@ cudaError_t bwd_of(const BlockNormBwdArgs& a, bool f32, int W, cudaStream_t st) 
 }  // namespace
 
 cudaError_t launch_block_norm_fwd(const BlockNormFwdArgs& a, bool x_fp32, cudaStream_t st) {
-  // Up to 1024 columns a row is one warp's; beyond, W warps share it.
+  // Up to 1024 columns a row is one warp's; beyond, W warps share it.  Three
+  // or four vectors per thread then: at 32768 x 1536, when three took 124 us
+  // (112 now), two took 132, one 149 and six 175.
   const int W = (a.d + 1023) / 1024, ch = (a.d + 256 * W - 1) / (256 * W);
   if (W == 1) {
     if (ch == 1) return fwd_of<1, false>(a, x_fp32, W, st);
@@ -889,7 +891,7 @@ namespace {
 // Warps per row and vectors per thread.  Up to 768 columns a row is one
 // warp's; beyond, two vectors per thread keep more warps at work than three
 // where their teams fill the block as well (32768 x 1536: five teams of three
-// against five of two).
+// warps took 119 us where five of two took 124).
 struct BwdShape {
   int W, ch;
 };
