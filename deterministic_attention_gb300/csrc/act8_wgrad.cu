@@ -222,6 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int n_units = unit_count(a);
   bool ok = true;
+  int steps = 0;  // warp 1: products issued (even block), or to be issued (odd block)
 
   if (warp < kCtrlWarps) {
     setmaxnreg_dec<kCtrlRegs>();
@@ -242,12 +243,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             r.next(kRawStages);
           }
         }
-        if (!ok) {
-          // The copies in flight, before the block ends.
-          for (int k = it > kRawStages ? it - kRawStages : 0; k < it; ++k)
-            mbar_wait_hint(bar(kBarRaw + k % kRawStages), (k / kRawStages) & 1, a.wait_ns);
-          gave_up();
-        }
+        // The copies in flight, before the block ends.
+        bool landed = true;
+        for (int k = it > kRawStages ? it - kRawStages : 0; k < it && landed; ++k)
+          landed = mbar_wait_hint(bar(kBarRaw + k % kRawStages), (k / kRawStages) & 1, a.wait_ns);
+        if (!ok || !landed) gave_up();
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -270,17 +270,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             r.next(kBStages);
           }
         }
-        if (!ok) {
-          // The odd block's copies complete here too; it leaves no earlier
-          // than this block.
-          if (rank == 0)
-            for (int k = it > kBStages ? it - kBStages : 0; k < it; ++k)
-              mbar_wait_hint(bar(kBarB + k % kBStages), (k / kBStages) & 1, a.wait_ns);
-          gave_up();
-        }
+        // The copies in flight.  The odd block's complete here too; it leaves
+        // no earlier than this block.
+        bool landed = true;
+        if (rank == 0)
+          for (int k = it > kBStages ? it - kBStages : 0; k < it && landed; ++k)
+            landed = mbar_wait_hint(bar(kBarB + k % kBStages), (k / kBStages) & 1, a.wait_ns);
+        if (!ok || !landed) gave_up();
       }
       __syncwarp();
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1 && rank == 1) {
+      steps = total_steps(a, pair, pairs);
+    } else if (warp == 1) {
       constexpr uint32_t kId = idesc_bf16(kWgradBM, kWgradBN, true, true);
       // MN-major tiles: 16 tokens are 16 rows of 128 bytes; atoms lie 8 KB apart.
       const uint64_t dA0 = sdesc_sw128(sA0, 8192, 1024);
@@ -307,12 +308,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma_commit_pair(bar(kBarBFree + rb.s));
             ra.next(kAStages);
             rb.next(kBStages);
+            ++steps;
           }
           if (ok) mma_commit_pair(bar(kBarAcc + acc));
         }
       }
       mma_commit_pair(bar(kBarDrain));
-      if (!warp_all(mbar_wait_hint(bar(kBarDrain), 0, a.wait_ns)) || !ok) gave_up();
     }
   } else if (warp < kCtrlWarps + kConvWarps) {
     // int8 -> bf16: thread (warp, lane) turns columns 8 j .. 8 j + 7, j =
@@ -494,8 +495,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  // Neither block leaves while the other's products, copies or arrivals may
-  // still reach it.
+  // A commit arrives in both blocks on its own time: neither a barrier of the
+  // threads nor the other block's copy of it orders that arrival.  So each
+  // block waits for its own copy of every commit that nobody here has waited
+  // for: the last round of both rings (the converting warps and the dY producer
+  // have seen all earlier ones, so the parities are not ambiguous), and the
+  // last commit of all.  (The epilogue has seen the accumulators'.)
+  if (warp == 1) {
+    for (int k = steps > kAStages ? steps - kAStages : 0; k < steps && ok; ++k)
+      ok = warp_all(mbar_wait_hint(bar(kBarAFree + k % kAStages), (k / kAStages) & 1, a.wait_ns));
+    for (int k = steps > kBStages ? steps - kBStages : 0; k < steps && ok; ++k)
+      ok = warp_all(mbar_wait_hint(bar(kBarBFree + k % kBStages), (k / kBStages) & 1, a.wait_ns));
+    if (!warp_all(mbar_wait_hint(bar(kBarDrain), 0, a.wait_ns)) || !ok) gave_up();
+    __syncwarp();
+  }
+  // Then neither leaves before the other: the even block's products read the
+  // odd one's shared memory, and the odd one's copies and arrivals go to the
+  // even one's barriers.
   cluster_sync();
   if (threadIdx.x >> 5 == 1) {
     tc_fence_after();
