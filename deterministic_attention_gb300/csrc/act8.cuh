@@ -111,6 +111,11 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   f2_split(v, lo, hi);
   return lo + hi;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays one
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 struct Vec8 {
   uint64_t p[4];
   __device__ __forceinline__ void fill(float x) {
@@ -159,18 +164,32 @@ struct Vec8 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum = f2_fma(p[i], p[i], sum);
   }
-  // Logistic function 1 / (1 + 2^(-x log2 e)), within a few units of 2^-23 for
-  // |x| up to about 8 (what the rounded exponent leaves, |x| 2^-24, shrinks
-  // with 1 - sigma for x > 0).  An infinite power gives 0.
-  __device__ __forceinline__ void sigmoid() {
+  // Logistic function 1 / (1 + t), t = 2^(-x log2 e), within a few units of 2^-23
+  // for |x| up to about 8 (what the rounded exponent leaves, |x| 2^-24, shrinks
+  // with 1 - sigma for x > 0).  `more` of every pair: its t.  x is kept above
+  // -88, where t is finite and a quotient below 2^-126 is given as 0.
+  template <class More>
+  __device__ __forceinline__ void logistic(More more) {
     const uint64_t k = f2_all(-1.44269504f), one = f2_all(1.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float x, y;
-      f2_split(f2_mul(p[i], k), x, y);
-      f2_split(f2_add(f2_make(ex2_approx(x), ex2_approx(y)), one), x, y);
+      f2_split(p[i], x, y);
+      f2_split(f2_mul(f2_make(max_nan(x, -88.0f), max_nan(y, -88.0f)), k), x, y);
+      const uint64_t t = f2_make(ex2_approx(x), ex2_approx(y));
+      f2_split(f2_add(t, one), x, y);
       p[i] = f2_make(__fdividef(1.0f, x), __fdividef(1.0f, y));
+      more(i, t);
     }
+  }
+  __device__ __forceinline__ void sigmoid() {
+    logistic([](int, uint64_t) {});
+  }
+  // And its slope, t sigma^2: 1 - sigma = t sigma keeps its digits however
+  // large x is, where sigma - sigma^2 from a sigma rounded next to 1 has lost
+  // them all at x = 17.
+  __device__ __forceinline__ void sigmoid(Vec8& slope) {
+    logistic([&](int i, uint64_t t) { slope.p[i] = f2_mul(f2_mul(t, p[i]), p[i]); });
   }
   __device__ __forceinline__ uint4 to_bf16() const {
     uint32_t w[4];

@@ -357,11 +357,7 @@ __device__ __forceinline__ void block_columns(const Vec8 (&acc)[CH], float* scra
 __device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at, Vec8& g, Vec8& slope) {
   load_gate(a.gate, at, a.gate_fp32, g);
   slope.fill(1.0f);
-  if (a.gate_sigmoid) {
-    g.sigmoid();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) slope.p[i] = f2_fma(f2_mul(g.p[i], f2_all(-1.0f)), g.p[i], g.p[i]);
-  }
+  if (a.gate_sigmoid) g.sigmoid(slope);
 }
 
 // Eight gate values of a row's own gate.
@@ -655,18 +651,14 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
               keep[c].scale(kd);
               keep[c].mul(gw);
               if constexpr (per_row_gate) {
-                // dgate = block_scale D yhat w_post slope, slope = 1 or g - g^2.
-                Vec8 g;
-                row_gate(a, at, g);
+                // dgate = block_scale D yhat w_post slope.
+                Vec8 g, slope;
+                gate_pairs(a, at, g, slope);
                 gw.mul(e);
                 gw.scale(a.block_scale * scale_y(c));
                 e.mul(g);
                 keep[c].mul(g);
-                if (a.gate_sigmoid) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    gw.p[i] = f2_mul(gw.p[i], f2_fma(f2_mul(g.p[i], f2_all(-1.0f)), g.p[i], g.p[i]));
-                }
+                if (a.gate_sigmoid) gw.mul(slope);
                 if (a.gate_fp32)
                   store8<true>(a.dgate, at, gw);
                 else

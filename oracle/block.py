@@ -133,7 +133,8 @@ def norm_bwd(dx_out, dh, xhat, yhat, rstd_pre, rstd_post, gate=None, w_post=None
         yhat = f64(yhat)
     w = f64(w_post) if w_post is not None else 1.0
     if gate is not None:
-        slope = g * (1.0 - g) if as_sigmoid else np.ones_like(g)
+        # sigma' = sigma(x) sigma(-x): 1 - sigma has no digits left for large x.
+        slope = g * gate_rows(-f64(gate), rows, True) if as_sigmoid else np.ones_like(g)
         G = np.asarray(gate).shape[0]
         t = s * D * yhat * w * slope
         tm = np.abs(out["|dx|"] / max(abs(r), 1e-300) * s * yhat * w * slope) if r else np.abs(t)

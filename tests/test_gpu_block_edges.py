@@ -11,7 +11,8 @@ import torch
 import deterministic_attention_gb300 as da
 from helpers import to_np
 from oracle import block as ob
-from test_gpu_block import BF, F32, U, _acts, _gen, _within
+from test_gpu_block import (BF, EPS, F32, U, _acts, _bwd_refs, _check_bwd, _cuda, _gen, _norm_inputs,
+                            _within)
 
 # ------------------------------------------------------------ weight gradient
 
@@ -44,3 +45,56 @@ def test_wgrad_blocks_leave_nothing_behind_for_the_next_kernel():
         for i, o in enumerate(outs):
             assert torch.equal(o, refs[i % len(calls)]), (k, i)
     da.check_status()
+
+
+# ------------------------------------------------------------ gates far from zero
+FAR = [-20.0, -12.0, -8.0, 8.0, 12.0, 20.0]
+
+
+def _far_gate_inputs(rows, d, G, gdt, stream, post, seed):
+    i = _norm_inputs(rows, d, (G, gdt), post, True, stream, seed)
+    logits = torch.tensor(FAR)[torch.randint(0, len(FAR), i["gate"].shape, generator=_gen(seed + 1))]
+    # A third of the gates as they were; the others at and next to the far logits.
+    far = torch.rand(i["gate"].shape, generator=_gen(seed + 2)) < 0.67
+    i["gate"] = torch.where(far, logits + 0.1 * i["gate"].float(), i["gate"].float()).to(gdt)
+    return i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gdt", [F32, BF])
+@pytest.mark.parametrize("rows,d,G,stream,post", [
+    (1, 64, 1, "fp32", True),        # one row: its own gate, nothing summed
+    (6, 256, "row", "bf16", True), (7, 2304, "row", "fp32", False),
+    (9, 768, 3, "fp32", True), (40, 1536, 1, "bf16", False), (12, 4608, 2, "fp32", True)])
+@pytest.mark.parametrize("keep8", [False, True])
+def test_sigmoid_gate_keeps_its_slope_when_open_or_shut(rows, d, G, stream, post, gdt, keep8):
+    """dgate through sigma' = sigma(x) sigma(-x) at logits up to 20, where sigma
+    (1 - sigma) from a rounded sigma has no digits left.  The bound is the one
+    for every gate: (rows + 264) u of the magnitudes, which hold sigma' itself.
+    (sigma' is within 8 u + |x| u here; 20 and the 64 u of the factors beside
+    it are counted with each term, of 264.)"""
+    i = _far_gate_inputs(rows, d, G, gdt, stream, post, rows + d)
+    c = _cuda(i)
+    kw = dict(gate=c["gate"], w_post=c["w_post"], w_pre=c["w_pre"], res_scale=0.9, block_scale=0.6,
+              gate_sigmoid=True)
+    _, _, kept = da.block_norm_fwd(c["x"], c["y"], eps=EPS, keep8=keep8, **kw)
+    got = da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw)
+    _check_bwd(got, _bwd_refs(i, kept, 0.9, 0.6, True), rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 2])
+def test_sigmoid_gate_at_infinite_logits(rows):
+    """A gate that is shut or open for good (a mask) has sigma 0 or 1 and a
+    slope of zero; a NaN stays in its own columns."""
+    d = 64
+    gate = torch.zeros((1, d), device="cuda")
+    gate[0, :8], gate[0, 8:16], gate[0, 16:24], gate[0, 24] = float("inf"), float("-inf"), -200.0, float("nan")
+    gate[0, 32:40] = torch.finfo(F32).min
+    x, y = torch.zeros((rows, d), device="cuda"), torch.ones((rows, d), dtype=BF, device="cuda")
+    x_out, _, kept = da.block_norm_fwd(x, y, gate=gate, gate_sigmoid=True)
+    assert (x_out[:, :8] == 1).all() and (x_out[:, 8:24] == 0).all() and (x_out[:, 32:40] == 0).all()
+    assert x_out[:, 24].isnan().all() and (x_out[:, 25:32] == 0.5).all() and (x_out[:, 40:] == 0.5).all()
+    g = da.block_norm_bwd(torch.ones_like(x), None, kept, gate=gate, gate_sigmoid=True)
+    assert not g.dgate[:, :24].any() and not g.dgate[:, 32:40].any() and g.dgate[:, 24].isnan().all()
+    assert (g.dgate[:, 25:32] == 0.25 * rows).all() and (g.dy[:, :8] == 1).all() and not g.dy[:, 8:24].any()
