@@ -111,9 +111,9 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   f2_split(v, lo, hi);
   return lo + hi;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays one
+__device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {  // a NaN stays one
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=&f"(d) : "f"(x), "f"(lo), "f"(hi));
   return d;
 }
 struct Vec8 {
@@ -164,21 +164,27 @@ struct Vec8 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum = f2_fma(p[i], p[i], sum);
   }
-  // Logistic function 1 / (1 + t), t = 2^(-x log2 e), within a few units of 2^-23
-  // for |x| up to about 8 (what the rounded exponent leaves, |x| 2^-24, shrinks
-  // with 1 - sigma for x > 0).  `more` of every pair: its t.  x is kept above
-  // -88, where t is finite and a quotient below 2^-126 is given as 0.
+  // Logistic function 1 / (1 + t), t = 2^(-x log2 e).  What rounding -x log2 e
+  // to p loses, |x| 2^-24 of t, is put back with the product's remainder d:
+  // t = 2^p (1 - d ln 2).  With the power (2^-22) and the quotient (two units
+  // in the last place) sigma is within 11 2^-24 of its value at any x.  x is
+  // kept in [-88, 128]: t stays finite, and a quotient below 2^-126 is given
+  // as 0.  `more` of every pair: its t.
   template <class More>
   __device__ __forceinline__ void logistic(More more) {
-    const uint64_t k = f2_all(-1.44269504f), one = f2_all(1.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x, y;
-      f2_split(p[i], x, y);
-      f2_split(f2_mul(f2_make(max_nan(x, -88.0f), max_nan(y, -88.0f)), k), x, y);
-      const uint64_t t = f2_make(ex2_approx(x), ex2_approx(y));
-      f2_split(f2_add(t, one), x, y);
-      p[i] = f2_make(__fdividef(1.0f, x), __fdividef(1.0f, y));
+      float a, b;
+      f2_split(p[i], a, b);
+      const uint64_t x = f2_make(clamp_nan(a, -88.0f, 128.0f), clamp_nan(b, -88.0f, 128.0f));
+      const uint64_t e = f2_mul(x, f2_all(-1.44269502f));
+      // log2 e = 1.44269502 (as rounded) + 1.92596303e-8
+      const uint64_t d = f2_fma(x, f2_all(1.92596303e-8f), f2_fma(x, f2_all(1.44269502f), e));
+      f2_split(e, a, b);
+      const uint64_t t0 = f2_make(ex2_approx(a), ex2_approx(b));
+      const uint64_t t = f2_fma(f2_mul(t0, f2_all(-0.693147181f)), d, t0);
+      f2_split(f2_add(t, f2_all(1.0f)), a, b);
+      p[i] = f2_make(__fdividef(1.0f, a), __fdividef(1.0f, b));
       more(i, t);
     }
   }

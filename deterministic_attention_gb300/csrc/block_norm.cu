@@ -158,8 +158,17 @@ __device__ __forceinline__ void team_sum3(float (&v)[3], float* words, int W, in
 // ------------------------------------------------------------ forward
 constexpr int kFwdWarps = 4;  // warps per block where a row takes one warp
 
-template <int CH, bool MULTI, bool F32, bool KEEP8>
-__global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? (CH == 3 ? 4 : 3) : 6)
+// Blocks of 128 threads that fit an SM with the registers they get: seven,
+// but for 1024 columns in fp32, which would spill (4096 x 1024 in bf16 with
+// checkpoints: 9.6 us with seven, 14.1 with six).
+constexpr int fwd_blocks(int ch, bool multi, bool f32) {
+  return multi ? (ch == 3 ? 4 : 3) : (ch == 4 && f32 ? 6 : 7);
+}
+// SIG: a gate that goes through its sigmoid (a kernel for both takes the
+// registers of the sigmoid in every call: 32768 x 1536 with checkpoints and no
+// sigmoid 85 us against 82).
+template <int CH, bool MULTI, bool F32, bool KEEP8, bool SIG>
+__global__ void __launch_bounds__(MULTI ? 256 : 128, fwd_blocks(CH, MULTI, F32))
     block_norm_fwd_kernel(const BlockNormFwdArgs a) {
   __shared__ float words[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(MULTI ? 256 : 128, MULTI ? (CH == 3 ? 4 : 3) :
         if (a.gate) {
           Vec8 g;
           load_gate(a.gate, gate_row + v * 8, a.gate_fp32, g);
-          if (a.gate_sigmoid) g.sigmoid();
+          if constexpr (SIG) g.sigmoid();
           z.mul(g);
         }
         const uint64_t r = f2_all(a.res_scale), s = f2_all(a.block_scale);
@@ -360,22 +369,19 @@ __device__ __forceinline__ void gate_pairs(const BlockNormBwdArgs& a, size_t at,
   if (a.gate_sigmoid) g.sigmoid(slope);
 }
 
-// Eight gate values of a row's own gate.
-__device__ __forceinline__ void row_gate(const BlockNormBwdArgs& a, size_t at, Vec8& g) {
-  load_gate(a.gate, at, a.gate_fp32, g);
-  if (a.gate_sigmoid) g.sigmoid();
-}
-
 // What the compiler knows of a call: that every input is there and no row has
-// a gate of its own; only the latter; that every row has one.
-enum BwdMode { kBwdFull, kBwdPlain, kBwdRowGate };
+// a gate of its own; only the latter; that every row has one, as it is or
+// through its sigmoid (32768 x 1536 with the flag read at run time took 220
+// and 252 us).
+enum BwdMode { kBwdFull, kBwdPlain, kBwdRowGate, kBwdRowSigmoid };
+constexpr bool of_row_gate(BwdMode m) { return m == kBwdRowGate || m == kBwdRowSigmoid; }
 template <int CH, bool MULTI, bool F32, bool FROM8, BwdMode MODE>
-__global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1) * 32, 1)
+__global__ void __launch_bounds__((bwd_warps(CH, MULTI, of_row_gate(MODE)) + 1) * 32, 1)
     block_norm_bwd_kernel(const BlockNormBwdArgs a, const BwdRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float words[2 * 64];  // two sets of four per warp
   __shared__ __align__(8) uint64_t bars[2 * kBwdMaxTeams * kBwdMaxStages];  // full, empty
-  constexpr bool FULL = MODE == kBwdFull, per_row_gate = MODE == kBwdRowGate;
+  constexpr bool FULL = MODE == kBwdFull, per_row_gate = of_row_gate(MODE);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = MULTI ? ring.W : 1;
   const int teams = ring.teams, team_threads = teams * W * 32;
@@ -608,7 +614,8 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
             raw_y(v, f);
             gw.mul(f);
             if constexpr (per_row_gate) {
-              row_gate(a, base + v * 8, f);
+              load_gate(a.gate, base + v * 8, a.gate_fp32, f);
+              if constexpr (MODE == kBwdRowSigmoid) f.sigmoid();
               gw.mul(f);
             }
             uint64_t part = 0, cross = 0;
@@ -653,12 +660,13 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, MODE == kBwdRowGate) + 1
               if constexpr (per_row_gate) {
                 // dgate = block_scale D yhat w_post slope.
                 Vec8 g, slope;
-                gate_pairs(a, at, g, slope);
+                load_gate(a.gate, at, a.gate_fp32, g);
+                if constexpr (MODE == kBwdRowSigmoid) g.sigmoid(slope);
                 gw.mul(e);
                 gw.scale(a.block_scale * scale_y(c));
                 e.mul(g);
                 keep[c].mul(g);
-                if (a.gate_sigmoid) gw.mul(slope);
+                if constexpr (MODE == kBwdRowSigmoid) gw.mul(slope);
                 if (a.gate_fp32)
                   store8<true>(a.dgate, at, gw);
                 else
@@ -792,18 +800,23 @@ cudaError_t fwd_of(const BlockNormFwdArgs& a, bool f32, int W, cudaStream_t st) 
   const unsigned grid = MULTI ? a.N : (a.N + kFwdWarps - 1) / kFwdWarps;
   const unsigned block = MULTI ? W * 32 : kFwdWarps * 32;
   const bool keep = a.xhat_q != nullptr || a.yhat_q != nullptr;
+  const bool sig = a.gate != nullptr && a.gate_sigmoid;
+  auto launch = [&](auto kernel) {
+    kernel<<<grid, block, 0, st>>>(a);
+    return cudaGetLastError();
+  };
   if (f32) {
     if (keep)
-      block_norm_fwd_kernel<CH, MULTI, true, true><<<grid, block, 0, st>>>(a);
-    else
-      block_norm_fwd_kernel<CH, MULTI, true, false><<<grid, block, 0, st>>>(a);
-  } else {
-    if (keep)
-      block_norm_fwd_kernel<CH, MULTI, false, true><<<grid, block, 0, st>>>(a);
-    else
-      block_norm_fwd_kernel<CH, MULTI, false, false><<<grid, block, 0, st>>>(a);
+      return launch(sig ? block_norm_fwd_kernel<CH, MULTI, true, true, true>
+                        : block_norm_fwd_kernel<CH, MULTI, true, true, false>);
+    return launch(sig ? block_norm_fwd_kernel<CH, MULTI, true, false, true>
+                      : block_norm_fwd_kernel<CH, MULTI, true, false, false>);
   }
-  return cudaGetLastError();
+  if (keep)
+    return launch(sig ? block_norm_fwd_kernel<CH, MULTI, false, true, true>
+                      : block_norm_fwd_kernel<CH, MULTI, false, true, false>);
+  return launch(sig ? block_norm_fwd_kernel<CH, MULTI, false, false, true>
+                    : block_norm_fwd_kernel<CH, MULTI, false, false, false>);
 }
 
 template <int CH, bool MULTI, bool F32, bool FROM8, BwdMode MODE>
@@ -828,7 +841,7 @@ cudaError_t bwd_mode(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   r.off_y = r.off_x + (pre ? (FROM8 ? 1 : x_bytes) * a.d : 0);
   r.bytes = r.off_y + (need_y ? (FROM8 ? 1 : 2) * a.d : 0);
   r.W = W;
-  r.teams = bwd_warps(CH, MULTI, MODE == kBwdRowGate) / W;
+  r.teams = bwd_warps(CH, MULTI, of_row_gate(MODE)) / W;
   // The rings leave no L1 to speak of, so w_pre would come from L2 for every
   // row: it has a copy behind the column multipliers, for which only fp32 rows
   // of more than 7200 columns leave no room (32768 x 1536: 118.5 us without,
@@ -847,7 +860,8 @@ cudaError_t bwd_mode(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
 template <int CH, bool MULTI, bool F32, bool FROM8>
 cudaError_t bwd_typed(const BlockNormBwdArgs& a, int W, cudaStream_t st) {
   if (a.gate != nullptr && a.rows_per_gate == 1)
-    return bwd_mode<CH, MULTI, F32, FROM8, kBwdRowGate>(a, W, st);
+    return a.gate_sigmoid ? bwd_mode<CH, MULTI, F32, FROM8, kBwdRowSigmoid>(a, W, st)
+                          : bwd_mode<CH, MULTI, F32, FROM8, kBwdRowGate>(a, W, st);
   if (a.dh != nullptr && a.dx_out != nullptr && a.dy != nullptr && a.w_post != nullptr)
     return bwd_mode<CH, MULTI, F32, FROM8, kBwdFull>(a, W, st);
   return bwd_mode<CH, MULTI, F32, FROM8, kBwdPlain>(a, W, st);

@@ -397,7 +397,9 @@ int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, 
  * [N, d]; w_post, w_pre: fp32 [d].  gate: [G, d], G dividing N, fp32 with
  * gate_fp32, else bf16: row t takes gate row t / (N / G) (G = 1: one for
  * every channel; G = the sequences of a batch; G = N: one for every
- * element).  The norm before the block takes x' before its rounding to the
+ * element).  A sigmoid and its slope are within 2^-20 of their values
+ * whatever the logit; what is below 2^-126 is zero.  The norm before the
+ * block takes x' before its rounding to the
  * stream's type.  Squares are summed in fp32: a row with a magnitude beyond
  * about 1e19 has 1 / rms = 0, and one with an infinity or NaN gives NaN there.
  * Outputs: x_out = x' (with y; may be x itself), h (with w_pre), rstd_post

@@ -98,3 +98,24 @@ def test_sigmoid_gate_at_infinite_logits(rows):
     g = da.block_norm_bwd(torch.ones_like(x), None, kept, gate=gate, gate_sigmoid=True)
     assert not g.dgate[:, :24].any() and not g.dgate[:, 32:40].any() and g.dgate[:, 24].isnan().all()
     assert (g.dgate[:, 25:32] == 0.25 * rows).all() and (g.dy[:, :8] == 1).all() and not g.dy[:, 8:24].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gdt", [F32, BF])
+def test_sigmoid_of_shut_gates_is_as_good_as_of_open_ones(gdt):
+    """sigma itself, read from an fp32 stream (r = 0, y = 1: x' = s sigma), over
+    -87 .. 87.  Its relative error: the power of two 4 u (2^-22), its exponent's
+    rounding carried along (1 u), the sum 1 u, the quotient 4 u (two units in
+    the last place), the last product 1 u: 11 u, held to 16 u at any logit."""
+    rows, d = 40, 1024
+    gate = ((torch.rand((rows, d), generator=_gen(71)) - 0.5) * 174.0).to(gdt)
+    x, y = torch.zeros((rows, d)), torch.ones((rows, d), dtype=BF)
+    x_out, _, kept = da.block_norm_fwd(x.cuda(), y.cuda(), gate=gate.cuda(), res_scale=0.0,
+                                       gate_sigmoid=True)
+    ref = ob.sigmoid(to_np(gate))
+    _within("sigma", to_np(x_out), ref, ref, 16, 0.0)
+    # Its slope: two more factors sigma, three roundings: 16 u + 11 u + 3 u.
+    g = da.block_norm_bwd(torch.ones((rows, d), device="cuda"), None, kept, gate=gate.cuda(),
+                          gate_sigmoid=True)
+    ref = ref * ob.sigmoid(-to_np(gate))
+    _within("slope", to_np(g.dgate), ref, ref, 30, 2.0 ** -8 if gdt == BF else 0.0)
