@@ -78,26 +78,6 @@ __device__ __forceinline__ uint32_t act8_quantise8(const float (&v)[8], float mu
 // 2^(e - 127); infinity for e = 255, whose group holds zeros: 0 * inf is NaN.
 __device__ __forceinline__ float act8_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
-// The whole numbers of four int8 bytes as floats: byte + 128 in the low bits
-// of 2^23's mantissa, less 2^23 + 128.
-__device__ __forceinline__ void act8_int4(uint32_t q, float (&f)[4]) {
-  const uint32_t u = q ^ 0x80808080u;
-  f[0] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.0f;
-  f[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.0f;
-  f[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.0f;
-  f[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.0f;
-}
-__device__ __forceinline__ void act8_values8(uint2 q, float scale, float (&v)[8]) {
-  float a[4], b[4];
-  act8_int4(q.x, a);
-  act8_int4(q.y, b);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i] * scale;
-    v[4 + i] = b[i] * scale;
-  }
-}
-
 // ------------------------------------------------------------ eight values as four pairs
 // The norms' arithmetic runs on f32x2 instructions: two results an issue slot.
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
@@ -136,7 +116,8 @@ struct Vec8 {
     p[2] = b.x;
     p[3] = b.y;
   }
-  // The whole numbers of eight int8 bytes (the low byte of 2^23's mantissa).
+  // The whole numbers of eight int8 bytes: byte + 128 in the low bits of 2^23's
+  // mantissa, less 2^23 + 128.
   __device__ __forceinline__ void from_int8(uint2 q) {
     const uint32_t u[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
     const uint64_t off = f2_all(-8388736.0f);

@@ -12,7 +12,7 @@
 // holds eight consecutive columns and an aligned quad of lanes one group of
 // 32, so a group's largest magnitude takes two shuffles.  Measured: a round
 // trip of 8192 x 4096 (203 MB) in 32 us, the gated unit's backward at 32768 x
-// 4096 from 8 bits (1.35 GB) in 194 us, 7.0 TB/s (part of what the pass before
+// 4096 from 8 bits (1.35 GB) in 196 us, 6.9 TB/s (part of what the pass before
 // left is still in L2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -83,8 +83,20 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// sigma(a); exp of a large -a is infinity and gives 0.
-__device__ __forceinline__ float sigmoid_fast(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+// sigma(a) = f^2 r and 1 - sigma(a), by w = exp(-|a| / 2) and r = 1 / (1 + w^2):
+// f is 1 for a >= 0 and w below.  sigma is applied as two factors f, one to
+// each factor of a product: a sigma(a) b with a at -90 or -150 and a large b is
+// an ordinary number, though sigma(a) alone is below 2^-126.  (w is zero from
+// a = -174 on, where h is below 2^-115 for every bf16 b.)
+struct Logistic {
+  float f, r, rest;  // rest: 1 - sigma
+  __device__ __forceinline__ explicit Logistic(float a) {
+    const float w = ex2_approx(-0.72134752f * fabsf(a));
+    r = rcp_approx(fmaf(w, w, 1.0f));
+    f = a < 0.0f ? w : 1.0f;
+    rest = a < 0.0f ? r : w * w * r;
+  }
+};
 
 template <bool KEEP8>
 __global__ void __launch_bounds__(kThreads)
@@ -94,12 +106,15 @@ __global__ void __launch_bounds__(kThreads)
   const bool in = v < n_vec;
   const unsigned row = (in ? v : 0u) / f8, col = (in ? v : 0u) - row * f8;
   const size_t ia = static_cast<size_t>(row) * (2 * f8) + col, ib = ia + f8;
-  float a[8], b[8], o[8];
   const uint4 ra = u[ia], rb = u[ib];
+  float a[8], b[8], o[8];
   bf16x8_to_float(ra, a);
   bf16x8_to_float(rb, b);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = a[i] * sigmoid_fast(a[i]) * b[i];
+  for (int i = 0; i < 8; ++i) {
+    const Logistic s(a[i]);
+    o[i] = (a[i] * s.f) * (b[i] * s.f) * s.r;
+  }
   if (in) h[v] = float_to_bf16x8(o);
   if constexpr (KEEP8) {
     uint2 qa, qb;
@@ -115,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// da = dh b (s + a s (1 - s)), db = dh a s with s = sigma(a).
+// da = dh b s (1 + a (1 - s)), db = dh a s with s = sigma(a).
 template <bool FROM8, bool WITH_H>
 __global__ void __launch_bounds__(kThreads)
     swiglu_bwd_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ u,
@@ -125,13 +140,18 @@ __global__ void __launch_bounds__(kThreads)
   if (v >= n_vec) return;
   const unsigned row = v / f8, col = v - row * f8;
   const size_t ia = static_cast<size_t>(row) * (2 * f8) + col, ib = ia + f8;
+  Vec8 va, vb;
   float g[8], a[8], b[8], da[8], db[8], o[8];
   const uint4 rg = dh[v];
   if constexpr (FROM8) {
     const uint2 qa = q[ia], qb = q[ib];
     const float sa = act8_scale(e[ia >> 2]), sb = act8_scale(e[ib >> 2]);
-    act8_values8(qa, sa, a);
-    act8_values8(qb, sb, b);
+    va.from_int8(qa);
+    vb.from_int8(qb);
+    va.scale(sa);
+    vb.scale(sb);
+    va.to_float(a);
+    vb.to_float(b);
   } else {
     const uint4 ra = u[ia], rb = u[ib];
     bf16x8_to_float(ra, a);
@@ -140,10 +160,11 @@ __global__ void __launch_bounds__(kThreads)
   bf16x8_to_float(rg, g);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float s = sigmoid_fast(a[i]), as = a[i] * s;
-    da[i] = g[i] * b[i] * fmaf(as, 1.0f - s, s);
-    db[i] = g[i] * as;
-    o[i] = as * b[i];
+    const Logistic s(a[i]);
+    const float as = a[i] * s.f * s.r, bs = b[i] * s.f, gs = g[i] * s.f;
+    da[i] = gs * (bs * s.r) * fmaf(a[i], s.rest, 1.0f);
+    db[i] = gs * as;
+    o[i] = as * bs;
   }
   du[ia] = float_to_bf16x8(da);
   du[ib] = float_to_bf16x8(db);

@@ -119,3 +119,40 @@ def test_sigmoid_of_shut_gates_is_as_good_as_of_open_ones(gdt):
                           gate_sigmoid=True)
     ref = ref * ob.sigmoid(-to_np(gate))
     _within("slope", to_np(g.dgate), ref, ref, 30, 2.0 ** -8 if gdt == BF else 0.0)
+
+
+# ------------------------------------------------------------ gated unit
+@pytest.mark.gpu
+@pytest.mark.parametrize("from8", [False, True])
+def test_swiglu_far_below_zero(from8):
+    """sigma(a) below 2^-126, where it is no normal fp32 number, times a b large
+    enough to bring the product back among bf16's: h and du keep the relative
+    accuracy of every other argument.  (2^-8 for the store; exp's rounded
+    argument |a| 2^-24, twice for the root squared, and a few units beside it:
+    400 u of the magnitudes, far below the store's; 1.2e-38: bf16's smallest
+    normal number, below which a store has fewer bits.)"""
+    a = torch.tensor([-80.0, -87.0, -87.5, -88.0, -88.5, -90.0, -95.0, -100.0, -120.0, -150.0, -170.0, -3e38]
+                     + [20.0, 88.0, 90.0, 120.0]).to(BF)
+    b = torch.tensor([1e30, 1e38, 3e38, -2e36]).to(BF)
+    f = 32 * len(b)
+    u = torch.zeros((len(a), 2 * f))
+    for j, v in enumerate(b):
+        # (32 equal values: a group of a checkpoint each)
+        u[:, 32 * j:32 * j + 32] = a.float()[:, None]
+        u[:, f + 32 * j:f + 32 * j + 32] = v.float() * torch.where(a.float() > 0, 1e-30, 1.0)[:, None]
+    u = u.to(BF)
+    dh = torch.full((len(a), f), -0.75, dtype=BF)
+    dh[:, ::2] = 1.5
+    c = da.act8_pack(u.cuda()) if from8 else u.cuda()
+    u64 = ob.act8_values(c.q.cpu().numpy(), c.e.cpu().numpy()) if from8 else to_np(u)
+    du, h = da.swiglu_bwd(dh.cuda(), c, with_h=True)
+    ref, dref = ob.swiglu(u64), ob.swiglu_grad(to_np(dh), u64)
+    x, y = np.split(u64, 2, axis=-1)
+    s, g = ob.sigmoid(x), np.abs(to_np(dh))
+    mag = np.concatenate([g * np.abs(y) * s * (1 + np.abs(x) * ob.sigmoid(-x)), g * np.abs(x) * s], -1)
+    for name, got, want, m in (("h", h, ref, np.abs(ref)), ("du", du, dref, mag)):
+        bound = 2.0 ** -8 * np.abs(want) + 400 * U * m + 1.2e-38
+        err = np.abs(to_np(got) - want)
+        assert np.isfinite(to_np(got)).all() and (err <= bound).all(), (name, float((err / bound).max()))
+    if not from8:
+        assert torch.equal(da.swiglu_fwd(u.cuda()), h)
