@@ -658,15 +658,18 @@ __global__ void __launch_bounds__((bwd_warps(CH, MULTI, of_row_gate(MODE)) + 1) 
               keep[c].scale(kd);
               keep[c].mul(gw);
               if constexpr (per_row_gate) {
-                // dgate = block_scale D yhat w_post slope.
-                Vec8 g, slope;
-                load_gate(a.gate, at, a.gate_fp32, g);
-                if constexpr (MODE == kBwdRowSigmoid) g.sigmoid(slope);
+                // dgate = block_scale D yhat w_post slope.  (Pair by pair: with
+                // eight slopes at a time fp32 rows of 768 columns spilled.)
+                Vec8 g;
                 gw.mul(e);
                 gw.scale(a.block_scale * scale_y(c));
+                load_gate(a.gate, at, a.gate_fp32, g);
+                if constexpr (MODE == kBwdRowSigmoid)
+                  g.logistic([&](int i, uint64_t t) {
+                    gw.p[i] = f2_mul(gw.p[i], f2_mul(f2_mul(t, g.p[i]), g.p[i]));
+                  });
                 e.mul(g);
                 keep[c].mul(g);
-                if constexpr (MODE == kBwdRowSigmoid) gw.mul(slope);
                 if (a.gate_fp32)
                   store8<true>(a.dgate, at, gw);
                 else
