@@ -926,15 +926,17 @@ BlockNormBwdPlan block_norm_bwd_plan(int N, int d, int G) {
     p.gate_parts = G == 1 && N > 1;
     return p;
   }
-  // About four items per block, so that their number divides well, and none
-  // without rows.
+  // About four items per block, so that their number divides well.  Slices of
+  // `per` rows each (the last may be shorter): as many as that gives, so that
+  // none is without rows.
   const int rows = N / G;
   int s = 4 * kBwdBlocks / G;
   s = s < 1 ? 1 : (s < rows ? s : rows);
-  p.slices = s;
-  p.items = G * s;
+  const int per = (rows + s - 1) / s;
+  p.slices = (rows + per - 1) / per;
+  p.items = G * p.slices;
   p.blocks = p.items < kBwdBlocks ? p.items : kBwdBlocks;
-  p.gate_parts = s > 1;
+  p.gate_parts = p.slices > 1;
   return p;
 }
 

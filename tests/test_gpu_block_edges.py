@@ -156,3 +156,21 @@ def test_swiglu_far_below_zero(from8):
         assert np.isfinite(to_np(got)).all() and (err <= bound).all(), (name, float((err / bound).max()))
     if not from8:
         assert torch.equal(da.swiglu_fwd(u.cuda()), h)
+
+
+# ------------------------------------------------------------ gate rows shared by few rows
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,G,d,stream", [(1000, 100, 768, "bf16"), (630, 90, 64, "fp32"),
+                                             (1824, 304, 2304, "bf16"), (1830, 305, 768, "bf16")])
+@pytest.mark.parametrize("keep8", [False, True])
+def test_gate_rows_shared_by_few_rows(rows, G, d, stream, keep8):
+    """Slices of one to three rows, uneven ones, and whole gate rows per item."""
+    i = _norm_inputs(rows, d, (G, F32), True, True, stream, rows + G)
+    c = _cuda(i)
+    kw = dict(gate=c["gate"], w_post=c["w_post"], w_pre=c["w_pre"], res_scale=0.9, block_scale=0.6)
+    _, _, kept = da.block_norm_fwd(c["x"], c["y"], eps=EPS, keep8=keep8, **kw)
+    got = da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw)
+    _check_bwd(got, _bwd_refs(i, kept, 0.9, 0.6, False), rows)
+    again = da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
