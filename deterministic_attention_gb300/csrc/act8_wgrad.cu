@@ -546,7 +546,26 @@ __global__ void __launch_bounds__(256) act8_wgrad_sum_kernel(const Act8WgradArgs
       make_float4(s.x * k, s.y * k, s.z * k, s.w * k);
 }
 
+// Failure-detection self-test: this kernel's two waits on a barrier that
+// nothing arrives on.
+__global__ void wgrad_wait_selftest_kernel(unsigned long long limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bar), 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  const bool own = warp_all(mbar_wait_hint(smem_u32(&bar), 0, limit_ns));
+  const bool pair = warp_all(mbar_wait_hint<true>(smem_u32(&bar), 0, limit_ns));
+  if (threadIdx.x == 0 && !own && !pair) gave_up();
+}
+
 }  // namespace
+
+cudaError_t launch_wgrad_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
+  wgrad_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
+  return cudaGetLastError();
+}
 
 Act8WgradPlan act8_wgrad_plan(int rows, int d, int n) {
   Act8WgradPlan p{};

@@ -59,7 +59,7 @@ struct BlockNormBwdArgs {
   int rows_per_gate;
   bool gate_fp32, gate_sigmoid;
   float res_scale, block_scale;
-  // Workspace: column sums of the row blocks (block_norm_bwd_layout).
+  // Workspace: column sums of the row blocks (laid out by the host, norm_layout).
   float* part_pre;        // [parts, d]
   float* part_post;       // [parts, d]
   float* part_gate;       // [items, d] (null: nothing to add up over blocks)
@@ -129,6 +129,9 @@ cudaError_t launch_act8_wgrad(const CUtensorMap& mq, const CUtensorMap& mdy,
 // Read-and-clear of the status words (bit 0: a wait ran out); synchronous on `st`.
 cudaError_t take_wgrad_status(cudaStream_t st, unsigned* out);
 cudaError_t take_norm_status(cudaStream_t st, unsigned* out);
+// One warp whose waits run out and set the status word.
+cudaError_t launch_wgrad_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
+cudaError_t launch_norm_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
 
 unsigned long long current_context_id();
 

@@ -798,6 +798,16 @@ __global__ void __launch_bounds__(kSumRuns * 32) sum_parts_kernel(const SumJobs 
   }
 }
 
+// Failure-detection self-test: the row teams' wait on a barrier that nothing
+// arrives on.
+__global__ void norm_wait_selftest_kernel(unsigned long long limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x != 0) return;
+  mbar_init(smem_u32(&bar), 1);
+  fence_barrier_init();
+  if (!mbar_wait(smem_u32(&bar), 0, limit_ns)) set_norm_status();
+}
+
 template <int CH, bool MULTI>
 cudaError_t fwd_of(const BlockNormFwdArgs& a, bool f32, int W, cudaStream_t st) {
   const unsigned grid = MULTI ? a.N : (a.N + kFwdWarps - 1) / kFwdWarps;
@@ -971,6 +981,11 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool x_fp32, cudaSt
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, sum_parts_kernel, j);
+}
+
+cudaError_t launch_norm_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
+  norm_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
+  return cudaGetLastError();
 }
 
 cudaError_t take_norm_status(cudaStream_t st, unsigned* out) {

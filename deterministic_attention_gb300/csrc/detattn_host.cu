@@ -1916,8 +1916,6 @@ int detattn_check_status(void* stream) {
   unsigned wg = 0, nm = 0;
   if (e == cudaSuccess) e = take_wgrad_status(st, &wg);
   if (e == cudaSuccess) e = take_norm_status(st, &nm);
-  if (wg) ly |= 2u;
-  if (nm) ly |= 4u;
   if (e != cudaSuccess) return fail(DETATTN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (em & 1u)
     return fail(DETATTN_ERR_INDEX,
@@ -1926,10 +1924,11 @@ int detattn_check_status(void* stream) {
     return fail(DETATTN_ERR_WORKSPACE,
                 "the dQ step found its tile counter not cleared: run attn_bwd_delta on this "
                 "workspace (with the same workspace_bytes) first");
-  if (f | b | ly)
+  if (f | b | ly | wg | nm)
     return fail(DETATTN_ERR_DEVICE_TIMEOUT,
-                "a kernel gave up on a pipeline wait (fwd flags %u, bwd flags %u, layer flags %u)",
-                f, b, ly);
+                "a kernel gave up on a pipeline wait (fwd flags %u, bwd flags %u, layer flags %u, "
+                "act8_wgrad %u, block_norm_bwd %u)",
+                f, b, ly, wg, nm);
   return ok_status();
 }
 
@@ -1996,8 +1995,11 @@ int detattn_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {
   if ((rc = check_device()) != DETATTN_OK) return rc;
   if (limit_ns < 1000000ull) limit_ns = 1000000ull;
   if (limit_ns > 10000000000ull) limit_ns = 10000000000ull;
-  return launched(launch_wait_timeout_selftest(limit_ns, static_cast<cudaStream_t>(stream)),
-                  "detattn_selftest_wait_timeout");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_wait_timeout_selftest(limit_ns, st);
+  if (e == cudaSuccess) e = launch_wgrad_wait_selftest(limit_ns, st);
+  if (e == cudaSuccess) e = launch_norm_wait_selftest(limit_ns, st);
+  return launched(e, "detattn_selftest_wait_timeout");
 }
 
 int detattn_diag_dkdv_list(int B, int T, int Hq, int Hkv, int causal, int c, int ng, int force,

@@ -448,7 +448,7 @@ int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void
                    int d, int G, int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale,
                    float block_scale, void* stream);
 
-/* Synchronises `stream`, then reads and clears the device-side status word
+/* Synchronises `stream`, then reads and clears the device-side status words
  * that kernels set when a pipeline wait runs out (a bounded wait, default
  * limit 1 s).  Returns DETATTN_OK, DETATTN_ERR_DEVICE_TIMEOUT,
  * DETATTN_ERR_WORKSPACE (a dQ step found the workspace's tile counter not
@@ -521,13 +521,15 @@ int detattn_diag_dkdv_list(int B, int T, int Hq, int Hkv, int causal, int c, int
  * Returns DETATTN_OK or DETATTN_ERR_SHAPE for another value. */
 int detattn_set_dkdv_deal(int mode);
 
-/* Failure-detection self-test.  Launches a one-thread kernel on `stream`
- * that waits, with the same bounded wait the attention kernels use, on a
- * barrier nothing ever completes; after `limit_ns` (clamped to [1 ms, 10 s])
- * it gives up, records a timeout in the device status word and returns, so
+/* Failure-detection self-test.  Launches three small kernels on `stream`, one
+ * after the other, that wait, with the same bounded waits that the attention
+ * kernels, act8_wgrad and block_norm_bwd use, on a barrier nothing ever
+ * completes; each wait (four in all) gives up after `limit_ns` (clamped to [1
+ * ms, 10 s]), the kernel records a timeout in its status word and returns, so
  * the context stays usable.  A following detattn_check_status() returns
- * DETATTN_ERR_DEVICE_TIMEOUT (and clears the word).  Not tied to a passage of
- * the method: it exists to test the timeout path without faulting a GPU. */
+ * DETATTN_ERR_DEVICE_TIMEOUT, whose text names the kinds (and clears the
+ * words).  Not tied to a passage of the method: it exists to test the timeout
+ * path without faulting a GPU. */
 int detattn_selftest_wait_timeout(unsigned long long limit_ns, void* stream);
 
 /* Tuning knob: number of thread blocks that share one 128-key tile in the

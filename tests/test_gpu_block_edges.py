@@ -174,3 +174,27 @@ def test_gate_rows_shared_by_few_rows(rows, G, d, stream, keep8):
     again = da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw)
     for a, b in zip(got, again):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ waits that run out
+@pytest.mark.gpu
+def test_waits_that_run_out_are_reported_by_name_and_cleared():
+    """The bounded waits of the weight gradient and of the norm backward, on a
+    barrier nothing completes: each sets its own status word, the host reads
+    which, and the same context then computes as before."""
+    i = _cuda(_norm_inputs(100, 768, (1, F32), True, True, "bf16", 73))
+    kw = dict(gate=i["gate"], w_post=i["w_post"], w_pre=i["w_pre"])
+    _, h, kept = da.block_norm_fwd(i["x"], i["y"], keep8=True, **kw)
+
+    def both():
+        return [*da.block_norm_bwd(i["dx_out"], i["dh"], kept, **kw), da.act8_wgrad(kept.xhat8, h)]
+    ref = both()
+    da.check_status()
+    da.selftest_wait_timeout(2_000_000)
+    with pytest.raises(da.DetAttnError, match="act8_wgrad 1, block_norm_bwd 1") as e:
+        da.check_status()
+    assert e.value.code == -7
+    da.check_status()
+    for a, b in zip(ref, both()):
+        assert torch.equal(a, b)
+    da.check_status()
