@@ -198,3 +198,120 @@ def test_waits_that_run_out_are_reported_by_name_and_cleared():
     for a, b in zip(ref, both()):
         assert torch.equal(a, b)
     da.check_status()
+
+
+# ------------------------------------------------------------ guard bytes
+class _Guards:
+    """Outputs with 256 guard bytes before and after; `shift` bytes off alignment."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, shape, dtype, shift=0):
+        size = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.bufs.append((raw, 256 + shift, size))
+        return raw[256 + shift:256 + shift + size]
+
+    def check(self):
+        for raw, at, size in self.bufs:
+            assert (raw[:at] == 0xA5).all() and (raw[at + size:] == 0xA5).all(), size
+
+
+def _same(got, ref):
+    """Raw bytes of a guarded output against the binding's tensor."""
+    assert torch.equal(got, ref.contiguous().view(-1).view(torch.uint8).view(-1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", [(1, F32), ("row", BF), (67, F32)])
+@pytest.mark.parametrize("rows,d,stream", [(67, 1056, "bf16"), (134, 96, "fp32"), (67, 4608, "bf16")])
+@pytest.mark.parametrize("keep8", [False, True])
+def test_norms_write_every_output_and_nothing_beside_it(rows, d, stream, gate, keep8):
+    """All outputs of both norms through the C entry points, workspace included:
+    the same bytes as through the binding, guard bytes untouched, the exponent
+    bytes at odd addresses and the statistics four bytes off."""
+    G = rows if gate[0] == "row" else gate[0]
+    i = _cuda(_norm_inputs(rows, d, gate, True, True, stream, rows + d))
+    kw = dict(gate=i["gate"], w_post=i["w_post"], w_pre=i["w_pre"])
+    x_out, h, kept = da.block_norm_fwd(i["x"], i["y"], keep8=keep8, **kw)
+    ref = da.block_norm_bwd(i["dx_out"], i["dh"], kept, **kw)
+    g, p = _Guards(), (lambda t: None if t is None else t.data_ptr())
+    st, f32 = i["x"].dtype, stream == "fp32"
+    out = {"x": g((rows, d), st), "h": g((rows, d), BF), "ro": g((rows,), F32, 4), "rp": g((rows,), F32, 4)}
+    for n in ("y", "x"):
+        out[n + "q"] = g((rows, d), torch.int8) if keep8 else None
+        out[n + "e"] = g((rows, d // 32), torch.uint8, 3) if keep8 else None
+    L, flags = da.lib(), (int(f32), int(gate[1] == F32), 0)
+    rc = L.block_norm_fwd(p(i["x"]), p(i["y"]), p(i["gate"]), p(i["w_post"]), p(i["w_pre"]), p(out["x"]),
+                          p(out["h"]), p(out["ro"]), p(out["rp"]), p(out["yq"]), p(out["ye"]), p(out["xq"]),
+                          p(out["xe"]), rows, d, G, *flags, 1.0, 1.0, EPS, None)
+    assert rc == 0, da.last_error()
+    torch.cuda.synchronize()
+    for a, b in ((out["x"], x_out), (out["h"], h), (out["ro"], kept.rstd_post), (out["rp"], kept.rstd_pre)):
+        _same(a, b)
+    if keep8:
+        for n, c in (("y", kept.yhat8), ("x", kept.xhat8)):
+            _same(out[n + "q"], c.q)
+            _same(out[n + "e"], c.e)
+    need = da.block_norm_bwd_workspace_bytes(rows, d, G)
+    ws = g((need,), torch.uint8)
+    grads = [g((rows, d), st), g((rows, d), BF), g((G, d), gate[1]), g((d,), F32), g((d,), F32)]
+    rc = L.block_norm_bwd(p(i["dx_out"]), p(i["dh"]), None if keep8 else p(x_out),
+                          None if keep8 else p(i["y"]), p(out["xq"]), p(out["xe"]), p(out["yq"]),
+                          p(out["ye"]), p(i["gate"]), p(i["w_post"]), p(i["w_pre"]), p(out["ro"]),
+                          p(out["rp"]), *(p(t) for t in grads), p(ws), need, rows, d, G, *flags, 1.0, 1.0,
+                          None)
+    assert rc == 0, da.last_error()
+    torch.cuda.synchronize()
+    for a, b in zip(grads, ref):
+        _same(a, b)
+    g.check()
+    da.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,d,n", [(1777, 1184, 504), (300, 96, 264), (129, 2496, 2056)])
+def test_wgrad_writes_every_output_and_nothing_beside_it(rows, d, n):
+    """Cut tiles (the partial tiles and their sum under guards), whole ones, and
+    more whole ones than pairs of blocks, ragged both ways; the exponent bytes
+    at odd addresses."""
+    need = da.act8_wgrad_workspace_bytes(rows, d, n)
+    assert (need > 0) == (rows > 1000)
+    g = _Guards()
+    x, dy = _acts(_gen(79), rows, d).cuda(), torch.randn((rows, n), generator=_gen(80)).to(BF).cuda()
+    ref = da.act8_wgrad(da.act8_pack(x), dy)
+    q, e = g((rows, d), torch.int8), g((rows, d // 32), torch.uint8, 1)
+    L = da.lib()
+    assert L.act8_pack(x.data_ptr(), q.data_ptr(), e.data_ptr(), rows, d, None) == 0
+    back = g((rows, d), BF)
+    assert L.act8_unpack(q.data_ptr(), e.data_ptr(), back.data_ptr(), rows, d, None) == 0
+    dw, ws = g((d, n), F32), g((max(need, 16),), torch.uint8)
+    assert L.act8_wgrad(q.data_ptr(), e.data_ptr(), dy.data_ptr(), None, dw.data_ptr(), ws.data_ptr(), need,
+                        rows, d, n, None) == 0, da.last_error()
+    torch.cuda.synchronize()
+    _same(dw, ref)
+    _same(back, da.act8_unpack(da.act8_pack(x)))
+    g.check()
+    da.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,f", [(1, 32), (67, 1056), (130, 96)])
+def test_swiglu_writes_every_output_and_nothing_beside_it(rows, f):
+    g, L = _Guards(), da.lib()
+    u, dh = _acts(_gen(81), rows, 2 * f).cuda(), torch.randn((rows, f), generator=_gen(82)).to(BF).cuda()
+    href, c = da.swiglu_fwd(u, keep8=True)
+    h, q, e = g((rows, f), BF), g((rows, 2 * f), torch.int8), g((rows, f // 16), torch.uint8, 5)
+    assert L.swiglu_fwd(u.data_ptr(), h.data_ptr(), q.data_ptr(), e.data_ptr(), rows, f, None) == 0
+    for from8 in (False, True):
+        duref, href2 = da.swiglu_bwd(dh, c if from8 else u, with_h=True)
+        du, h2 = g((rows, 2 * f), BF), g((rows, f), BF)
+        kept = (None, q.data_ptr(), e.data_ptr()) if from8 else (u.data_ptr(), None, None)
+        assert L.swiglu_bwd(dh.data_ptr(), *kept, du.data_ptr(), h2.data_ptr(), rows, f, None) == 0
+        torch.cuda.synchronize()
+        _same(du, duref)
+        _same(h2, href2)
+    for a, b in ((h, href), (q, c.q), (e, c.e)):
+        _same(a, b)
+    g.check()
