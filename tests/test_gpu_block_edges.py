@@ -315,3 +315,118 @@ def test_swiglu_writes_every_output_and_nothing_beside_it(rows, f):
     for a, b in ((h, href), (q, c.q), (e, c.e)):
         _same(a, b)
     g.check()
+
+
+# ------------------------------------------------------------ forms of the norms' calls
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,d,gate,sig,post,stream", [
+    (37, 768, (1, F32), False, True, "bf16"), (37, 768, ("row", BF), True, True, "fp32"),
+    (40, 1536, (4, F32), True, False, "fp32"), (21, 2304, None, False, True, "bf16"),
+    (50, 8, (1, F32), False, True, "bf16"), (9, 8192, None, False, False, "fp32")])
+@pytest.mark.parametrize("keep8", [False, True])
+def test_nothing_comes_back_along_the_stream(rows, d, gate, sig, post, stream, keep8):
+    """dx_out = None behind a block (the last norm of a model): the gradients
+    with a dx_out of zeros.  From checkpoints the stream is then taken as bf16."""
+    if keep8 and d % 32:
+        pytest.skip("a checkpoint needs a multiple of 32 columns")
+    i = _norm_inputs(rows, d, gate, post, True, stream, 3 * rows + d)
+    c = _cuda(i)
+    kw = dict(gate=c["gate"], w_post=c["w_post"], w_pre=c["w_pre"], res_scale=0.9, block_scale=0.6,
+              gate_sigmoid=sig)
+    _, _, kept = da.block_norm_fwd(c["x"], c["y"], eps=EPS, keep8=keep8, **kw)
+    got = da.block_norm_bwd(None, c["dh"], kept, **kw)
+    assert got.dx.dtype == (BF if keep8 else i["x"].dtype)
+    i["dx_out"] = None
+    _check_bwd(got, _bwd_refs(i, kept, 0.9, 0.6, sig), rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keep8", [False, True])
+def test_has_block_says_what_kept_does_not(keep8):
+    """A block without gate or norm after it needs no y: with has_block its
+    gradient comes without y being kept; without, there is no dy and the
+    scales are not used."""
+    i = _norm_inputs(70, 1056, None, False, True, "bf16", 83)
+    c = _cuda(i)
+    _, _, kept = da.block_norm_fwd(c["x"], c["y"], w_pre=c["w_pre"], keep8=keep8)
+    kw = dict(w_pre=c["w_pre"], res_scale=0.9, block_scale=0.6)
+    ref = da.block_norm_bwd(c["dx_out"], c["dh"], kept, **kw)
+    less = kept._replace(y=None, yhat8=None)
+    for a, b in zip(da.block_norm_bwd(c["dx_out"], c["dh"], less, has_block=True, **kw), ref):
+        assert (a is None and b is None) or torch.equal(a, b)
+    alone = da.block_norm_bwd(c["dx_out"], c["dh"], kept, has_block=False, **kw)
+    plain = da.block_norm_bwd(c["dx_out"], c["dh"], less, w_pre=c["w_pre"])
+    assert alone.dy is None and torch.equal(alone.dx, plain.dx) and torch.equal(alone.dw_pre, plain.dw_pre)
+    with pytest.raises(ValueError, match="belong to"):
+        da.block_norm_bwd(c["dx_out"], c["dh"], kept, has_block=False, w_post=c["w_pre"], **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", [None, (1, F32), ("row", BF)])
+def test_gradients_may_overwrite_what_they_come_from(gate):
+    """dx over dx_out and dy over y, through the C entry point."""
+    rows, d = 1300, 1536
+    i = _cuda(_norm_inputs(rows, d, gate, True, True, "bf16", 89))
+    kw = dict(gate=i["gate"], w_post=i["w_post"], w_pre=i["w_pre"])
+    x_out, _, kept = da.block_norm_fwd(i["x"], i["y"], **kw)
+    ref = da.block_norm_bwd(i["dx_out"], i["dh"], kept, **kw)
+    p = lambda t: None if t is None else t.data_ptr()
+    G = 1 if gate is None else i["gate"].shape[0]
+    dgate, dwo, dwp = (None if t is None else torch.empty_like(t)
+                       for t in (i["gate"], i["w_post"], i["w_pre"]))
+    ws = torch.empty(da.block_norm_bwd_workspace_bytes(rows, d, G), dtype=torch.uint8, device="cuda")
+    rc = da.lib().block_norm_bwd(p(i["dx_out"]), p(i["dh"]), p(x_out), p(i["y"]), None, None, None, None,
+                                 p(i["gate"]), p(i["w_post"]), p(i["w_pre"]), p(kept.rstd_post),
+                                 p(kept.rstd_pre), p(i["dx_out"]), p(i["y"]), p(dgate), p(dwo), p(dwp),
+                                 p(ws), ws.numel(), rows, d, G, 0, int(gate == (1, F32)), 0, 1.0, 1.0, None)
+    assert rc == 0, da.last_error()
+    torch.cuda.synchronize()
+    for a, b in zip((i["dx_out"], i["y"], dgate, dwo, dwp), ref):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_gate_row_is_shared_by_consecutive_rows():
+    """[B, d] and [B, 1, d] gates are one row per sequence of a [B, T, d] stream;
+    [B, T, d] one per token."""
+    B, T, d = 3, 5, 64
+    g = _gen(97)
+    x, y = torch.zeros((B, T, d), device="cuda"), torch.ones((B, T, d), dtype=BF, device="cuda")
+    for shape in ((B, d), (B, 1, d), (B, T, d), (d,), (1, 1, d)):
+        gate = torch.randn(shape, generator=g).cuda()
+        want = (gate[:, None] if shape == (B, d) else gate).expand(B, T, d)
+        assert torch.equal(da.block_norm_fwd(x, y, gate=gate)[0], want)
+
+
+@pytest.mark.gpu
+def test_two_host_threads_at_once():
+    """First calls of kernels not used before, from two threads on two streams."""
+    import threading
+    outs, errs = {}, []
+    i = _cuda(_norm_inputs(60, 5120, (1, F32), True, True, "fp32", 101))
+    dy = torch.randn((60, 40), generator=_gen(103)).to(BF).cuda()
+    torch.cuda.synchronize()
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    kw = dict(gate=i["gate"], w_post=i["w_post"], w_pre=i["w_pre"])
+                    _, h, kept = da.block_norm_fwd(i["x"], i["y"], keep8=True, **kw)
+                    got = da.block_norm_bwd(i["dx_out"], i["dh"], kept, **kw)
+                    dw = da.act8_wgrad(kept.xhat8, dy)
+                    with pytest.raises(da.DetAttnError, match="eps"):
+                        da.block_norm_fwd(i["x"], w_pre=i["w_pre"], eps=-1.0)
+                torch.cuda.current_stream().synchronize()
+                outs[k] = [h, *got, dw]
+        except BaseException as e:  # noqa: BLE001
+            errs.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errs, errs
+    for a, b in zip(outs[0], outs[1]):
+        assert torch.equal(a, b)
+    da.check_status()
