@@ -32,7 +32,7 @@
 // 810 that a step has, and the arithmetic holds the ALU for 330.  The rings
 // are deep enough (six other splits of the same shared memory were within 2 %).
 // Two accumulators in TMEM take turns: one is added to the tile's sum in
-// registers after every 1024 tokens while the other fills.
+// registers after every 512 tokens while the other fills.
 // Tiles left over when all pairs have taken an equal number of whole ones
 // are cut along the tokens, one range per pair, and a second kernel adds the
 // ranges in ascending order.  Every element's sum has one fixed order.

@@ -99,9 +99,11 @@ constexpr int kWgradBM = 256;
 constexpr int kWgradBN = 256;
 constexpr int kWgradBK = 64;
 // Steps that one accumulator takes before it is added to the tile's sum in
-// fp32 registers: the tensor core's own additions lose about 6e-7 of a sum of
-// 1024 tokens, and in proportion to their number.
-constexpr int kWgradChunk = 16;
+// fp32 registers: the tensor core's own additions lose about 2e-7 of a
+// sum of 512 tokens, and in proportion to their number.  (Runs of 1024 tokens
+// left the result a little further from 64 bits than a product in fp32, at
+// 8192 x 4096 x 6144 in 263 us against 269; runs of 256 would take 287.)
+constexpr int kWgradChunk = 8;
 // Persistent pairs, one block per SM of the GB300.  A constant, so that the
 // deal of the work, and with it every bit, follows from the shape alone (no
 // pair waits for another, so any SM count is correct).

@@ -364,7 +364,7 @@ size_t act8_wgrad_workspace_bytes(int rows, int d, int n);
  * dy bf16 [rows, n]; dw fp32 [d, n], fully overwritten (zeros for rows = 0);
  * row_scale fp32 [d] or NULL (1): the norm's weight where the checkpoint
  * holds the normed input before it (block_norm_fwd).  bf16 tensor cores; runs
- * of at most 1024 tokens are summed there and the runs in fp32 registers, all
+ * of at most 512 tokens are summed there and the runs in fp32 registers, all
  * in a fixed order.  rows in [0, 2^24], d a
  * multiple of 32 and n of 8, both up to 2^20, rows * d, rows * n and d * n
  * at most 4e9.  q, dy, dw, row_scale and workspace 16-byte aligned. */
