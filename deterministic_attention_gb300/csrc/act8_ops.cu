@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // da = dh b s (1 + a (1 - s)), db = dh a s with s = sigma(a).
 template <bool FROM8, bool WITH_H>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     swiglu_bwd_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ u,
                       const uint2* __restrict__ q, const uint8_t* __restrict__ e,
                       uint4* __restrict__ du, uint4* __restrict__ h, unsigned n_vec, unsigned f8) {
