@@ -13,7 +13,7 @@
 #include <cstdint>
 
 #include "exp2_poly.cuh"
-#include "sm103_ptx.cuh"
+#include "block_ptx.cuh"
 
 namespace detattn {
 
