@@ -629,8 +629,10 @@ def block_norm_fwd(x, y=None, gate=None, w_post=None, w_pre=None, res_scale=1.0,
     """x' = res_scale x + block_scale g norm(y) w_post, h = norm(x') w_pre
     (include/detattn.h): returns (x', h, kept).  x [..., d] is the residual
     stream (bf16 or fp32), y bf16 the block's output (None: x' is x), gate
-    [d] or [..., d] (one row for every channel, sequence or token; its sigmoid
-    with gate_sigmoid), w_post and w_pre fp32 [d] or None.  kept is what
+    [d] or [..., d] (its sigmoid with gate_sigmoid): G rows in all, each shared
+    by N / G consecutive rows of the stream, so [d] is one for every channel,
+    [B, d] one for each sequence of a [B, T, d] stream and [B, T, d] one for
+    each token (a [T, d] gate is not repeated over B).  w_post and w_pre fp32 [d] or None.  kept is what
     block_norm_bwd takes: the row statistics with x' and y, or, with keep8,
     with their normed values in 8 bits."""
     rows, d = _rows(x, "x")

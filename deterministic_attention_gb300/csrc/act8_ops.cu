@@ -12,7 +12,7 @@
 // holds eight consecutive columns and an aligned quad of lanes one group of
 // 32, so a group's largest magnitude takes two shuffles.  Measured: a round
 // trip of 8192 x 4096 (203 MB) in 32 us, the gated unit's backward at 32768 x
-// 4096 from 8 bits (1.35 GB) in 196 us, 6.9 TB/s (part of what the pass before
+// 4096 from 8 bits (1.35 GB) in 193 us, 7.0 TB/s (part of what the pass before
 // left is still in L2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -14,8 +14,8 @@
 //
 // Shared memory decides the tile: for a step of 64 tokens a block alone on a
 // 128 x 256 tile would move 112 KB (int8 in and out 16, bf16 in and out 32, dY
-// in and out 64), 875 clocks at 128 bytes a clock for 512 clocks of MMA.  A
-// pair of blocks (cta_group::2) on a 256 x 256 tile shares dY: 80 KB each, 625
+// in and out 64), 896 clocks at 128 bytes a clock for 512 clocks of MMA.  A
+// pair of blocks (cta_group::2) on a 256 x 256 tile shares dY: 80 KB each, 640
 // clocks.  So blocks work in pairs, one persistent block per SM:
 //   warp 0       TMA producer of the int8 tiles (64 tokens each)
 //   warp 1       (even block) tcgen05.mma issuer, M = N = 256, K = 16
@@ -24,13 +24,17 @@
 //   warps 16-23  epilogue: accumulators -> fp32 sums in registers -> dw
 // Measured at 8192 x 4096 x 6144: single blocks 437 us, pairs with eight
 // converting warps and arithmetic through fp32 298 us, twelve warps and bytes
-// to bf16 by masks 255 us (254 to 261 over three cards): 1.62 PFLOP/s, 84 % of the measured bf16 peak.
-// The conversion is what it pays for: 208 us without its stores, 232 without
-// its arithmetic, 238 without its loads of the bytes.  Shared memory is
-// nearest to its limit: copies (24 KB a step and block), conversion (24 KB)
-// and operands (at least 32 KB) take 640 cycles at 128 bytes a cycle of the
-// 810 that a step has, and the arithmetic holds the ALU for 330.  The rings
-// are deep enough (six other splits of the same shared memory were within 2 %).
+// to bf16 by masks 255 us with runs of 1024 tokens, 264 to 270 with runs of 512
+// on a card that took 263 with the former: 1.53 to 1.56 PFLOP/s, 79 to 81 % of
+// the measured bf16 peak.  Kept busy, a card slows under its power limit: passes
+// one after another take up to 306 us (a library product in bf16 alone, 220 to
+// 224).  The conversion is what it pays for: 208 us of that 255 without its
+// stores, 232 without its arithmetic, 238 without its loads of the bytes.
+// Shared memory is nearest to its limit: copies (24 KB a step and block),
+// conversion (24 KB) and operands (at least 32 KB) take 640 cycles at 128 bytes
+// a cycle of the 810 that a step has, and the arithmetic holds the ALU for 330.
+// The rings are deep enough (six other splits of the same shared memory were
+// within 2 %).
 // Two accumulators in TMEM take turns: one is added to the tile's sum in
 // registers after every 512 tokens while the other fills.
 // Tiles left over when all pairs have taken an equal number of whole ones

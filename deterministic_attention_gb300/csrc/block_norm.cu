@@ -22,13 +22,20 @@
 // block order.  The deal of rows follows from the shape alone.
 //
 // Both move each tensor once and should be bound by memory.  The forward is:
-// 32768 x 1536 with an fp32 stream and a gate for every element, 705 MB, takes
-// 111 us, 6.3 TB/s or 93 % of the measured copy rate.  The backward is not
-// quite: 32768 x 1536 in bf16 with 32 gate rows, 605 MB, takes 113 us (79 %);
-// it issues 37 instructions an element, of which a third are a row's own
-// (its sums, waits and addresses), at 0.45 of the issue rate.  4096 x 768 from
-// checkpoints, 32 MB, takes 14 us with the second kernel, of which two to
-// three rows per team and the two launches' ramps are most.
+// 32768 x 1536 with an fp32 stream and a sigmoid gate for every element, 705
+// MB, takes 110 us, 6.4 TB/s or 95 % of the measured copy rate (what L2 keeps
+// of the pass before included).  The backward is not quite: 32768 x 1536 in
+// bf16 with 32 gate rows, 605 MB, takes 113 us (79 %); it issues 37
+// instructions an element, of which a third are a row's own (its sums, waits
+// and addresses), at 0.45 of the issue rate.  4096 x 768 from checkpoints, 32
+// MB, takes 14 us with the second kernel, of which two to three rows per team
+// and the two launches' ramps are most.  Where one team fills a block a row's
+// exchange has nothing beside it: 8192 x 4096 without a gate takes 82 us, 4096 x
+// 8192 76 us (59 either at the copy rate), 16384 x 2048 with three teams 72.  A
+// gate of each element's own leaves eleven warps, and its values are read for
+// both passes: 32768 x 1536 takes 202 us, 232 through a sigmoid (119 at the
+// copy rate).  Gate rows shared by two rows each keep two of eleven teams at
+// work: 32768 x 768 with 16384 of them takes 698 us, 56 without a gate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

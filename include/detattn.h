@@ -399,17 +399,19 @@ int swiglu_bwd(const void* dh, const void* u, const void* u_q, const void* u_e, 
  * [N, d]; w_post, w_pre: fp32 [d].  gate: [G, d], G dividing N, fp32 with
  * gate_fp32, else bf16: row t takes gate row t / (N / G) (G = 1: one for
  * every channel; G = the sequences of a batch; G = N: one for every
- * element).  A sigmoid and its slope are within 2^-20 of their values
- * whatever the logit; what is below 2^-126 is zero.  The norm before the
- * block takes x' before its rounding to the
- * stream's type.  Squares are summed in fp32: a row with a magnitude beyond
- * about 1e19 has 1 / rms = 0, and one with an infinity or NaN gives NaN there.
+ * element).  A sigmoid is within 2^-20 of its value whatever the logit, its
+ * slope within 2^-19; what is below 2^-126 is zero.  The norm before the
+ * block takes x' before its rounding to the stream's type.  Squares are summed
+ * in fp32: a row whose sum of squares passes 3.4e38 (one magnitude of 1.8e19,
+ * or 768 of 6.6e17) has 1 / rms = 0, and one with an infinity or NaN gives NaN
+ * there.
  * Outputs: x_out = x' (with y; may be x itself), h (with w_pre), rstd_post
  * and rstd_pre fp32 [N] = 1 / sqrt(mean + eps) (with w_post, w_pre), and,
  * where not NULL, the checkpoints of yhat (with y) and xhat (with w_pre), for
  * block_norm_bwd.  y or w_pre (or both) must be given; an argument that
  * needs another which is NULL must be NULL as well (w_post, gate, x_out,
- * yhat_q: y; rstd_post: w_post; h, rstd_pre, xhat_q: w_pre), and outputs named here with "(with ...)" must be given.
+ * yhat_q: y; rstd_post: w_post; h, rstd_pre, xhat_q: w_pre), and outputs named
+ * here with "(with ...)" must be given.
  * N in [0, 2^30], d a multiple of 8 (of 32 with checkpoints) in [8, 8192],
  * N * d at most 2^36.  eps > 0; the scales finite.  16-byte aligned pointers
  * (rstd_post and rstd_pre: 4-byte; yhat_e and xhat_e need no alignment). */
