@@ -87,7 +87,9 @@ __global__ void __launch_bounds__(kThreads)
 // f is 1 for a >= 0 and w below.  sigma is applied as two factors f, one to
 // each factor of a product: a sigma(a) b with a at -90 or -150 and a large b is
 // an ordinary number, though sigma(a) alone is below 2^-126.  (w is zero from
-// a = -174 on, where h is below 2^-115 for every bf16 b.)
+// a = -174 on, where h is below 2^-115 for every bf16 b.)  Powers and quotients
+// are the special-function unit's, within 2^-22 and 2^-23, and the exponent's
+// rounding is left in, |a| 2^-24: all far below half a step of the bf16 stores.
 struct Logistic {
   float f, r, rest;  // rest: 1 - sigma
   __device__ __forceinline__ explicit Logistic(float a) {
