@@ -376,7 +376,8 @@ int act8_wgrad(const void* q, const void* e, const void* dy, const float* row_sc
  * [0, 2^30], f a multiple of 8 (of 32 with a checkpoint), rows * f at most
  * 2^34.  h and u must not overlap.  h, and du below, keep their relative
  * accuracy where sigma(a) itself is below 2^-126 (a below -87); from a = -174
- * on they are zero.  An infinite a with sigma(a) = 0 gives NaN. */
+ * on they are zero.  An infinite a gives NaN in da, and minus infinity in h and
+ * db too. */
 int swiglu_fwd(const void* u, void* h, void* u_q, void* u_e, int rows, int f, void* stream);
 
 /* Its backward from dh, bf16 [rows, f], and either u (u_q, u_e NULL) or its
