@@ -31,7 +31,9 @@ __all__ = ["attn_fwd", "attn_bwd", "attn_bwd_delta", "attn_bwd_dkdv", "attn_bwd_
            "layer_train_step", "ds_workspace_bytes", "set_bwd_dq_mode", "Act8", "act8_pack",
            "act8_unpack", "act8_wgrad", "act8_wgrad_workspace_bytes", "swiglu_fwd", "swiglu_bwd",
            "BlockNormKept", "BlockNormGrads", "block_norm_fwd", "block_norm_bwd",
-           "block_norm_bwd_workspace_bytes"]
+           "block_norm_bwd_workspace_bytes", "rope_freqs", "rope_fwd", "rope_bwd", "linear_ce_fwd",
+           "linear_ce_fwd_workspace_bytes", "linear_ce_bwd", "linear_ce_bwd_workspace_bytes",
+           "muon_update", "muon_update_workspace_bytes"]
 
 STATUS = {0: "DETATTN_OK", -1: "DETATTN_ERR_NULL", -2: "DETATTN_ERR_ALIGN",
           -3: "DETATTN_ERR_SHAPE", -4: "DETATTN_ERR_HEADDIM", -5: "DETATTN_ERR_SCALE",
@@ -101,6 +103,18 @@ def lib() -> ctypes.CDLL:
     L.block_norm_bwd_workspace_bytes.argtypes = [i, i, i]
     L.block_norm_bwd_workspace_bytes.restype = sz
     L.block_norm_bwd.argtypes = [vp] * 19 + [sz] + [i] * 6 + [f] * 2 + [vp]
+    ll, db = ctypes.c_longlong, ctypes.c_double
+    L.rope_freqs.argtypes = [vp, vp, i, db, i, db, i, db, db]
+    L.rope_fwd.argtypes = L.rope_bwd.argtypes = [vp] * 6 + [i] + [ll] * 4 + [i] * 8 + [f, vp]
+    L.linear_ce_fwd_workspace_bytes.argtypes = L.linear_ce_bwd_workspace_bytes.argtypes = [i] * 3
+    L.linear_ce_fwd_workspace_bytes.restype = L.linear_ce_bwd_workspace_bytes.restype = sz
+    L.linear_ce_fwd.argtypes = [vp] * 6 + [sz] + [i] * 3 + [vp]
+    L.linear_ce_bwd.argtypes = [vp] * 9 + [sz] + [i] * 4 + [vp]
+    L.muon_update_workspace_bytes.argtypes = [i] * 3
+    L.muon_update_workspace_bytes.restype = sz
+    L.muon_update.argtypes = [vp] * 4 + [sz] + [i] * 6 + [vp, f, f, vp]
+    for name in ("rope_freqs", "rope_fwd", "rope_bwd", "linear_ce_fwd", "linear_ce_bwd", "muon_update"):
+        getattr(L, name).restype = i
     for name in ("act8_pack", "act8_unpack", "act8_wgrad", "swiglu_fwd", "swiglu_bwd",
                  "block_norm_fwd", "block_norm_bwd"):
         getattr(L, name).restype = i
@@ -756,6 +770,219 @@ def block_norm_bwd(dx_out, dh, kept, gate=None, w_post=None, w_pre=None, res_sca
         gate is not None and gate.dtype is f32, bool(gate_sigmoid), res_scale, block_scale,
         _stream()), "block_norm_bwd")
     return BlockNormGrads(dx, dy, dgate, dwo, dwp)
+
+
+# ------------------------------------------------------------ the ends of a training step
+_ROPE_KINDS = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+
+
+def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, context=0, low=1.0, high=None,
+               device="cuda"):
+    """(freqs, mscale) for rope_fwd: the angles per position, float64 [rot / 2]
+    on `device`, and the factor of the results.  scaling: None, "linear", "base",
+    "ramp" or "bands" (kinds 0 to 4 of include/detattn.h), `high` 32 turns for a
+    ramp and 4 for bands unless given."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {list(_ROPE_KINDS)}, got {scaling!r}")
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
+    rot = int(rot)
+    f = (ctypes.c_double * max(1, min(rot, 1024) // 2))()
+    m = ctypes.c_float(1.0)
+    _check(lib().rope_freqs(f, ctypes.byref(m), rot, base, _ROPE_KINDS[scaling], factor,
+                            context, low, high), "rope_freqs")
+    return torch.tensor(list(f), dtype=torch.float64, device=device), m.value
+
+
+def _heads(t, name, dev):
+    """(tokens, T, H, D, token stride) of a [..., T, H, D] tensor whose heads and
+    components are contiguous and whose tokens lie one stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [..., T, H, D], got {tuple(t.shape)}")
+    T, H, D = t.shape[-3:]
+    tokens = t.numel() // max(1, H * D)
+    st = t.stride()
+    if tokens and ((D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D)):
+        raise ValueError(f"{name}: heads and components must be contiguous, strides {st}")
+    ld, span = H * D, None
+    for n, s in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
+        if n == 1 or not tokens:
+            continue
+        if span is None:
+            ld = s
+        elif s != span:
+            raise ValueError(f"{name}: tokens must lie one stride apart, strides {st}")
+        span = s * n
+    return tokens, T, H, D, ld
+
+
+def _rope(call, where, q, k, freqs, positions, interleaved, mscale, q_out, k_out):
+    if q is None:
+        raise TypeError("q must be a torch.Tensor")
+    dev = _current(q, "q")
+    N, T, Hq, D, q_ld = _heads(q, "q", dev)
+    Hkv, k_ld, ko_ld = 0, 0, 0
+    if k is not None:
+        Nk, _, Hkv, Dk, k_ld = _heads(k, "k", dev)
+        if k.dtype is not q.dtype or Dk != D or k.shape[:-2] != q.shape[:-2]:
+            raise ValueError(f"k is {k.dtype} {tuple(k.shape)}, q {q.dtype} {tuple(q.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    outs = []
+    for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if t is None:
+            outs.append((None, 0))
+        elif o is None:
+            outs.append((torch.empty(t.shape, dtype=t.dtype, device=t.device), t.shape[-2] * D))
+        else:
+            ld = _heads(o, name, dev)[4]
+            if o.dtype is not t.dtype or o.shape != t.shape:
+                raise ValueError(f"{name} is {o.dtype} {tuple(o.shape)}, expected {t.dtype} {tuple(t.shape)}")
+            outs.append((o, ld))
+    (qo, qo_ld), (ko, ko_ld) = outs
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise TypeError("freqs must be a float64 tensor [rot / 2]")
+    _on_device(freqs, "freqs", torch.float64, freqs.shape, dev)
+    n_pos = 0
+    if positions is not None:
+        _on_device(positions, "positions", torch.int32, positions.shape, dev)
+        n_pos = positions.numel()
+        if tuple(positions.shape) not in ((T,), tuple(q.shape[:-2])):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(T,)} or {tuple(q.shape[:-2])}")
+    if N:
+        _check(call(q.data_ptr(), _addr(k), qo.data_ptr(), _addr(ko), freqs.data_ptr(), _addr(positions),
+                    n_pos, q_ld, k_ld, qo_ld, ko_ld, N, T, Hq, Hkv, D, 2 * freqs.numel(), bool(interleaved),
+                    q.dtype is torch.float32, mscale, _stream()), where)
+    return qo, ko
+
+
+def rope_fwd(q, k, freqs, positions=None, interleaved=False, mscale=1.0, q_out=None, k_out=None):
+    """Rotary positions of q [..., T, Hq, D] and k [..., T, Hkv, D] (None: q
+    alone), bf16 or fp32, on the first 2 freqs.numel() components of every head:
+    returns (q, k) turned, new and contiguous unless q_out, k_out are given (q and k
+    themselves for in place).  q and k may be parts of a joined projection
+    (tokens one stride apart).  freqs: float64 on the device (rope_freqs);
+    positions int32 [T] or [..., T] (None: 0 .. T - 1)."""
+    return _rope(lib().rope_fwd, "rope_fwd", q, k, freqs, positions, interleaved, mscale, q_out, k_out)
+
+
+def rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=1.0, dq_out=None, dk_out=None):
+    """The gradients of rope_fwd's q and k from those of its results."""
+    return _rope(lib().rope_bwd, "rope_bwd", dq, dk, freqs, positions, interleaved, mscale, dq_out, dk_out)
+
+
+@functools.lru_cache(maxsize=256)
+def linear_ce_fwd_workspace_bytes(N, V, d) -> int:
+    return int(lib().linear_ce_fwd_workspace_bytes(N, V, d))
+
+
+@functools.lru_cache(maxsize=256)
+def linear_ce_bwd_workspace_bytes(N, V, d) -> int:
+    return int(lib().linear_ce_bwd_workspace_bytes(N, V, d))
+
+
+def _workspace(workspace, size, dev, device):
+    if workspace is None:
+        return torch.empty((max(16, size),), dtype=torch.uint8, device=device), max(16, size)
+    return workspace, _workspace_size(workspace, dev)
+
+
+def _linear_ce(x, w, targets):
+    N, d = _rows(x, "x")
+    dev = _current(x, "x")
+    _on_device(x, "x", torch.bfloat16, x.shape, dev)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise TypeError("w must be a torch.Tensor [V, d]")
+    _on_device(w, "w", torch.bfloat16, (w.shape[0], d), dev)
+    _on_device(targets, "targets", torch.int32, x.shape[:-1], dev)
+    return N, d, w.shape[0], dev
+
+
+def linear_ce_fwd(x, w, targets, loss=None, lse=None, workspace=None):
+    """Softmax cross entropy of the logits x w^T, which are not kept: x bf16 [..., d],
+    w bf16 [V, d], targets int32 [...] (negative: none).  Returns (loss, lse) fp32
+    [...], loss 0 where there is no target."""
+    N, d, V, dev = _linear_ce(x, w, targets)
+    out = []
+    for t, name in ((loss, "loss"), (lse, "lse")):
+        if t is None:
+            t = torch.empty(targets.shape, dtype=torch.float32, device=x.device)
+        else:
+            _on_device(t, name, torch.float32, targets.shape, dev)
+        out.append(t)
+    workspace, size = _workspace(workspace, linear_ce_fwd_workspace_bytes(N, V, d), dev, x.device)
+    _check(lib().linear_ce_fwd(x.data_ptr(), w.data_ptr(), targets.data_ptr(), out[0].data_ptr(),
+                               out[1].data_ptr(), workspace.data_ptr(), size, N, V, d, _stream()),
+           "linear_ce_fwd")
+    return tuple(out)
+
+
+def linear_ce_bwd(x, w, targets, lse, dloss, dlse=None, dx=None, dw=None, dw_fp32=False, workspace=None):
+    """Gradients (dx bf16 [..., d], dw [V, d], bf16 or with dw_fp32 fp32) of
+    linear_ce_fwd from dloss and dlse (None: zero), fp32 [...]; lse is the forward's."""
+    N, d, V, dev = _linear_ce(x, w, targets)
+    f32 = torch.float32
+    _on_device(lse, "lse", f32, targets.shape, dev)
+    _on_device(dloss, "dloss", f32, targets.shape, dev)
+    if dlse is not None:
+        _on_device(dlse, "dlse", f32, targets.shape, dev)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _on_device(dx, "dx", x.dtype, x.shape, dev)
+    if dw is None:
+        dw = torch.empty((V, d), dtype=f32 if dw_fp32 else x.dtype, device=x.device)
+    else:
+        _on_device(dw, "dw", f32 if dw_fp32 else x.dtype, (V, d), dev)
+    workspace, size = _workspace(workspace, linear_ce_bwd_workspace_bytes(N, V, d), dev, x.device)
+    _check(lib().linear_ce_bwd(x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                               dloss.data_ptr(), _addr(dlse), dx.data_ptr(), dw.data_ptr(),
+                               workspace.data_ptr(), size, N, V, d, bool(dw_fp32), _stream()),
+           "linear_ce_bwd")
+    return dx, dw
+
+
+@functools.lru_cache(maxsize=256)
+def muon_update_workspace_bytes(batch, m, n) -> int:
+    return int(lib().muon_update_workspace_bytes(batch, m, n))
+
+
+def muon_update(g, momentum=None, beta=0.95, nesterov=True, steps=5, coeffs=None, eps=1e-7, out=None,
+                workspace=None):
+    """The orthogonalised update (include/detattn.h) of the gradients g [..., m, n],
+    bf16 or fp32, as bf16; momentum fp32 of g's shape is updated in place.
+    coeffs: (a, b, c) for each of the steps (None: one set for all)."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    if g.dim() < 2 or g.shape[-1] == 0 or g.shape[-2] == 0:
+        raise ValueError(f"g must be [..., m, n], got {tuple(g.shape)}")
+    dev = _current(g, "g")
+    _need_stream(g, "g", g.shape, dev)
+    m, n = g.shape[-2:]
+    batch = g.numel() // (m * n)
+    if momentum is not None:
+        _on_device(momentum, "momentum", torch.float32, g.shape, dev)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    else:
+        _on_device(out, "out", torch.bfloat16, g.shape, dev)
+    c = None
+    if coeffs is not None:
+        flat = [float(v) for row in coeffs for v in row]
+        if len(flat) != 3 * steps:
+            raise ValueError(f"coeffs must be (a, b, c) for each of {steps} steps")
+        c = (ctypes.c_float * len(flat))(*flat)
+    workspace, size = _workspace(workspace, muon_update_workspace_bytes(batch, m, n), dev, g.device)
+    _check(lib().muon_update(g.data_ptr(), _addr(momentum), out.data_ptr(), workspace.data_ptr(), size,
+                             batch, m, n, g.dtype is torch.float32, bool(nesterov), steps, c, beta, eps,
+                             _stream()), "muon_update")
+    return out
 
 
 def embed_grad_workspace_bytes(N, V, E) -> int:

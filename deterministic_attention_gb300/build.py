@@ -17,7 +17,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdetattn.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["attn_fwd.cu", "attn_bwd.cu", "attn_dq_ds.cu", "embed_grad.cu", "layer_ops.cu",
-           "block_norm.cu", "act8_ops.cu", "act8_wgrad.cu", "detattn_host.cu"]
+           "block_norm.cu", "act8_ops.cu", "act8_wgrad.cu", "rope.cu", "linear_ce.cu", "muon.cu",
+           "detattn_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

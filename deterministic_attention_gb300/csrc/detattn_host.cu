@@ -21,6 +21,7 @@
 #include "block_launch.h"
 #include "embed_launch.h"
 #include "layer_launch.h"
+#include "step_launch.h"
 
 using namespace detattn;
 
@@ -1258,6 +1259,204 @@ NormLayout norm_layout(const BlockNormBwdPlan& p, int d) {
   return l;
 }
 
+// ------------------------------------------------------------ ends of a training step
+// 3-D map of 16-bit matrices: `batch` of `outer` rows of `inner` contiguous
+// elements (row stride ld, matrix stride `matrix`, in elements), boxes of 64
+// columns and `box_outer` rows, 128-byte swizzle.  Reads past inner, outer give zero.
+int encode_3d(CUtensorMap* m, const void* ptr, long inner, long outer, long batch, long ld, long matrix,
+              int box_outer, const char* what) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                        static_cast<cuuint64_t>(batch)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(matrix) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_outer), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DETATTN_ERR_CUDA, "tensor map for %s: CUresult %d", what, (int)r);
+  return DETATTN_OK;
+}
+// An operand with K contiguous (its rows are the tile's rows), or with K along
+// its rows.
+int encode_rows_of_k(CUtensorMap* m, const void* p, long k, long rows, long batch, long ld, long matrix,
+                     const char* what) {
+  return encode_3d(m, p, k, rows, batch, ld, matrix, 128, what);
+}
+int encode_k_rows(CUtensorMap* m, const void* p, long cols, long k, long batch, long ld, long matrix,
+                  const char* what) {
+  return encode_3d(m, p, cols, k, batch, ld, matrix, 64, what);
+}
+
+int check_step_workspace(const void* w, size_t bytes, size_t need, const char* what) {
+  if (w == nullptr || bytes < need)
+    return fail(DETATTN_ERR_WORKSPACE, "%s workspace needs %zu bytes, got %zu%s", what, need, bytes,
+                w ? "" : " (NULL)");
+  if (!aligned16(w)) return fail(DETATTN_ERR_ALIGN, "workspace is not 16-byte aligned");
+  return DETATTN_OK;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_rope(int N, int T, int Hq, int Hkv, int D, int rot, long long n_pos,
+               std::initializer_list<long long> q_ld, std::initializer_list<long long> k_ld) {
+  if (N < 0 || N > (1 << 30)) return fail(DETATTN_ERR_SHAPE, "N=%d tokens: must be in [0, 2^30]", N);
+  if (T < 1) return fail(DETATTN_ERR_SHAPE, "T=%d must be >= 1", T);
+  if (Hq < 0 || Hkv < 0 || Hq + Hkv < 1 || Hq > 4096 || Hkv > 4096)
+    return fail(DETATTN_ERR_SHAPE, "Hq=%d Hkv=%d: in [0, 4096], one at least", Hq, Hkv);
+  if (D < 2 || D > 1024) return fail(DETATTN_ERR_HEADDIM, "D=%d: must be in [2, 1024]", D);
+  if (rot < 2 || rot > D || rot % 2 != 0)
+    return fail(DETATTN_ERR_HEADDIM, "rot=%d: must be even, in [2, D=%d]", rot, D);
+  if (n_pos < 0) return fail(DETATTN_ERR_SHAPE, "n_pos=%lld", n_pos);
+  for (long long ld : q_ld)
+    if (ld < static_cast<long long>(Hq) * D)
+      return fail(DETATTN_ERR_SHAPE, "a token's stride %lld is shorter than its %d heads of %d", ld, Hq, D);
+  for (long long ld : k_ld)
+    if (ld < static_cast<long long>(Hkv) * D)
+      return fail(DETATTN_ERR_SHAPE, "a token's stride %lld is shorter than its %d heads of %d", ld, Hkv, D);
+  return DETATTN_OK;
+}
+
+int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const double* freqs,
+              const int* positions, int n_pos, long long q_ld, long long k_ld, long long q_out_ld,
+              long long k_out_ld, int N, int T, int Hq, int Hkv, int D, int rot, int interleaved, int fp32,
+              float mscale, float sign, void* stream, const char* what) {
+  int rc;
+  if ((rc = check_rope(N, T, Hq, Hkv, D, rot, n_pos, {q_ld, q_out_ld}, {k_ld, k_out_ld})) != DETATTN_OK)
+    return rc;
+  if ((rc = check_flags({interleaved, fp32})) != DETATTN_OK) return rc;
+  if (!std::isfinite(mscale)) return fail(DETATTN_ERR_SCALE, "mscale=%g must be finite", static_cast<double>(mscale));
+  if (N == 0) return ok_status();
+  const int size = fp32 ? 4 : 2;
+  if ((rc = check_norm_ptrs({{q, Hq > 0, size, "q"},
+                             {q_out, Hq > 0, size, "q_out"},
+                             {k, Hkv > 0, size, "k"},
+                             {k_out, Hkv > 0, size, "k_out"},
+                             {freqs, true, 8, "freqs"},
+                             {positions, positions != nullptr, 4, "positions"}})) != DETATTN_OK)
+    return rc;
+  if ((positions != nullptr) != (n_pos > 0))
+    return fail(DETATTN_ERR_SHAPE, "positions and n_pos=%d go together", n_pos);
+  if (q != nullptr && q == q_out && q_ld != q_out_ld)
+    return fail(DETATTN_ERR_SHAPE, "q in place needs one stride");
+  if (k != nullptr && k == k_out && k_ld != k_out_ld)
+    return fail(DETATTN_ERR_SHAPE, "k in place needs one stride");
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  TurnArgs a{};
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.freqs = freqs;
+  a.positions = positions;
+  a.tokens = N;
+  a.n_pos = n_pos;
+  a.q_ld = static_cast<long>(q_ld);
+  a.k_ld = static_cast<long>(k_ld);
+  a.q_out_ld = static_cast<long>(q_out_ld);
+  a.k_out_ld = static_cast<long>(k_out_ld);
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.fp32 = fp32 != 0;
+  a.mscale = mscale;
+  a.sign = sign;
+  return launched(launch_turn(a, static_cast<cudaStream_t>(stream)), what);
+}
+
+int check_ce_shape(int N, int V, int d) {
+  if (N < 0 || N > (1 << 24)) return fail(DETATTN_ERR_SHAPE, "N=%d rows: must be in [0, 2^24]", N);
+  if (V < 1 || V > (1 << 24)) return fail(DETATTN_ERR_SHAPE, "V=%d words: must be in [1, 2^24]", V);
+  if (d < 8 || d % 8 != 0 || d > (1 << 16))
+    return fail(DETATTN_ERR_SHAPE, "d=%d columns: must be a positive multiple of 8 up to 2^16", d);
+  if (static_cast<double>(N) * d > 1.7e10 || static_cast<double>(V) * d > 1.7e10 ||
+      static_cast<double>(N) * V > 3.0e13)
+    return fail(DETATTN_ERR_SHAPE, "cross entropy too large (N=%d V=%d d=%d)", N, V, d);
+  return DETATTN_OK;
+}
+// Workspace of linear_ce_fwd: the column tiles' (largest, sum) pairs, the
+// targets' logits.
+struct CeFwdLayout {
+  int parts;
+  size_t z, total;
+};
+CeFwdLayout ce_fwd_layout(int N, int V) {
+  CeFwdLayout l{};
+  l.parts = 2 * ((V + kCeTile - 1) / kCeTile);
+  l.z = up256(static_cast<size_t>(l.parts) * N * sizeof(float2));
+  l.total = l.z + up256(static_cast<size_t>(N) * sizeof(float));
+  return l;
+}
+// The vocabulary in pieces whose dz takes at most 512 MB (or one tile's width):
+// all of it where that is enough, else pieces of nearly one size.  Their width is fixed
+// by the shape.
+constexpr double kCePieceBytes = 536870912.0;
+int ce_piece_width(int N, int V) {
+  const long tiles = (V + kCeTile - 1) / kCeTile;
+  long most = static_cast<long>(kCePieceBytes / (2.0 * kCeTile * N));
+  if (most < 1) most = 1;
+  const long pieces = (tiles + most - 1) / most;
+  return static_cast<int>((tiles + pieces - 1) / pieces) * kCeTile;
+}
+struct CeBwdLayout {
+  int width;               // of a piece (the last may be narrower)
+  long ld;                 // of dz
+  size_t unit, acc, partial, total;
+};
+CeBwdLayout ce_bwd_layout(int N, int V, int d) {
+  CeBwdLayout l{};
+  l.width = ce_piece_width(N, V);
+  if (l.width > V) l.width = V;
+  l.ld = (l.width + 63) / 64 * 64;
+  l.unit = up256(static_cast<size_t>(N) * l.ld * 2);
+  l.acc = l.unit + 256;
+  l.partial = l.acc + (l.width < V ? up256(static_cast<size_t>(N) * d * sizeof(float)) : 0);
+  size_t part = 0;
+  const int last = V % l.width == 0 ? l.width : V % l.width;
+  for (int w : {l.width, last}) {
+    part = std::max(part, product_partial_bytes(product_plan(2, N, d, w, 1, false, true), 2));
+    part = std::max(part, product_partial_bytes(product_plan(2, w, d, N, 1, false, true), 2));
+  }
+  l.total = l.partial + up256(part);
+  return l;
+}
+
+int check_muon_shape(int batch, int m, int n) {
+  if (batch < 0 || batch > 65535) return fail(DETATTN_ERR_SHAPE, "batch=%d: must be in [0, 65535]", batch);
+  if (m < 1 || m > 32768) return fail(DETATTN_ERR_SHAPE, "m=%d rows: must be in [1, 32768]", m);
+  if (n < 8 || n % 8 != 0 || n > 32768)
+    return fail(DETATTN_ERR_SHAPE, "n=%d columns: must be a positive multiple of 8 up to 32768", n);
+  if (static_cast<double>(batch) * m * n > 1.7e10)
+    return fail(DETATTN_ERR_SHAPE, "update too large (batch=%d m=%d n=%d)", batch, m, n);
+  return DETATTN_OK;
+}
+struct MuonLayout {
+  int side, blocks;        // the shorter side; blocks per matrix that sum squares
+  long ld;                 // of the side x side matrices
+  size_t x0, x1, gram, poly, total;
+};
+MuonLayout muon_layout(int batch, int m, int n) {
+  MuonLayout l{};
+  l.side = std::min(m, n);
+  l.ld = (l.side + 7) / 8 * 8;
+  l.blocks = muon_sum_blocks(batch, static_cast<long>(m) * n);
+  const size_t x = up256(static_cast<size_t>(batch) * m * n * 2);
+  const size_t s = up256(static_cast<size_t>(batch) * l.side * l.ld * 2);
+  l.x0 = up256(static_cast<size_t>(batch) * l.blocks * sizeof(double));
+  l.x1 = l.x0 + x;
+  l.gram = l.x1 + x;
+  l.poly = l.gram + s;
+  l.total = l.poly + s;
+  return l;
+}
+// Two blocks on a tile of 256 x 256, or one on 128 x 128.
+int muon_ctas(int batch, int m, int n) {
+  (void)batch, (void)m, (void)n;
+  return 2;
+}
+
 }  // namespace
 
 namespace detattn {
@@ -1903,6 +2102,228 @@ int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void
   return launched(launch_block_norm_bwd(a, x_fp32 != 0, st), "block_norm_bwd");
 }
 
+int rope_freqs(double* freqs, float* mscale, int rot, double base, int kind, double factor, int context,
+               double low, double high) {
+  if (freqs == nullptr || mscale == nullptr) return fail(DETATTN_ERR_NULL, "freqs and mscale must not be NULL");
+  if (rot < 2 || rot % 2 != 0 || rot > 1024)
+    return fail(DETATTN_ERR_HEADDIM, "rot=%d: must be even, in [2, 1024]", rot);
+  if (kind < 0 || kind > 4) return fail(DETATTN_ERR_SHAPE, "kind=%d: must be 0 to 4", kind);
+  if (!std::isfinite(base) || !(base > 1.0)) return fail(DETATTN_ERR_SCALE, "base=%g must be > 1", base);
+  if (kind != 0 && (!std::isfinite(factor) || !(factor >= 1.0)))
+    return fail(DETATTN_ERR_SCALE, "factor=%g must be >= 1", factor);
+  if (kind == 2 && rot == 2) return fail(DETATTN_ERR_HEADDIM, "a scaled base needs rot > 2");
+  if (kind >= 3 && (context < 1 || !std::isfinite(high) || !(low > 0.0) || !(high > low)))
+    return fail(DETATTN_ERR_SCALE, "context=%d, low=%g, high=%g: needs context >= 1 and 0 < low < high",
+                context, low, high);
+  const double pi2 = 6.283185307179586;
+  const int n = rot / 2;
+  *mscale = kind == 3 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+  if (kind == 2) base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+  // kind 3: the pairs' numbers at which `high` and `low` turns fit the context.
+  auto pair_at = [&](double turns) { return rot * std::log(context / (turns * pi2)) / (2.0 * std::log(base)); };
+  double lo = 0.0, hi = 0.0;
+  if (kind == 3) {
+    lo = std::max(std::floor(pair_at(high)), 0.0);
+    hi = std::min(std::ceil(pair_at(low)), static_cast<double>(rot - 1));
+  }
+  for (int i = 0; i < n; ++i) {
+    double f = std::pow(base, -2.0 * i / rot), keep = 1.0;
+    if (kind == 1) keep = 0.0;
+    if (kind == 3) keep = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+    if (kind == 4) keep = std::min(std::max((context * f / pi2 - low) / (high - low), 0.0), 1.0);
+    if (kind == 1 || kind >= 3) f *= keep + (1.0 - keep) / factor;
+    freqs[i] = f;
+  }
+  return ok_status();
+}
+
+int rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const double* freqs,
+             const int* positions, int n_pos, long long q_ld, long long k_ld, long long q_out_ld,
+             long long k_out_ld, int N, int T, int Hq, int Hkv, int D, int rot, int interleaved, int fp32,
+             float mscale, void* stream) {
+  return rope_impl(q, k, q_out, k_out, freqs, positions, n_pos, q_ld, k_ld, q_out_ld, k_out_ld, N, T, Hq,
+                   Hkv, D, rot, interleaved, fp32, mscale, 1.0f, stream, "rope_fwd");
+}
+
+int rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const double* freqs,
+             const int* positions, int n_pos, long long dq_ld, long long dk_ld, long long dq_out_ld,
+             long long dk_out_ld, int N, int T, int Hq, int Hkv, int D, int rot, int interleaved, int fp32,
+             float mscale, void* stream) {
+  return rope_impl(dq, dk, dq_out, dk_out, freqs, positions, n_pos, dq_ld, dk_ld, dq_out_ld, dk_out_ld, N,
+                   T, Hq, Hkv, D, rot, interleaved, fp32, mscale, -1.0f, stream, "rope_bwd");
+}
+
+size_t linear_ce_fwd_workspace_bytes(int N, int V, int d) {
+  if (check_ce_shape(N, V, d) != DETATTN_OK || N == 0) return 0;
+  return ce_fwd_layout(N, V).total;
+}
+
+int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss, float* lse,
+                  void* workspace, size_t workspace_bytes, int N, int V, int d, void* stream) {
+  int rc;
+  if ((rc = check_ce_shape(N, V, d)) != DETATTN_OK) return rc;
+  if (N == 0) return ok_status();
+  if ((rc = check_ptrs({{x, "x"}, {w, "w"}, {targets, "targets"}, {loss, "loss"}, {lse, "lse"}})) != DETATTN_OK)
+    return rc;
+  const CeFwdLayout l = ce_fwd_layout(N, V);
+  if ((rc = check_step_workspace(workspace, workspace_bytes, l.total, "linear_ce_fwd")) != DETATTN_OK) return rc;
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap mx, mw;
+  if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, static_cast<long>(N) * d, "x")) != DETATTN_OK) return rc;
+  if ((rc = encode_rows_of_k(&mw, w, d, V, 1, d, static_cast<long>(V) * d, "w")) != DETATTN_OK) return rc;
+  ProductPlan p = product_plan(2, N, V, d, 1, false, false);
+  p.wait_ns = g_wait_ns;
+  char* ws = static_cast<char*>(workspace);
+  float2* part = reinterpret_cast<float2*>(ws);
+  float* z = reinterpret_cast<float*>(ws + l.z);
+  if ((rc = launched(launch_ce_stats(mx, mw, p, {targets, part, z, N, V}, st), "linear_ce_fwd")) != DETATTN_OK)
+    return rc;
+  return launched(launch_ce_finish({targets, part, z, loss, lse, N, V, l.parts}, st), "linear_ce_fwd (merge)");
+}
+
+size_t linear_ce_bwd_workspace_bytes(int N, int V, int d) {
+  if (check_ce_shape(N, V, d) != DETATTN_OK || N == 0) return 0;
+  return ce_bwd_layout(N, V, d).total;
+}
+
+int linear_ce_bwd(const void* x, const void* w, const int* targets, const float* lse, const float* dloss,
+                  const float* dlse, void* dx, void* dw, void* workspace, size_t workspace_bytes, int N,
+                  int V, int d, int dw_fp32, void* stream) {
+  int rc;
+  if ((rc = check_ce_shape(N, V, d)) != DETATTN_OK) return rc;
+  if ((rc = check_flags({dw_fp32})) != DETATTN_OK) return rc;
+  if ((rc = check_ptrs({{dw, "dw"}})) != DETATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t dw_size = dw_fp32 ? sizeof(float) : 2;
+  if (N == 0) {
+    if ((rc = check_device()) != DETATTN_OK) return rc;
+    return launched(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * d * dw_size, st), "linear_ce_bwd (zeros)");
+  }
+  if ((rc = check_ptrs({{x, "x"}, {w, "w"}, {targets, "targets"}, {lse, "lse"}, {dloss, "dloss"}, {dx, "dx"}})) !=
+      DETATTN_OK)
+    return rc;
+  if (dlse != nullptr && !aligned16(dlse)) return fail(DETATTN_ERR_ALIGN, "dlse is not 16-byte aligned");
+  const CeBwdLayout l = ce_bwd_layout(N, V, d);
+  if ((rc = check_step_workspace(workspace, workspace_bytes, l.total, "linear_ce_bwd")) != DETATTN_OK) return rc;
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  const char* wb = static_cast<const char*>(w);
+  float* acc = reinterpret_cast<float*>(ws + l.acc);
+  float* partial = reinterpret_cast<float*>(ws + l.partial);
+  float* unit = reinterpret_cast<float*>(ws + l.unit);
+  const long nd = static_cast<long>(N) * d;
+  CUtensorMap mx, mxk;
+  if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, nd, "x")) != DETATTN_OK) return rc;
+  if ((rc = encode_k_rows(&mxk, x, d, N, 1, d, nd, "x")) != DETATTN_OK) return rc;
+  if ((rc = launched(launch_ce_unit(targets, dloss, unit, N, V, st), "linear_ce_bwd (unit)")) != DETATTN_OK)
+    return rc;
+  for (int v0 = 0; v0 < V; v0 += l.width) {
+    const int width = std::min(l.width, V - v0);
+    const bool first = v0 == 0, last = v0 + width == V;
+    const void* wp = wb + static_cast<size_t>(v0) * d * 2;
+    const long wd = static_cast<long>(width) * d, nz = static_cast<long>(N) * l.ld;
+    CUtensorMap mw, mwk, mz, mzk;
+    if ((rc = encode_rows_of_k(&mw, wp, d, width, 1, d, wd, "w")) != DETATTN_OK) return rc;
+    if ((rc = encode_k_rows(&mwk, wp, d, width, 1, d, wd, "w")) != DETATTN_OK) return rc;
+    if ((rc = encode_rows_of_k(&mz, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
+    if ((rc = encode_k_rows(&mzk, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
+    ProductPlan p = product_plan(2, N, width, d, 1, false, false);
+    p.wait_ns = g_wait_ns;
+    CeGradArgs ga{targets, lse, dloss, dlse, unit, ws, N, V, v0, width, l.ld};
+    if ((rc = launched(launch_ce_dz(mx, mw, p, ga, st), "linear_ce_bwd (dz)")) != DETATTN_OK) return rc;
+    p = product_plan(2, N, d, width, 1, false, true);
+    p.wait_ns = g_wait_ns;
+    CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0};
+    if ((rc = launched(launch_ce_dx(mz, mwk, p, sa, st), "linear_ce_bwd (dx)")) != DETATTN_OK) return rc;
+    p = product_plan(2, width, d, N, 1, false, true);
+    p.wait_ns = g_wait_ns;
+    sa = {unit, static_cast<char*>(dw) + static_cast<size_t>(v0) * d * dw_size, nullptr, partial, width, d, 0, dw_fp32};
+    if ((rc = launched(launch_ce_dw(mzk, mxk, p, sa, st), "linear_ce_bwd (dw)")) != DETATTN_OK) return rc;
+  }
+  return ok_status();
+}
+
+size_t muon_update_workspace_bytes(int batch, int m, int n) {
+  if (check_muon_shape(batch, m, n) != DETATTN_OK || batch == 0) return 0;
+  return muon_layout(batch, m, n).total;
+}
+
+int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t workspace_bytes, int batch,
+                int m, int n, int g_fp32, int nesterov, int steps, const float* coeffs, float beta, float eps,
+                void* stream) {
+  int rc;
+  if ((rc = check_muon_shape(batch, m, n)) != DETATTN_OK) return rc;
+  if ((rc = check_flags({g_fp32, nesterov})) != DETATTN_OK) return rc;
+  if (steps < 1 || steps > 64) return fail(DETATTN_ERR_SHAPE, "steps=%d: must be in [1, 64]", steps);
+  if (!std::isfinite(beta) || !std::isfinite(eps) || !(eps >= 1e-30f))
+    return fail(DETATTN_ERR_SCALE, "beta=%g must be finite, eps=%g at least 1e-30", static_cast<double>(beta),
+                static_cast<double>(eps));
+  for (int i = 0; coeffs != nullptr && i < 3 * steps; ++i)
+    if (!std::isfinite(coeffs[i]))
+      return fail(DETATTN_ERR_SCALE, "coefficient %d of step %d is not finite", i % 3, i / 3);
+  if (batch == 0) return ok_status();
+  if ((rc = check_ptrs({{g, "g"}, {o, "o"}})) != DETATTN_OK) return rc;
+  if (!aligned16(momentum)) return fail(DETATTN_ERR_ALIGN, "momentum is not 16-byte aligned");
+  const MuonLayout l = muon_layout(batch, m, n);
+  if ((rc = check_step_workspace(workspace, workspace_bytes, l.total, "muon_update")) != DETATTN_OK) return rc;
+  if ((rc = check_device()) != DETATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const bool wide = m <= n;
+  const int s = l.side, ctas = muon_ctas(batch, m, n);
+  const long mn = static_cast<long>(m) * n, ss = static_cast<long>(s) * l.ld;
+  MuonInArgs in{};
+  in.g = g;
+  in.momentum = momentum;
+  in.sums = reinterpret_cast<double*>(ws);
+  in.x = ws + l.x0;
+  in.count = mn;
+  in.batch = batch;
+  in.blocks = l.blocks;
+  in.g_fp32 = g_fp32 != 0;
+  in.nesterov = nesterov != 0;
+  in.beta = beta;
+  in.eps = eps;
+  // X in either buffer, as rows and as columns of K; the symmetric matrices.
+  CUtensorMap xr[2], xk[2], mg, mp;
+  for (int i = 0; i < 2; ++i) {
+    const void* x = ws + (i ? l.x1 : l.x0);
+    if ((rc = encode_rows_of_k(&xr[i], x, n, m, batch, n, mn, "X")) != DETATTN_OK) return rc;
+    if ((rc = encode_k_rows(&xk[i], x, n, m, batch, n, mn, "X")) != DETATTN_OK) return rc;
+  }
+  if ((rc = encode_rows_of_k(&mg, ws + l.gram, s, s, batch, l.ld, ss, "X X^T")) != DETATTN_OK) return rc;
+  if ((rc = encode_rows_of_k(&mp, ws + l.poly, s, s, batch, l.ld, ss, "P")) != DETATTN_OK) return rc;
+  ProductPlan gram = product_plan(ctas, s, s, wide ? n : m, batch, true, false);
+  ProductPlan poly = product_plan(ctas, s, s, s, batch, true, false);
+  ProductPlan full = product_plan(ctas, m, n, s, batch, false, false);
+  gram.wait_ns = poly.wait_ns = full.wait_ns = g_wait_ns;
+  if ((rc = launched(launch_muon_momentum(in, st), "muon_update (momentum)")) != DETATTN_OK) return rc;
+  if ((rc = launched(launch_muon_scale(in, st), "muon_update (scale)")) != DETATTN_OK) return rc;
+  for (int i = 0; i < steps; ++i) {
+    const float c[3] = {coeffs ? coeffs[3 * i] : 3.4445f, coeffs ? coeffs[3 * i + 1] : -4.7750f,
+                        coeffs ? coeffs[3 * i + 2] : 2.0315f};
+    const int cur = i & 1;
+    const bool last = i == steps - 1;
+    // A (stored times kMuonX) = X X^T; P (times kMuonP) = a I + b A + c A A.
+    MuonStoreArgs a{ws + l.gram, nullptr, ss, s, s, l.ld, 1.0f / kMuonX, 0.0f, 0.0f, 0};
+    const CUtensorMap& x = wide ? xr[cur] : xk[cur];
+    if ((rc = launched(launch_muon_product(x, x, ctas, !wide, !wide, gram, a, st), "muon_update (gram)")) != DETATTN_OK)
+      return rc;
+    a = {ws + l.poly, ws + l.gram, ss, s, s, l.ld, c[2] * kMuonP / (kMuonX * kMuonX), c[1] * kMuonP / kMuonX,
+         c[0] * kMuonP, 0};
+    if ((rc = launched(launch_muon_product(mg, mg, ctas, false, false, poly, a, st), "muon_update (polynomial)")) !=
+        DETATTN_OK)
+      return rc;
+    a = {last ? o : ws + (cur ? l.x0 : l.x1), nullptr, mn, m, n, n, last ? 1.0f / (kMuonX * kMuonP) : 1.0f / kMuonP,
+         0.0f, 0.0f, last ? 1 : 0};
+    rc = wide ? launched(launch_muon_product(mp, xk[cur], ctas, false, true, full, a, st), "muon_update (P X)")
+              : launched(launch_muon_product(xr[cur], mp, ctas, false, false, full, a, st), "muon_update (X P)");
+    if (rc != DETATTN_OK) return rc;
+  }
+  return ok_status();
+}
+
 int detattn_check_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned f = 0, b = 0, em = 0, ly = 0;
@@ -1916,19 +2337,24 @@ int detattn_check_status(void* stream) {
   unsigned wg = 0, nm = 0;
   if (e == cudaSuccess) e = take_wgrad_status(st, &wg);
   if (e == cudaSuccess) e = take_norm_status(st, &nm);
+  unsigned ce = 0, mu = 0;
+  if (e == cudaSuccess) e = take_ce_status(st, &ce);
+  if (e == cudaSuccess) e = take_muon_status(st, &mu);
   if (e != cudaSuccess) return fail(DETATTN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (em & 1u)
     return fail(DETATTN_ERR_INDEX,
                 "embed_grad found token ids outside [0, V); those tokens were left out of dw");
+  if (ce & 2u)
+    return fail(DETATTN_ERR_INDEX, "linear_ce found targets >= V; those rows were taken as rows without a target");
   if (b & 16u)
     return fail(DETATTN_ERR_WORKSPACE,
                 "the dQ step found its tile counter not cleared: run attn_bwd_delta on this "
                 "workspace (with the same workspace_bytes) first");
-  if (f | b | ly | wg | nm)
+  if (f | b | ly | wg | nm | ce | mu)
     return fail(DETATTN_ERR_DEVICE_TIMEOUT,
                 "a kernel gave up on a pipeline wait (fwd flags %u, bwd flags %u, layer flags %u, "
-                "act8_wgrad %u, block_norm_bwd %u)",
-                f, b, ly, wg, nm);
+                "act8_wgrad %u, block_norm_bwd %u, linear_ce %u, muon_update %u)",
+                f, b, ly, wg, nm, ce, mu);
   return ok_status();
 }
 
@@ -1999,6 +2425,8 @@ int detattn_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {
   cudaError_t e = launch_wait_timeout_selftest(limit_ns, st);
   if (e == cudaSuccess) e = launch_wgrad_wait_selftest(limit_ns, st);
   if (e == cudaSuccess) e = launch_norm_wait_selftest(limit_ns, st);
+  if (e == cudaSuccess) e = launch_ce_wait_selftest(limit_ns, st);
+  if (e == cudaSuccess) e = launch_muon_wait_selftest(limit_ns, st);
   return launched(e, "detattn_selftest_wait_timeout");
 }
 

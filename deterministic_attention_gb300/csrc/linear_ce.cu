@@ -1,0 +1,363 @@
+// Softmax cross entropy of the output projection without its logits, forward
+// and backward, for sm_103a (oxide-train README: the output projection of a
+// vocabulary of 50,257, padded to 50,432, on bf16 tensor cores):
+//
+//   z = x w^T,  lse_n = ln sum_v exp z_nv,  loss_n = lse_n - z_n,target
+//   dz_nv = (g_n + e_n) exp(z_nv - lse_n) - g_n [v = target_n]
+//   dx = dz w,  dw = dz^T x
+//
+// Forward: one product (product.cuh) whose epilogue leaves, for every row and
+// 128 columns, the largest logit and the sum of exponentials below it, and a
+// second kernel that merges them.  Backward, one piece of the vocabulary after
+// another: the piece's dz as bf16 into the workspace (the logits computed
+// again), then its share of dx, and its rows of dw.  Rounding dz to bf16, which
+// the tensor core's second products need, is the one rounding between the
+// inputs and the results (half a step is 2^-8 of a dz at most); the sums over the
+// vocabulary and over the tokens are in fp32.  dz is held over the largest
+// |dloss|: where all rows weigh the same, as with a mean, a target's dz is then
+// next to -1, which is a bf16 number, and not next to -dloss, whose rounding
+// would be the same in every row and so in dx and dw as a whole (dloss = 1/240:
+// 3.4e-3).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "product.cuh"
+
+namespace detattn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPairs = 2;   // blocks per tile
+constexpr int kSumThreads = 256;
+
+// ------------------------------------------------------------ forward
+struct StatsEpi {
+  static constexpr int kCols = 128;
+  using Args = CeStatsArgs;
+  const Args& a;
+  int row, col, target, part;
+  __device__ __forceinline__ StatsEpi(const Args& args, const product::Unit& w, int r, int c, int)
+      : a(args), row(r), col(c) {
+    target = row < a.N ? a.targets[row] : -1;
+    part = 2 * w.nt + (c >> 7 & 1);
+    if (target >= a.V && c == 0) atomicOr(&g_product_status, 2u);
+  }
+  __device__ __forceinline__ void take(uint32_t taddr) {
+    float m = -INFINITY, s = 0.0f;
+    // (Columns past the vocabulary are those of the last tile.)
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t v[32];
+      __syncwarp();
+      tmem_ld32(taddr + c, v);
+      const int c0 = col + c;
+      if (c0 + 32 > a.V) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c0 + i >= a.V) v[i] = 0xFF800000u;
+      }
+      float t = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) t = fmaxf(t, __uint_as_float(v[i]));
+      const float top = fmaxf(m, t);
+      const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+      float sum[4] = {};
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        sum[i & 3] += ex2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -base));
+      s = s * ex2_approx(m == -INFINITY ? -INFINITY : m * kLog2e - base) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      m = top;
+      const unsigned at = static_cast<unsigned>(target - c0);
+      if (at < 32u && target < a.V) {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z = at == static_cast<unsigned>(i) ? __uint_as_float(v[i]) : z;
+        a.z_target[row] = z;
+      }
+    }
+    if (row < a.N) a.part[static_cast<size_t>(part) * a.N + row] = make_float2(m, s);
+  }
+};
+
+// A block merges 32 rows; 16 threads share a row's parts.  A part's sum is
+// 2^r times what the largest logit asks for, r the rounding of m log2e: it is
+// taken back here, so that loss does not lose what lse does.
+constexpr int kFinishRows = 32, kFinishGroups = 16;
+__global__ void __launch_bounds__(kFinishRows* kFinishGroups) ce_finish_kernel(const CeFinishArgs a) {
+  __shared__ float2 sh[kFinishGroups][kFinishRows];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int row = blockIdx.x * kFinishRows + lane;
+  float m = -INFINITY, s = 0.0f;
+  auto merge = [&](float m1, float s1) {
+    const float top = fmaxf(m, m1);
+    const float base = top == -INFINITY ? 0.0f : top;
+    s = s * exp2f((m - base) * kLog2e) + s1 * exp2f((m1 - base) * kLog2e);
+    m = top;
+  };
+  if (row < a.N) {
+#pragma unroll 4
+    for (int i = group; i < a.parts; i += kFinishGroups) {
+      const float2 p = a.part[static_cast<size_t>(i) * a.N + row];
+      const float b = p.x == -INFINITY ? 0.0f : p.x * kLog2e;
+      const float r = p.x == -INFINITY ? 0.0f : fmaf(p.x, kLog2e, -b);
+      merge(p.x, p.y * exp2f(-r));
+    }
+  }
+  sh[group][lane] = make_float2(m, s);
+  __syncthreads();
+  if (group != 0 || row >= a.N) return;
+  for (int i = 1; i < kFinishGroups; ++i) merge(sh[i][lane].x, sh[i][lane].y);
+  const float ln = logf(s);
+  const int t = a.targets[row];
+  a.lse[row] = m + ln;
+  a.loss[row] = t >= 0 && t < a.V ? (m - a.z_target[row]) + ln : 0.0f;
+}
+
+// ------------------------------------------------------------ backward: dz of a piece
+__global__ void __launch_bounds__(1024) ce_unit_kernel(const int* __restrict__ targets,
+                                                       const float* __restrict__ dloss,
+                                                       float* __restrict__ unit, int N, int V) {
+  __shared__ float sh[32];
+  griddep_launch_dependents();
+  float m = 0.0f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < N; i += 1024) {
+    const int t = targets[i];
+    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
+  }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  m = sh[threadIdx.x];
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (threadIdx.x == 0) *unit = m > 0.0f && m < INFINITY ? m : 1.0f;
+}
+
+struct GradEpi {
+  static constexpr int kCols = 128;
+  using Args = CeGradArgs;
+  const Args& a;
+  int row, col, target;
+  float lse2, g, gp;  // g: dloss, gp: dloss + dlse, over the unit
+  __device__ __forceinline__ GradEpi(const Args& args, const product::Unit&, int r, int c, int)
+      : a(args), row(r), col(c), target(-1), lse2(0.0f), g(0.0f), gp(0.0f) {
+    if (row < a.N) {
+      const float unit = *a.unit;
+      target = a.targets[row];
+      lse2 = a.lse[row] * kLog2e;
+      if (target >= a.V && c == 0 && a.v0 == 0) atomicOr(&g_product_status, 2u);
+      if (target >= a.V) target = -1;
+      if (target >= 0) g = a.dloss[row];
+      gp = (g + (a.dlse != nullptr ? a.dlse[row] : 0.0f)) / unit;
+      g /= unit;
+      target -= a.v0;  // column of the piece (none: negative)
+    }
+  }
+  __device__ __forceinline__ void take(uint32_t taddr) {
+    // A row that takes no gradient is zero whatever its logits are.
+    const uint32_t live = gp != 0.0f || g != 0.0f ? 0xFFFFFFFFu : 0u;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dz) + static_cast<size_t>(row) * a.ld + col;
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t v[32];
+      __syncwarp();
+      tmem_ld32(taddr + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = __float_as_uint(gp * ex2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -lse2)));
+      const unsigned at = static_cast<unsigned>(target - (col + c));
+      if (at < 32u) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (at == static_cast<unsigned>(i)) v[i] = __float_as_uint(__uint_as_float(v[i]) - g);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        auto two = [&](int j) {
+          return pack_bf16x2(__uint_as_float(v[i + j]), __uint_as_float(v[i + j + 1])) & live;
+        };
+        // (Rows of the workspace are whole vectors; what lies behind the piece is never read.)
+        if (row < a.N && col + c + i < a.width)
+          *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(two(0), two(2), two(4), two(6));
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------ backward: dx and dw
+// Four neighbouring columns of a finished sum.
+__device__ __forceinline__ void store4(const CeStoreArgs& a, int row, int col, float4 s, float unit) {
+  const size_t at = static_cast<size_t>(row) * a.cols + col;
+  s = make_float4(s.x * unit, s.y * unit, s.z * unit, s.w * unit);
+  if (a.add) {
+    const float4 o = *reinterpret_cast<const float4*>(a.acc + at);
+    s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w);
+  }
+  if (a.out == nullptr)
+    *reinterpret_cast<float4*>(a.acc + at) = s;
+  else if (a.out_fp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = s;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+        make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
+struct StoreEpi {
+  static constexpr int kCols = 128;
+  using Args = CeStoreArgs;
+  const Args& a;
+  int row, col, part, tile_row, tile_col;
+  float unit;
+  __device__ __forceinline__ StoreEpi(const Args& args, const product::Unit& w, int r, int c, int)
+      : a(args), row(r), col(c), part(w.part), tile_row(r - w.mt * kCeTile), tile_col(c - w.nt * kCeTile),
+        unit(*args.unit) {}
+  __device__ __forceinline__ void take(uint32_t taddr) {
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t v[32];
+      __syncwarp();
+      tmem_ld32(taddr + c, v);
+      auto four = [&](int i) {
+        return make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                           __uint_as_float(v[i + 3]));
+      };
+      if (part >= 0) {
+        float* dst = a.partial + (static_cast<size_t>(part) * kCeTile + tile_row) * kCeTile + tile_col + c;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + i) = four(i);
+      } else if (row < a.rows) {
+        const size_t at = static_cast<size_t>(row) * a.cols + col + c;
+        if (!a.add && a.out != nullptr && !a.out_fp32) {
+          // The common case in 16-byte stores.
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            auto two = [&](int j) {
+              return pack_bf16x2(__uint_as_float(v[i + j]) * unit, __uint_as_float(v[i + j + 1]) * unit);
+            };
+            if (col + c + i < a.cols)
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(two(0), two(2), two(4), two(6));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            if (col + c + i < a.cols) store4(a, row, col + c + i, four(i), unit);
+        }
+      }
+    }
+  }
+};
+
+// Tiles that were cut along K: their ranges added in ascending order, four
+// columns per thread.
+__global__ void __launch_bounds__(kSumThreads) ce_sum_kernel(const CeStoreArgs a, const ProductPlan p) {
+  constexpr int kVecs = kCeTile * kCeTile / 4;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int idx = blockIdx.x * kSumThreads + threadIdx.x;
+  const int cut = idx / kVecs, at = idx % kVecs;
+  int mt, nt;
+  product::tile_at(p, p.whole + cut, &mt, &nt);
+  const int row = mt * kCeTile + at / (kCeTile / 4), col = nt * kCeTile + (at % (kCeTile / 4)) * 4;
+  if (row >= a.rows || col >= a.cols) return;
+  const float4* src = reinterpret_cast<const float4*>(a.partial) + static_cast<size_t>(cut) * p.splits * kVecs + at;
+  float4 s = src[0];
+#pragma unroll 4
+  for (int z = 1; z < p.splits; ++z) {
+    const float4 x = src[static_cast<size_t>(z) * kVecs];
+    s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+  }
+  store4(a, row, col, s, *a.unit);
+}
+
+cudaError_t launch_sum(const CeStoreArgs& a, const ProductPlan& p, cudaStream_t st) {
+  if (p.splits == 1) return cudaSuccess;
+  const int cut = p.tiles_m * p.tiles_n - p.whole;
+  return launch_dependent(ce_sum_kernel, dim3(static_cast<unsigned>(cut * (kCeTile * kCeTile / 4 / kSumThreads))),
+                          kSumThreads, st, true, a, p);
+}
+
+}  // namespace
+
+ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool lower, bool cut) {
+  const int tile = 128 * ctas;
+  ProductPlan p{};
+  p.tiles_m = static_cast<int>((M + tile - 1) / tile);
+  p.tiles_n = static_cast<int>((N + tile - 1) / tile);
+  p.batch = batch;
+  p.n_k = static_cast<int>((K + product::kBK - 1) / product::kBK);
+  p.lower = lower ? 1 : 0;
+  const long per = lower ? static_cast<long>(p.tiles_m) * (p.tiles_m + 1) / 2
+                         : static_cast<long>(p.tiles_m) * p.tiles_n;
+  const long tiles = per * batch;
+  const int teams = product_teams(ctas);
+  p.splits = 1;
+  p.whole = static_cast<int>(tiles);
+  const int rem = static_cast<int>(tiles % teams);
+  if (cut && rem != 0) {
+    // The cut of the last round's tiles that leaves the busiest team the
+    // fewest steps; cutting at all costs about twelve (partial tiles written
+    // and added up, a second launch).
+    double best = 0.0;
+    for (int s = 1; s <= 32 && s <= p.n_k; ++s) {
+      const int rounds = (rem * s + teams - 1) / teams;
+      const double cost = rounds * (static_cast<double>((p.n_k + s - 1) / s) + (s > 1 ? 12.0 : 0.0));
+      if (s == 1 || cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
+    if (p.splits > 1) p.whole = static_cast<int>(tiles - rem);
+  }
+  const long units = p.whole + (tiles - p.whole) * p.splits;
+  p.units = static_cast<int>(units);
+  p.teams = static_cast<int>(units < teams ? units : teams);
+  return p;
+}
+
+cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
+                            const CeStatsArgs& a, cudaStream_t st) {
+  return product::launch<kPairs, false, false, false, StatsEpi>(mx, mw, p, a, false, st);
+}
+
+cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st) {
+  return launch_dependent(ce_finish_kernel, dim3(static_cast<unsigned>((a.N + kFinishRows - 1) / kFinishRows)),
+                          kFinishRows * kFinishGroups, st, true, a);
+}
+
+cudaError_t launch_ce_unit(const int* targets, const float* dloss, float* unit, int N, int V,
+                           cudaStream_t st) {
+  return launch_dependent(ce_unit_kernel, dim3(1), 1024, st, false, targets, dloss, unit, N, V);
+}
+
+cudaError_t launch_ce_dz(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
+                         const CeGradArgs& a, cudaStream_t st) {
+  return product::launch<kPairs, false, false, false, GradEpi>(mx, mw, p, a, true, st);
+}
+
+cudaError_t launch_ce_dx(const CUtensorMap& mdz, const CUtensorMap& mw, const ProductPlan& p,
+                         const CeStoreArgs& a, cudaStream_t st) {
+  cudaError_t e = product::launch<kPairs, false, true, false, StoreEpi>(mdz, mw, p, a, true, st);
+  return e != cudaSuccess ? e : launch_sum(a, p, st);
+}
+
+cudaError_t launch_ce_dw(const CUtensorMap& mdz, const CUtensorMap& mx, const ProductPlan& p,
+                         const CeStoreArgs& a, cudaStream_t st) {
+  cudaError_t e = product::launch<kPairs, true, true, false, StoreEpi>(mdz, mx, p, a, true, st);
+  return e != cudaSuccess ? e : launch_sum(a, p, st);
+}
+
+cudaError_t take_ce_status(cudaStream_t st, unsigned* out) { return product::take_status(st, out); }
+
+cudaError_t launch_ce_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
+  product::wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
+  return cudaGetLastError();
+}
+
+}  // namespace detattn

@@ -1,0 +1,146 @@
+// Internal interface of the kernels at the ends of a training step (rope.cu,
+// linear_ce.cu, muon.cu): argument blocks and launch functions.  Not part of
+// the public API.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace detattn {
+
+// ------------------------------------------------------------ rotary positions
+struct TurnArgs {
+  const void* q;           // [tokens, Hq, D], a token every q_ld elements
+  const void* k;           // [tokens, Hkv, D] (null with Hkv = 0)
+  void* q_out;
+  void* k_out;
+  const double* freqs;     // [rot / 2] radians per position
+  const int* positions;    // [n_pos] or null: position = token % T
+  long tokens, n_pos;
+  long q_ld, k_ld, q_out_ld, k_out_ld;
+  int T, Hq, Hkv, D, rot;
+  bool interleaved, fp32;
+  float mscale, sign;      // sign -1: the opposite angle
+};
+cudaError_t launch_turn(const TurnArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------ products
+// Work of one launch of the tensor-core product (product.cuh): C tiles of
+// 128 CTAS x 128 CTAS, CTAS = 1 or 2 blocks on one tile.
+struct ProductPlan {
+  int tiles_m, tiles_n, batch;
+  int n_k;                 // steps of 64 along K
+  int lower;               // 1: only tiles on and below the diagonal (tiles_m = tiles_n)
+  int whole;               // tiles computed by one team each
+  int splits;              // K ranges of each of the other tiles (1: none cut)
+  int units;               // whole + (tiles - whole) * splits
+  int teams;               // pairs (or blocks) at work
+  unsigned long long wait_ns;
+};
+// Teams of the GB300's 152 SMs.  Constants, so that the deal of the work, and
+// with it every bit, follows from the shape alone.
+constexpr int kProductSms = 152;
+inline int product_teams(int ctas) { return kProductSms / ctas; }
+// cut: whether tiles of an incomplete last round are cut along K (the caller
+// has then room for partial tiles and adds them up).
+ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool lower, bool cut);
+inline size_t product_partial_bytes(const ProductPlan& p, int ctas) {
+  const size_t cut = static_cast<size_t>(p.tiles_m) * p.tiles_n * p.batch - p.whole;
+  return p.splits == 1 ? 0 : cut * p.splits * (128 * ctas) * (128 * ctas) * sizeof(float);
+}
+
+// ------------------------------------------------------------ cross entropy of the output projection
+// Logits of a 256 x 256 tile leave two (largest, sum) pairs per row.
+struct CeStatsArgs {
+  const int* targets;      // [N]
+  float2* part;            // [2 * column tiles][N]: (m, sum 2^(z log2e - m log2e))
+  float* z_target;         // [N] the target's logit
+  int N, V;
+};
+struct CeFinishArgs {
+  const int* targets;
+  const float2* part;
+  const float* z_target;
+  float* loss;
+  float* lse;
+  int N, V, parts;
+};
+struct CeGradArgs {
+  const int* targets;      // [N]
+  const float* lse;        // [N]
+  const float* dloss;      // [N]
+  const float* dlse;       // [N] or null
+  const float* unit;       // dz is held over this (launch_ce_unit)
+  void* dz;                // bf16 [N, ld]: columns v0 .. v0 + width - 1 of dz
+  int N, V;
+  int v0, width;
+  long ld;
+};
+// What becomes of a tile's sum s = *unit * sum: out (bf16 or fp32) = [acc +] s, or acc = [acc +] s.
+struct CeStoreArgs {
+  const float* unit;
+  void* out;               // [rows, cols]; null: the sum goes to acc
+  float* acc;              // fp32 [rows, cols] or null
+  float* partial;          // tiles cut along K
+  int rows, cols;
+  int add;                 // add what acc holds
+  int out_fp32;
+};
+constexpr int kCeTile = 256;
+// mx: x [N, d] as rows of K; mw: w [V, d] as rows of K.
+cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
+                            const CeStatsArgs& a, cudaStream_t st);
+cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st);
+// *unit = the largest |dloss| of the rows that have a target (1 where that is
+// zero or not finite).
+cudaError_t launch_ce_unit(const int* targets, const float* dloss, float* unit, int N, int V,
+                           cudaStream_t st);
+cudaError_t launch_ce_dz(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
+                         const CeGradArgs& a, cudaStream_t st);
+// mdz: dz as rows of K; mw: w with K along its rows.
+cudaError_t launch_ce_dx(const CUtensorMap& mdz, const CUtensorMap& mw, const ProductPlan& p,
+                         const CeStoreArgs& a, cudaStream_t st);
+// mdz: dz with K along its rows; mx: x likewise.
+cudaError_t launch_ce_dw(const CUtensorMap& mdz, const CUtensorMap& mx, const ProductPlan& p,
+                         const CeStoreArgs& a, cudaStream_t st);
+cudaError_t take_ce_status(cudaStream_t st, unsigned* out);  // bit 0: wait, bit 1: target >= V
+cudaError_t launch_ce_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
+
+// ------------------------------------------------------------ orthogonalised update
+struct MuonInArgs {
+  const void* g;           // bf16 or fp32 [batch, m * n]
+  float* momentum;         // fp32 [batch, m * n] or null
+  double* sums;            // [batch][blocks]
+  void* x;                 // fp16 [batch, m * n]: the update over its norm, times kMuonX
+  long count;              // m * n (a multiple of 8)
+  int batch, blocks;       // blocks per matrix
+  bool g_fp32, nesterov;
+  float beta, eps;
+};
+// Scales of the stored fp16 matrices: X and X X^T hold values up to about 1.2
+// (16 fit), the polynomial up to about 3 (64 fit).
+constexpr float kMuonX = 4096.0f, kMuonP = 1024.0f;
+int muon_sum_blocks(int batch, long count);
+cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st);
+cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st);
+struct MuonStoreArgs {
+  void* out;               // fp16 (or, last, bf16) [batch][rows][ld]
+  const void* add;         // fp16 [batch][rows][ld] or null
+  long batch_stride;       // elements, of out and add
+  int rows, cols;
+  long ld;
+  float alpha, beta, diag; // out = alpha * sum + beta * add + diag on the diagonal
+  int bf16;
+};
+// mn_a, mn_b: whether K runs along the operand's rows in memory (0, 0: X X^T of
+// rows; 1, 1: of columns; 0, 1: P X).
+cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, int ctas, bool mn_a,
+                                bool mn_b, const ProductPlan& p, const MuonStoreArgs& a,
+                                cudaStream_t st);
+cudaError_t take_muon_status(cudaStream_t st, unsigned* out);
+cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
+
+unsigned long long current_context_id();
+
+}  // namespace detattn

@@ -66,7 +66,8 @@ typedef enum {
                                       a dQ step ran on a workspace attn_bwd_delta had not
                                       prepared */
   DETATTN_ERR_INDEX = -10          /* from detattn_check_status: embed_grad met token ids
-                                      outside [0, V) (it left those tokens out) */
+                                      outside [0, V) (it left those tokens out), or linear_ce
+                                      targets >= V */
 } detattn_status;
 
 /* Forward.  Writes o [B,T,Hq,D] (bf16) and lse [B,Hq,T] (fp32).
@@ -451,13 +452,117 @@ int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void
                    int d, int G, int x_fp32, int gate_fp32, int gate_sigmoid, float res_scale,
                    float block_scale, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The ends of a training step: rotary positions before the attention, the
+ * output projection's cross entropy, the orthogonalised update (RustingBrain
+ * vs PyTorch/TensorFlow page, "The setup": rotary positions; oxide-train
+ * README: an output projection of a vocabulary of 50,257 padded to 50,432; no
+ * page describes the update).  Every result is written once in a fixed order,
+ * with no atomics on data, so repeated calls give identical bytes.
+ */
+
+/* Angles per position of rot / 2 pairs, in radians, and the factor of the
+ * results, on the HOST (no GPU needed): freqs[i] = base^(-2 i / rot), with
+ *   kind 0  as they are
+ *   kind 1  over factor (linear: positions interpolated)
+ *   kind 2  with base factor^(rot / (rot - 2)) (a scaled base)
+ *   kind 3  over factor where fewer than `low` turns fit `context` positions, as
+ *           they are where more than `high` do, between in proportion to the
+ *           pair's number (whole pairs, from the numbers at which exactly
+ *           `high` and `low` turns fit); *mscale = 0.1 ln(factor) + 1
+ *   kind 4  the same in proportion to the number of turns (bands of
+ *           wavelengths); *mscale = 1
+ * rot even in [2, 1024]; base > 1; factor >= 1; 0 < low < high and context >= 1
+ * (kinds 3 and 4; not read otherwise). */
+int rope_freqs(double* freqs, float* mscale, int rot, double base, int kind, double factor,
+               int context, double low, double high);
+
+/* Rotary positions of q and k: for every token at position t and every head,
+ * the pairs (a, b) of its first `rot` components become
+ *   (mscale (a cos t f_i - b sin t f_i),  mscale (b cos t f_i + a sin t f_i))
+ * pairs are components (2 i, 2 i + 1) with interleaved, else (i, i + rot / 2);
+ * components from rot on are copied.  q [N, Hq, D] and k [N, Hkv, D], bf16 or fp32
+ * (fp32 = 1), a token every q_ld, k_ld elements (at least Hq D, Hkv D: so parts of
+ * a joined projection are taken where they lie), heads and components
+ * contiguous; q_out, k_out likewise with their own strides.  q_out may be q, and
+ * k_out k, with one stride; else they must not overlap.  Hq or Hkv may be 0 (its
+ * pointers NULL).  freqs: double [rot / 2] on the DEVICE, radians per position,
+ * finite (rope_freqs gives such).  positions: int32 [n_pos] on the device, token
+ * r takes positions[r % n_pos] (any int32); NULL with n_pos = 0: t = r % T.
+ * Angles are exact to t 2^-54 turns, whatever t; arithmetic is fp32, with one
+ * rounding.  N in [0, 2^30], D in [2, 1024], rot even in [2, D].
+ * Pointers need the alignment of their elements; with 16-byte aligned pointers,
+ * strides, D and halves (rot / 2, or rot where interleaved) the memory is moved
+ * 16 bytes at a time, which is several times faster. */
+int rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const double* freqs,
+             const int* positions, int n_pos, long long q_ld, long long k_ld, long long q_out_ld,
+             long long k_out_ld, int N, int T, int Hq, int Hkv, int D, int rot, int interleaved,
+             int fp32, float mscale, void* stream);
+
+/* Its backward: the same with the opposite angle (the transpose; mscale stays). */
+int rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const double* freqs,
+             const int* positions, int n_pos, long long dq_ld, long long dk_ld, long long dq_out_ld,
+             long long dk_out_ld, int N, int T, int Hq, int Hkv, int D, int rot, int interleaved,
+             int fp32, float mscale, void* stream);
+
+/* Softmax cross entropy of the output projection, without its logits:
+ *   z = x w^T,  lse_n = ln sum_v exp z_nv,  loss_n = lse_n - z_n,target
+ * x bf16 [N, d], w bf16 [V, d], targets int32 [N]; loss, lse fp32 [N].  A row
+ * whose target is negative has none: its loss is 0, its lse is as any other's.  A
+ * target >= V is taken as none and reported by detattn_check_status
+ * (DETATTN_ERR_INDEX).  Logits are fp32; loss is formed from differences with
+ * the largest logit, so a small one is within about 1e-6 too.  N in [0, 2^24],
+ * V in [1, 2^24], d a multiple of 8 in [8, 2^16]; N d and V d at most 1.7e10, N V
+ * 3e13.  16-byte aligned device pointers.  The workspace holds one pair of
+ * floats for every row and 128 words. */
+size_t linear_ce_fwd_workspace_bytes(int N, int V, int d);
+int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss, float* lse,
+                  void* workspace, size_t workspace_bytes, int N, int V, int d, void* stream);
+
+/* Its backward from dloss, the gradient of loss (not read in rows without a
+ * target), and dlse, that of lse (NULL: zero), both fp32 [N]:
+ *   dz_nv = (dloss_n + dlse_n) exp(z_nv - lse_n) - dloss_n [v = target_n]
+ *   dx = dz w  (bf16 [N, d]),  dw = dz^T x  (bf16 [V, d], or fp32 with dw_fp32)
+ * dx and dw fully overwritten (dw zeros for N = 0).  lse is the forward's.  The
+ * logits are computed again, one piece of the vocabulary after another; a
+ * piece's dz is in the workspace as bf16 (at most 512 MB, or N rows of 256), and
+ * that rounding is in dx and dw, which are otherwise fp32 sums rounded once.  A
+ * row without a gradient has dz = 0 whatever its logits are; its x must still be
+ * finite, since dw holds 0 x. */
+size_t linear_ce_bwd_workspace_bytes(int N, int V, int d);
+int linear_ce_bwd(const void* x, const void* w, const int* targets, const float* lse,
+                  const float* dloss, const float* dlse, void* dx, void* dw, void* workspace,
+                  size_t workspace_bytes, int N, int V, int d, int dw_fp32, void* stream);
+
+/* Orthogonalised update of `batch` gradients g [m, n], bf16 or fp32 (g_fp32):
+ *   M <- beta M + g (M = momentum, fp32, updated in place; NULL: none)
+ *   u = g + beta M with nesterov, else M (without momentum: g)
+ *   X = u / (|u| + eps), |u| the Frobenius norm
+ *   `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * o = X as bf16 [batch, m, n].  coeffs: HOST floats [steps][3] (a, b, c), NULL:
+ * 3.4445, -4.7750, 2.0315 in every step.  Between the products X, X X^T and the
+ * polynomial are fp16, scaled by powers of two, so singular values must stay
+ * below 16 and the polynomial's values below 64 (with the coefficients above
+ * they stay below 1.3 and 3.5); beyond, results are infinite or NaN.  o is within about
+ * 2e-3 of its norm of the formula (of which rounding it to bf16 is 1.7e-3) for
+ * matrices of normal numbers; directions whose singular value is below 2^-11 of
+ * the largest are only known to that.  Squares are summed in ranges, so the norm
+ * neither overflows nor vanishes for any finite fp32 update.  An infinity or NaN
+ * in a matrix makes its o NaN and leaves the batch's other matrices as they are.
+ * batch in [0, 65535], m in [1, 32768], n a multiple of 8 in [8, 32768], batch m n
+ * at most 1.7e10, steps in [1, 64], eps >= 1e-30.  16-byte aligned device pointers. */
+size_t muon_update_workspace_bytes(int batch, int m, int n);
+int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t workspace_bytes,
+                int batch, int m, int n, int g_fp32, int nesterov, int steps, const float* coeffs,
+                float beta, float eps, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device-side status words
  * that kernels set when a pipeline wait runs out (a bounded wait, default
  * limit 1 s).  Returns DETATTN_OK, DETATTN_ERR_DEVICE_TIMEOUT,
  * DETATTN_ERR_WORKSPACE (a dQ step found the workspace's tile counter not
  * cleared, i.e. attn_bwd_delta had not run on that workspace: that dQ
  * step's dq is not valid), DETATTN_ERR_INDEX (embed_grad met ids outside
- * [0, V)) or DETATTN_ERR_CUDA. */
+ * [0, V), or linear_ce targets >= V) or DETATTN_ERR_CUDA. */
 int detattn_check_status(void* stream);
 
 /* Diagnostic for accuracy tests: evaluates on n device floats x the three
@@ -524,10 +629,10 @@ int detattn_diag_dkdv_list(int B, int T, int Hq, int Hkv, int causal, int c, int
  * Returns DETATTN_OK or DETATTN_ERR_SHAPE for another value. */
 int detattn_set_dkdv_deal(int mode);
 
-/* Failure-detection self-test.  Launches three small kernels on `stream`, one
+/* Failure-detection self-test.  Launches five small kernels on `stream`, one
  * after the other, that wait, with the same bounded waits that the attention
- * kernels, act8_wgrad and block_norm_bwd use, on a barrier nothing ever
- * completes; each wait (four in all) gives up after `limit_ns` (clamped to [1
+ * kernels, act8_wgrad, block_norm_bwd, linear_ce and muon_update use, on a
+ * barrier nothing ever completes; each wait (eight in all) gives up after `limit_ns` (clamped to [1
  * ms, 10 s]), the kernel records a timeout in its status word and returns, so
  * the context stays usable.  A following detattn_check_status() returns
  * DETATTN_ERR_DEVICE_TIMEOUT, whose text names the kinds (and clears the
