@@ -1419,7 +1419,7 @@ CeBwdLayout ce_bwd_layout(int N, int V, int d) {
     part = std::max(part, product_partial_bytes(product_plan(2, N, d, w, 1, false, true), 2));
     part = std::max(part, product_partial_bytes(product_plan(2, w, d, N, 1, false, true), 2));
   }
-  l.total = l.partial + up256(part);
+  l.total = l.partial + up256(part) + 256;  // (a start on 256 bytes within the caller's)
   return l;
 }
 
@@ -1448,13 +1448,8 @@ MuonLayout muon_layout(int batch, int m, int n) {
   l.x1 = l.x0 + x;
   l.gram = l.x1 + x;
   l.poly = l.gram + s;
-  l.total = l.poly + s;
+  l.total = l.poly + s + 256;  // (a start on 256 bytes within the caller's)
   return l;
-}
-// Two blocks on a tile of 256 x 256, or one on 128 x 128.
-int muon_ctas(int batch, int m, int n) {
-  (void)batch, (void)m, (void)n;
-  return 2;
 }
 
 }  // namespace
@@ -2173,6 +2168,7 @@ int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss,
   if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, static_cast<long>(N) * d, "x")) != DETATTN_OK) return rc;
   if ((rc = encode_rows_of_k(&mw, w, d, V, 1, d, static_cast<long>(V) * d, "w")) != DETATTN_OK) return rc;
   ProductPlan p = product_plan(2, N, V, d, 1, false, false);
+  p.band = 16;
   p.wait_ns = g_wait_ns;
   char* ws = static_cast<char*>(workspace);
   float2* part = reinterpret_cast<float2*>(ws);
@@ -2207,7 +2203,9 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
   const CeBwdLayout l = ce_bwd_layout(N, V, d);
   if ((rc = check_step_workspace(workspace, workspace_bytes, l.total, "linear_ce_bwd")) != DETATTN_OK) return rc;
   if ((rc = check_device()) != DETATTN_OK) return rc;
-  char* ws = static_cast<char*>(workspace);
+  // Every part begins on 256 bytes: rows of dz are stored 32 bytes at a time.
+  char* ws = static_cast<char*>(workspace) + (256 - (reinterpret_cast<uintptr_t>(workspace) & 255)) % 256;
+  auto on32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
   const char* wb = static_cast<const char*>(w);
   float* acc = reinterpret_cast<float*>(ws + l.acc);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
@@ -2234,11 +2232,12 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
     if ((rc = launched(launch_ce_dz(mx, mw, p, ga, st), "linear_ce_bwd (dz)")) != DETATTN_OK) return rc;
     p = product_plan(2, N, d, width, 1, false, true);
     p.wait_ns = g_wait_ns;
-    CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0};
+    CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0, d % 16 == 0 && on32(dx)};
     if ((rc = launched(launch_ce_dx(mz, mwk, p, sa, st), "linear_ce_bwd (dx)")) != DETATTN_OK) return rc;
     p = product_plan(2, width, d, N, 1, false, true);
     p.wait_ns = g_wait_ns;
-    sa = {unit, static_cast<char*>(dw) + static_cast<size_t>(v0) * d * dw_size, nullptr, partial, width, d, 0, dw_fp32};
+    sa = {unit, static_cast<char*>(dw) + static_cast<size_t>(v0) * d * dw_size, nullptr, partial, width, d, 0, dw_fp32,
+          d % 16 == 0 && on32(dw)};
     if ((rc = launched(launch_ce_dw(mzk, mxk, p, sa, st), "linear_ce_bwd (dw)")) != DETATTN_OK) return rc;
   }
   return ok_status();
@@ -2269,9 +2268,10 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
   if ((rc = check_step_workspace(workspace, workspace_bytes, l.total, "muon_update")) != DETATTN_OK) return rc;
   if ((rc = check_device()) != DETATTN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
+  // Every part begins on 256 bytes: rows are stored 32 bytes at a time.
+  char* ws = static_cast<char*>(workspace) + (256 - (reinterpret_cast<uintptr_t>(workspace) & 255)) % 256;
   const bool wide = m <= n;
-  const int s = l.side, ctas = muon_ctas(batch, m, n);
+  const int s = l.side;
   const long mn = static_cast<long>(m) * n, ss = static_cast<long>(s) * l.ld;
   MuonInArgs in{};
   in.g = g;
@@ -2294,9 +2294,9 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
   }
   if ((rc = encode_rows_of_k(&mg, ws + l.gram, s, s, batch, l.ld, ss, "X X^T")) != DETATTN_OK) return rc;
   if ((rc = encode_rows_of_k(&mp, ws + l.poly, s, s, batch, l.ld, ss, "P")) != DETATTN_OK) return rc;
-  ProductPlan gram = product_plan(ctas, s, s, wide ? n : m, batch, true, false);
-  ProductPlan poly = product_plan(ctas, s, s, s, batch, true, false);
-  ProductPlan full = product_plan(ctas, m, n, s, batch, false, false);
+  ProductPlan gram = muon_plan(s, s, wide ? n : m, batch, true);
+  ProductPlan poly = muon_plan(s, s, s, batch, true);
+  ProductPlan full = muon_plan(m, n, s, batch, false);
   gram.wait_ns = poly.wait_ns = full.wait_ns = g_wait_ns;
   if ((rc = launched(launch_muon_momentum(in, st), "muon_update (momentum)")) != DETATTN_OK) return rc;
   if ((rc = launched(launch_muon_scale(in, st), "muon_update (scale)")) != DETATTN_OK) return rc;
@@ -2306,19 +2306,19 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
     const int cur = i & 1;
     const bool last = i == steps - 1;
     // A (stored times kMuonX) = X X^T; P (times kMuonP) = a I + b A + c A A.
-    MuonStoreArgs a{ws + l.gram, nullptr, ss, s, s, l.ld, 1.0f / kMuonX, 0.0f, 0.0f, 0};
+    MuonStoreArgs a{ws + l.gram, nullptr, ss, s, s, l.ld, 1.0f / kMuonX, 0.0f, 0.0f, 0, l.ld % 16 == 0};
     const CUtensorMap& x = wide ? xr[cur] : xk[cur];
-    if ((rc = launched(launch_muon_product(x, x, ctas, !wide, !wide, gram, a, st), "muon_update (gram)")) != DETATTN_OK)
+    if ((rc = launched(launch_muon_product(x, x, !wide, !wide, gram, a, st), "muon_update (gram)")) != DETATTN_OK)
       return rc;
     a = {ws + l.poly, ws + l.gram, ss, s, s, l.ld, c[2] * kMuonP / (kMuonX * kMuonX), c[1] * kMuonP / kMuonX,
-         c[0] * kMuonP, 0};
-    if ((rc = launched(launch_muon_product(mg, mg, ctas, false, false, poly, a, st), "muon_update (polynomial)")) !=
+         c[0] * kMuonP, 0, l.ld % 16 == 0};
+    if ((rc = launched(launch_muon_product(mg, mg, false, false, poly, a, st), "muon_update (polynomial)")) !=
         DETATTN_OK)
       return rc;
     a = {last ? o : ws + (cur ? l.x0 : l.x1), nullptr, mn, m, n, n, last ? 1.0f / (kMuonX * kMuonP) : 1.0f / kMuonP,
-         0.0f, 0.0f, last ? 1 : 0};
-    rc = wide ? launched(launch_muon_product(mp, xk[cur], ctas, false, true, full, a, st), "muon_update (P X)")
-              : launched(launch_muon_product(xr[cur], mp, ctas, false, false, full, a, st), "muon_update (X P)");
+         0.0f, 0.0f, last ? 1 : 0, n % 16 == 0 && (!last || (reinterpret_cast<uintptr_t>(o) & 31) == 0)};
+    rc = wide ? launched(launch_muon_product(mp, xk[cur], false, true, full, a, st), "muon_update (P X)")
+              : launched(launch_muon_product(xr[cur], mp, false, false, full, a, st), "muon_update (X P)");
     if (rc != DETATTN_OK) return rc;
   }
   return ok_status();

@@ -24,6 +24,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "exp2_poly.cuh"
 #include "product.cuh"
 
 namespace detattn {
@@ -47,28 +48,29 @@ struct StatsEpi {
   }
   __device__ __forceinline__ void take(uint32_t taddr) {
     float m = -INFINITY, s = 0.0f;
-    // (Columns past the vocabulary are those of the last tile.)
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      uint32_t v[32];
-      __syncwarp();
-      tmem_ld32(taddr + c, v);
+    each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       const int c0 = col + c;
+      // Columns past the vocabulary, in its last tile.
       if (c0 + 32 > a.V) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (c0 + i >= a.V) v[i] = 0xFF800000u;
       }
-      float t = -INFINITY;
+      float top = m;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) t = fmaxf(t, __uint_as_float(v[i]));
-      const float top = fmaxf(m, t);
+      for (int i = 0; i < 32; i += 2) top = fmax3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
       const float base = top == -INFINITY ? 0.0f : top * kLog2e;
-      float sum[4] = {};
+      const uint64_t nb = f2_make(-base, -base), l2 = f2_make(kLog2e, kLog2e);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        sum[i & 3] += ex2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -base));
-      s = s * ex2_approx(m == -INFINITY ? -INFINITY : m * kLog2e - base) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      for (int i = 0; i < 32; i += 2) {
+        float p, q;
+        f2_split(f2_fma(f2_make(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), l2, nb), p, q);
+        sum[i / 2 & 1] = f2_add(sum[i / 2 & 1], f2_make(ex2_approx(p), ex2_approx(q)));
+      }
+      float s0, s1;
+      f2_split(f2_add(sum[0], sum[1]), s0, s1);
+      s = s * ex2_approx(m == -INFINITY ? -INFINITY : m * kLog2e - base) + (s0 + s1);
       m = top;
       const unsigned at = static_cast<unsigned>(target - c0);
       if (at < 32u && target < a.V) {
@@ -77,42 +79,49 @@ struct StatsEpi {
         for (int i = 0; i < 32; ++i) z = at == static_cast<unsigned>(i) ? __uint_as_float(v[i]) : z;
         a.z_target[row] = z;
       }
-    }
+    });
     if (row < a.N) a.part[static_cast<size_t>(part) * a.N + row] = make_float2(m, s);
   }
 };
 
-// A block merges 32 rows; 16 threads share a row's parts.  A part's sum is
-// 2^r times what the largest logit asks for, r the rounding of m log2e: it is
+// A block merges kFinishRows rows; kFinishGroups threads share a row's parts:
+// first the largest logit of all, then the sums brought to it.  A part's sum is
+// 2^r times what its largest logit asks for, r the rounding of m log2e: it is
 // taken back here, so that loss does not lose what lse does.
-constexpr int kFinishRows = 32, kFinishGroups = 16;
+constexpr int kFinishRows = 8, kFinishGroups = 64;
 __global__ void __launch_bounds__(kFinishRows* kFinishGroups) ce_finish_kernel(const CeFinishArgs a) {
-  __shared__ float2 sh[kFinishGroups][kFinishRows];
+  __shared__ float sh[kFinishGroups][kFinishRows];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int lane = threadIdx.x % kFinishRows, group = threadIdx.x / kFinishRows;
   const int row = blockIdx.x * kFinishRows + lane;
-  float m = -INFINITY, s = 0.0f;
-  auto merge = [&](float m1, float s1) {
-    const float top = fmaxf(m, m1);
-    const float base = top == -INFINITY ? 0.0f : top;
-    s = s * exp2f((m - base) * kLog2e) + s1 * exp2f((m1 - base) * kLog2e);
-    m = top;
-  };
-  if (row < a.N) {
-#pragma unroll 4
-    for (int i = group; i < a.parts; i += kFinishGroups) {
-      const float2 p = a.part[static_cast<size_t>(i) * a.N + row];
-      const float b = p.x == -INFINITY ? 0.0f : p.x * kLog2e;
-      const float r = p.x == -INFINITY ? 0.0f : fmaf(p.x, kLog2e, -b);
-      merge(p.x, p.y * exp2f(-r));
-    }
+  const float2* p = a.part + min(row, a.N - 1);
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = group; i < a.parts; i += kFinishGroups) m = fmaxf(m, p[static_cast<size_t>(i) * a.N].x);
+  sh[group][lane] = m;
+  for (int o = kFinishGroups / 2; o > 0; o >>= 1) {
+    __syncthreads();
+    if (group < o) sh[group][lane] = fmaxf(sh[group][lane], sh[group + o][lane]);
   }
-  sh[group][lane] = make_float2(m, s);
   __syncthreads();
+  m = sh[0][lane];
+  __syncthreads();
+  const float base = m == -INFINITY ? 0.0f : m;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int i = group; i < a.parts; i += kFinishGroups) {
+    const float2 x = p[static_cast<size_t>(i) * a.N];
+    const float r = x.x == -INFINITY ? 0.0f : fmaf(x.x, kLog2e, -(x.x * kLog2e));
+    s += x.y * exp2f((x.x - base) * kLog2e - r);
+  }
+  sh[group][lane] = s;
+  for (int o = kFinishGroups / 2; o > 0; o >>= 1) {
+    __syncthreads();
+    if (group < o) sh[group][lane] += sh[group + o][lane];
+  }
   if (group != 0 || row >= a.N) return;
-  for (int i = 1; i < kFinishGroups; ++i) merge(sh[i][lane].x, sh[i][lane].y);
-  const float ln = logf(s);
+  const float ln = logf(sh[0][lane]);
   const int t = a.targets[row];
   a.lse[row] = m + ln;
   a.loss[row] = t >= 0 && t < a.V ? (m - a.z_target[row]) + ln : 0.0f;
@@ -144,9 +153,10 @@ struct GradEpi {
   using Args = CeGradArgs;
   const Args& a;
   int row, col, target;
-  float lse2, g, gp;  // g: dloss, gp: dloss + dlse, over the unit
+  float lse2, g;       // g: dloss over the unit
+  uint32_t live, sign; // masks of a pair
   __device__ __forceinline__ GradEpi(const Args& args, const product::Unit&, int r, int c, int)
-      : a(args), row(r), col(c), target(-1), lse2(0.0f), g(0.0f), gp(0.0f) {
+      : a(args), row(r), col(c), target(-1), lse2(0.0f), g(0.0f), live(0u), sign(0u) {
     if (row < a.N) {
       const float unit = *a.unit;
       target = a.targets[row];
@@ -154,39 +164,47 @@ struct GradEpi {
       if (target >= a.V && c == 0 && a.v0 == 0) atomicOr(&g_product_status, 2u);
       if (target >= a.V) target = -1;
       if (target >= 0) g = a.dloss[row];
-      gp = (g + (a.dlse != nullptr ? a.dlse[row] : 0.0f)) / unit;
+      const float gp = (g + (a.dlse != nullptr ? a.dlse[row] : 0.0f)) / unit;
       g /= unit;
+      // gp exp(z - lse) = +-2^(z log2e - (lse log2e - log2 |gp|)); a row that takes
+      // no gradient is zero whatever its logits are.
+      live = gp != 0.0f || g != 0.0f ? 0xFFFFFFFFu : 0u;
+      lse2 -= log2f(fabsf(gp));
+      if (gp < 0.0f) sign = 0x80008000u;
       target -= a.v0;  // column of the piece (none: negative)
     }
   }
   __device__ __forceinline__ void take(uint32_t taddr) {
-    // A row that takes no gradient is zero whatever its logits are.
-    const uint32_t live = gp != 0.0f || g != 0.0f ? 0xFFFFFFFFu : 0u;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dz) + static_cast<size_t>(row) * a.ld + col;
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      uint32_t v[32];
-      __syncwarp();
-      tmem_ld32(taddr + c, v);
+    const uint64_t nb = f2_make(-lse2, -lse2), l2 = f2_make(kLog2e, kLog2e);
+    each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
+      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = __float_as_uint(gp * ex2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -lse2)));
+      for (int i = 0; i < 16; ++i) {
+        float p, q;
+        f2_split(f2_fma(f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), l2, nb), p, q);
+        p = ex2_approx(p);
+        q = ex2_approx(q);
+        v[2 * i] = __float_as_uint(p);
+        v[2 * i + 1] = __float_as_uint(q);
+        w[i] = (pack_bf16x2(p, q) ^ sign) & live;
+      }
       const unsigned at = static_cast<unsigned>(target - (col + c));
       if (at < 32u) {
+        // The target's pair again, with -g.
+        const float s = sign ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (at == static_cast<unsigned>(i)) v[i] = __float_as_uint(__uint_as_float(v[i]) - g);
+        for (int i = 0; i < 16; ++i) {
+          const float p = s * __uint_as_float(v[2 * i]), q = s * __uint_as_float(v[2 * i + 1]);
+          if (at >> 1 == static_cast<unsigned>(i)) w[i] = pack_bf16x2(at & 1 ? p : p - g, at & 1 ? q - g : q) & live;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        auto two = [&](int j) {
-          return pack_bf16x2(__uint_as_float(v[i + j]), __uint_as_float(v[i + j + 1])) & live;
-        };
-        // (Rows of the workspace are whole vectors; what lies behind the piece is never read.)
-        if (row < a.N && col + c + i < a.width)
-          *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(two(0), two(2), two(4), two(6));
+      // (Rows of the workspace are whole sectors; what lies behind the piece is never read.)
+      if (row < a.N) {
+        if (col + c < a.width) store32(dst + c, w);
+        if (col + c + 16 < a.width) store32(dst + c + 16, w + 8);
       }
-    }
+    });
   }
 };
 
@@ -218,11 +236,7 @@ struct StoreEpi {
       : a(args), row(r), col(c), part(w.part), tile_row(r - w.mt * kCeTile), tile_col(c - w.nt * kCeTile),
         unit(*args.unit) {}
   __device__ __forceinline__ void take(uint32_t taddr) {
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      uint32_t v[32];
-      __syncwarp();
-      tmem_ld32(taddr + c, v);
+    each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       auto four = [&](int i) {
         return make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
                            __uint_as_float(v[i + 3]));
@@ -230,19 +244,23 @@ struct StoreEpi {
       if (part >= 0) {
         float* dst = a.partial + (static_cast<size_t>(part) * kCeTile + tile_row) * kCeTile + tile_col + c;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + i) = four(i);
+        for (int i = 0; i < 32; i += 8) store32(dst + i, v + i);
       } else if (row < a.rows) {
         const size_t at = static_cast<size_t>(row) * a.cols + col + c;
         if (!a.add && a.out != nullptr && !a.out_fp32) {
-          // The common case in 16-byte stores.
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at;
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            auto two = [&](int j) {
-              return pack_bf16x2(__uint_as_float(v[i + j]) * unit, __uint_as_float(v[i + j + 1]) * unit);
-            };
-            if (col + c + i < a.cols)
-              *reinterpret_cast<uint4*>(dst + i) = make_uint4(two(0), two(2), two(4), two(6));
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * unit, __uint_as_float(v[2 * i + 1]) * unit);
+          if (a.wide && col + c + 32 <= a.cols) {
+            store32(dst, w);
+            store32(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (col + c + 8 * i < a.cols)
+                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
         } else {
 #pragma unroll
@@ -250,7 +268,7 @@ struct StoreEpi {
             if (col + c + i < a.cols) store4(a, row, col + c + i, four(i), unit);
         }
       }
-    }
+    });
   }
 };
 
@@ -288,6 +306,8 @@ cudaError_t launch_sum(const CeStoreArgs& a, const ProductPlan& p, cudaStream_t 
 ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool lower, bool cut) {
   const int tile = 128 * ctas;
   ProductPlan p{};
+  p.ctas = ctas;
+  p.band = 8;
   p.tiles_m = static_cast<int>((M + tile - 1) / tile);
   p.tiles_n = static_cast<int>((N + tile - 1) / tile);
   p.batch = batch;

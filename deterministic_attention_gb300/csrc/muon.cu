@@ -167,35 +167,34 @@ struct MuonEpi {
   static constexpr int kCols = 64 * CTAS;
   using Args = MuonStoreArgs;
   const Args& a;
-  int row, col, lane;
+  int row, col;
   bool mirror;
-  size_t base;
-  __device__ __forceinline__ MuonEpi(const Args& args, const product::Unit& w, int r, int c, int l)
-      : a(args), row(r), col(c), lane(l), mirror(false), base(static_cast<size_t>(w.batch) * args.batch_stride) {
-    mirror = w.mt != w.nt;
-  }
-  __device__ __forceinline__ void take(uint32_t taddr, bool lower) {
-    const size_t at = base + static_cast<size_t>(row) * a.ld + col;
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      uint32_t v[32];
-      uint4 add[4];
-      const bool mine = row < a.rows;
-      if (a.add != nullptr && mine) {
+  size_t base, at;
+  uint4 add[kCols / 8];
+  __device__ __forceinline__ MuonEpi(const Args& args, const product::Unit& w, int r, int c, int)
+      : a(args), row(r), col(c), mirror(w.mt != w.nt) {
+    base = static_cast<size_t>(w.batch) * args.batch_stride;
+    at = base + static_cast<size_t>(row) * a.ld + col;
+    // What is added is under way while the tile is computed.
+    if (a.add != nullptr) {
+      const __half* p = static_cast<const __half*>(a.add) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + c + 8 * i < a.cols)
-            add[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.add) + at + c + 8 * i);
-      }
-      __syncwarp();
-      tmem_ld32(taddr + c, v);
+      for (int i = 0; i < kCols / 8; ++i)
+        add[i] = row < a.rows && col + 8 * i < a.cols ? *reinterpret_cast<const uint4*>(p + 8 * i)
+                                                      : make_uint4(0, 0, 0, 0);
+    }
+  }
+  template <bool LOWER>
+  __device__ __forceinline__ void take_as(uint32_t taddr) {
+    each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float x = a.alpha * __uint_as_float(v[2 * i]), y = a.alpha * __uint_as_float(v[2 * i + 1]);
         if (a.add != nullptr) {
-          const uint32_t s[4] = {add[i / 4].x, add[i / 4].y, add[i / 4].z, add[i / 4].w};
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s[i % 4]));
+          const uint4 q = add[c / 8 + i / 4];
+          const uint32_t s = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
           x = fmaf(a.beta, f.x, x);
           y = fmaf(a.beta, f.y, y);
           if (row == col + c + 2 * i) x += a.diag;
@@ -208,36 +207,48 @@ struct MuonEpi {
           w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
+      const bool mine = row < a.rows;
+      __half* dst = static_cast<__half*>(a.out) + at + c;
       if (mine) {
+        if (a.wide && col + c + 32 <= a.cols) {
+          store32(dst, w);
+          store32(dst + 16, w + 8);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + c + 8 * i < a.cols)
-            *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at + c + 8 * i) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        if (lower && mirror) {
-          // The tile's transpose: at each column the warp's rows are neighbours.
-          __half* dst = static_cast<__half*>(a.out) + base + row;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
-            if (col + c + 2 * i < a.rows) dst[static_cast<size_t>(col + c + 2 * i) * a.ld] = __low2half(h);
-            if (col + c + 2 * i + 1 < a.rows) dst[static_cast<size_t>(col + c + 2 * i + 1) * a.ld] = __high2half(h);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (col + c + 8 * i < a.cols)
+              *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
-    }
+      if (LOWER && mirror) {
+        // The tile's transpose: lanes 2 k and 2 k + 1 exchange, so that each has
+        // two neighbouring rows of one column (rows of the result are whole
+        // vectors: a row past the last is never read).
+        const int odd = row & 1;
+        __half* to = static_cast<__half*>(a.out) + base + (row & ~1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, w[i], 1);
+          const uint32_t two = odd ? __byte_perm(other, w[i], 0x7632) : __byte_perm(w[i], other, 0x5410);
+          const int k = col + c + 2 * i + odd;
+          if (k < a.rows && (row & ~1) < a.rows)
+            *reinterpret_cast<uint32_t*>(to + static_cast<size_t>(k) * a.ld) = two;
+        }
+      }
+    });
   }
 };
-// Symmetric results (tiles below the diagonal are written twice), and X.
-template <int CTAS>
-struct SymEpi : MuonEpi<CTAS> {
-  using MuonEpi<CTAS>::MuonEpi;
-  __device__ __forceinline__ void take(uint32_t t) { MuonEpi<CTAS>::take(t, true); }
-};
+// All tiles of a result, and those of a symmetric one on and below the
+// diagonal, written twice.
 template <int CTAS>
 struct FullEpi : MuonEpi<CTAS> {
   using MuonEpi<CTAS>::MuonEpi;
-  __device__ __forceinline__ void take(uint32_t t) { MuonEpi<CTAS>::take(t, false); }
+  __device__ __forceinline__ void take(uint32_t t) { this->template take_as<false>(t); }
+};
+template <int CTAS>
+struct LowerEpi : MuonEpi<CTAS> {
+  using MuonEpi<CTAS>::MuonEpi;
+  __device__ __forceinline__ void take(uint32_t t) { this->template take_as<true>(t); }
 };
 
 template <int CTAS>
@@ -245,8 +256,9 @@ cudaError_t launch_product_t(const CUtensorMap& ma, const CUtensorMap& mb, bool 
                              const ProductPlan& p, const MuonStoreArgs& a, cudaStream_t st) {
   using product::launch;
   if (p.lower)
-    return mn_a ? launch<CTAS, true, true, true, SymEpi<CTAS>>(ma, mb, p, a, true, st)
-                : launch<CTAS, false, false, true, SymEpi<CTAS>>(ma, mb, p, a, true, st);
+    return mn_a ? launch<CTAS, true, true, true, LowerEpi<CTAS>>(ma, mb, p, a, true, st)
+                : launch<CTAS, false, false, true, LowerEpi<CTAS>>(ma, mb, p, a, true, st);
+  if (mn_a) return launch<CTAS, true, true, true, FullEpi<CTAS>>(ma, mb, p, a, true, st);
   return mn_b ? launch<CTAS, false, true, true, FullEpi<CTAS>>(ma, mb, p, a, true, st)
               : launch<CTAS, false, false, true, FullEpi<CTAS>>(ma, mb, p, a, true, st);
 }
@@ -267,11 +279,30 @@ cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st) {
 cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st) {
   return launch_dependent(muon_scale_kernel, dim3(a.blocks, a.batch), kInThreads, st, true, a);
 }
-cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, int ctas, bool mn_a,
-                                bool mn_b, const ProductPlan& p, const MuonStoreArgs& a,
-                                cudaStream_t st) {
-  return ctas == 2 ? launch_product_t<2>(ma, mb, mn_a, mn_b, p, a, st)
-                   : launch_product_t<1>(ma, mb, mn_a, mn_b, p, a, st);
+ProductPlan muon_plan(long M, long N, long K, int batch, bool symmetric) {
+  ProductPlan best{};
+  double least = 0.0;
+  for (int form = 0; form < 4; ++form) {
+    const int ctas = 1 + (form & 1);
+    const bool lower = form >= 2;
+    if (lower && !symmetric) continue;
+    const ProductPlan p = product_plan(ctas, M, N, K, batch, lower, false);
+    // Clocks: rounds of tiles, 512 a step of K for a pair, 256 for a block and a
+    // quarter more for its loads, then the last tile's epilogue.
+    const long rounds = (p.units + product_teams(ctas) - 1) / product_teams(ctas);
+    const double cost = static_cast<double>(rounds) * p.n_k * (ctas == 2 ? 512.0 : 320.0) +
+                        ctas * (lower ? 2200.0 : 1600.0);
+    if (form == 0 || cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, bool mn_a, bool mn_b,
+                                const ProductPlan& p, const MuonStoreArgs& a, cudaStream_t st) {
+  return p.ctas == 2 ? launch_product_t<2>(ma, mb, mn_a, mn_b, p, a, st)
+                     : launch_product_t<1>(ma, mb, mn_a, mn_b, p, a, st);
 }
 cudaError_t take_muon_status(cudaStream_t st, unsigned* out) { return product::take_status(st, out); }
 cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {

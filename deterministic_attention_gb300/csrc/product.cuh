@@ -92,8 +92,9 @@ struct Unit {
   int kb0, kb1;        // steps [kb0, kb1)
   int part;            // partial slot, -1: a whole tile
 };
-// Row and column tile of tile `t` of one matrix.  Rows first: the teams at work
-// at one time share few column tiles.
+// Row and column tile of tile `t` of one matrix.  Bands of p.band tile rows, and
+// in a band column by column: the teams at work at one time share few
+// rows of either operand.
 __device__ __forceinline__ void tile_at(const ProductPlan& p, int t, int* mt, int* nt) {
   if (p.lower) {
     // Tiles (i, j), j <= i, in order of i: i (i + 1) / 2 + j = t.
@@ -103,8 +104,10 @@ __device__ __forceinline__ void tile_at(const ProductPlan& p, int t, int* mt, in
     *mt = i;
     *nt = t - i * (i + 1) / 2;
   } else {
-    *mt = t % p.tiles_m;
-    *nt = t / p.tiles_m;
+    const int band = t / (p.band * p.tiles_n), m0 = band * p.band, rows = min(p.band, p.tiles_m - m0);
+    const int r = t - m0 * p.tiles_n;
+    *mt = m0 + r % rows;
+    *nt = r / rows;
   }
 }
 __device__ __forceinline__ int tiles_of(const ProductPlan& p) {
@@ -388,6 +391,28 @@ static cudaError_t take_status(cudaStream_t st, unsigned* out) {
 }
 
 }  // namespace product
+
+// 32 bytes in one store: a whole sector of a row by one thread.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// COLS columns of TMEM, 32 at a time: f(c, v) with the next ones under way.
+template <int COLS, class F>
+__device__ __forceinline__ void each32(uint32_t taddr, F&& f) {
+  uint32_t v[2][32];
+  tmem_ld32_nowait(taddr, v[0]);
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t(&now)[32] = v[c / 32 & 1];
+    __syncwarp();
+    tmem_wait_ld();
+    reg_fence32(now);
+    if (c + 32 < COLS) tmem_ld32_nowait(taddr + c + 32, v[c / 32 + 1 & 1]);
+    f(c, now);
+  }
+}
 
 // A small kernel after the products that waits for the kernel before it.
 template <class... P, class... A>

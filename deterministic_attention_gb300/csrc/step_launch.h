@@ -29,8 +29,10 @@ cudaError_t launch_turn(const TurnArgs& a, cudaStream_t st);
 // Work of one launch of the tensor-core product (product.cuh): C tiles of
 // 128 CTAS x 128 CTAS, CTAS = 1 or 2 blocks on one tile.
 struct ProductPlan {
+  int ctas;                // blocks on one tile
   int tiles_m, tiles_n, batch;
   int n_k;                 // steps of 64 along K
+  int band;                // tile rows that are walked together, column by column
   int lower;               // 1: only tiles on and below the diagonal (tiles_m = tiles_n)
   int whole;               // tiles computed by one team each
   int splits;              // K ranges of each of the other tiles (1: none cut)
@@ -86,6 +88,7 @@ struct CeStoreArgs {
   int rows, cols;
   int add;                 // add what acc holds
   int out_fp32;
+  int wide;                // rows of out begin on 32 bytes
 };
 constexpr int kCeTile = 256;
 // mx: x [N, d] as rows of K; mw: w [V, d] as rows of K.
@@ -124,6 +127,9 @@ constexpr float kMuonX = 4096.0f, kMuonP = 1024.0f;
 int muon_sum_blocks(int batch, long count);
 cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st);
 cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st);
+// The plan of a product of muon_update: one or two blocks on a tile; all of a
+// symmetric result's tiles or those on and below the diagonal.
+ProductPlan muon_plan(long M, long N, long K, int batch, bool symmetric);
 struct MuonStoreArgs {
   void* out;               // fp16 (or, last, bf16) [batch][rows][ld]
   const void* add;         // fp16 [batch][rows][ld] or null
@@ -132,11 +138,12 @@ struct MuonStoreArgs {
   long ld;
   float alpha, beta, diag; // out = alpha * sum + beta * add + diag on the diagonal
   int bf16;
+  int wide;                // rows of out begin on 32 bytes
 };
 // mn_a, mn_b: whether K runs along the operand's rows in memory (0, 0: X X^T of
 // rows; 1, 1: of columns; 0, 1: P X).
-cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, int ctas, bool mn_a,
-                                bool mn_b, const ProductPlan& p, const MuonStoreArgs& a,
+cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, bool mn_a, bool mn_b,
+                                const ProductPlan& p, const MuonStoreArgs& a,
                                 cudaStream_t st);
 cudaError_t take_muon_status(cudaStream_t st, unsigned* out);
 cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
