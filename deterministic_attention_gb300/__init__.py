@@ -794,71 +794,78 @@ def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, context=0, low=1.0, 
     return torch.tensor(list(f), dtype=torch.float64, device=device), m.value
 
 
-def _heads(t, name, dev):
+def _heads(t, name, dev, dtype=None):
     """(tokens, T, H, D, token stride) of a [..., T, H, D] tensor whose heads and
     components are contiguous and whose tokens lie one stride apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    dt = t.dtype
+    if (dt is not torch.bfloat16 and dt is not torch.float32) or (dtype is not None and dt is not dtype):
+        raise TypeError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float32'}, got {dt}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if t.dim() < 3:
-        raise ValueError(f"{name} must be [..., T, H, D], got {tuple(t.shape)}")
-    T, H, D = t.shape[-3:]
-    tokens = t.numel() // max(1, H * D)
+    shape = t.shape
+    n = len(shape)
+    if n < 3:
+        raise ValueError(f"{name} must be [..., T, H, D], got {tuple(shape)}")
+    T, H, D = shape[n - 3], shape[n - 2], shape[n - 1]
+    ld = H * D
+    tokens = t.numel() // max(1, ld)
+    if not tokens or t.is_contiguous():
+        return tokens, T, H, D, ld
     st = t.stride()
-    if tokens and ((D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D)):
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
         raise ValueError(f"{name}: heads and components must be contiguous, strides {st}")
-    ld, span = H * D, None
-    for n, s in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
-        if n == 1 or not tokens:
+    span = None
+    for i in range(n - 3, -1, -1):
+        if shape[i] == 1:
             continue
         if span is None:
-            ld = s
-        elif s != span:
+            ld = st[i]
+        elif st[i] != span:
             raise ValueError(f"{name}: tokens must lie one stride apart, strides {st}")
-        span = s * n
+        span = st[i] * shape[i]
     return tokens, T, H, D, ld
 
 
+def _heads_out(o, name, t, N, T, H, D, dev):
+    """(result like t, token stride): o, or a new contiguous tensor."""
+    if o is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device), H * D
+    No, To, Ho, Do, ld = _heads(o, name, dev, t.dtype)
+    if No != N or To != T or Ho != H or Do != D:
+        raise ValueError(f"{name} is {tuple(o.shape)}, expected {tuple(t.shape)}")
+    return o, ld
+
+
 def _rope(call, where, q, k, freqs, positions, interleaved, mscale, q_out, k_out):
-    if q is None:
+    if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev = _current(q, "q")
     N, T, Hq, D, q_ld = _heads(q, "q", dev)
-    Hkv, k_ld, ko_ld = 0, 0, 0
+    qo, qo_ld = _heads_out(q_out, "q_out", q, N, T, Hq, D, dev)
+    ko, Hkv, k_ld, ko_ld = None, 0, 0, 0
     if k is not None:
-        Nk, _, Hkv, Dk, k_ld = _heads(k, "k", dev)
-        if k.dtype is not q.dtype or Dk != D or k.shape[:-2] != q.shape[:-2]:
-            raise ValueError(f"k is {k.dtype} {tuple(k.shape)}, q {q.dtype} {tuple(q.shape)}")
+        Nk, Tk, Hkv, Dk, k_ld = _heads(k, "k", dev, q.dtype)
+        if Nk != N or Tk != T or Dk != D:
+            raise ValueError(f"k is {tuple(k.shape)}, q {tuple(q.shape)}")
+        ko, ko_ld = _heads_out(k_out, "k_out", k, N, T, Hkv, D, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    outs = []
-    for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if t is None:
-            outs.append((None, 0))
-        elif o is None:
-            outs.append((torch.empty(t.shape, dtype=t.dtype, device=t.device), t.shape[-2] * D))
-        else:
-            ld = _heads(o, name, dev)[4]
-            if o.dtype is not t.dtype or o.shape != t.shape:
-                raise ValueError(f"{name} is {o.dtype} {tuple(o.shape)}, expected {t.dtype} {tuple(t.shape)}")
-            outs.append((o, ld))
-    (qo, qo_ld), (ko, ko_ld) = outs
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise TypeError("freqs must be a float64 tensor [rot / 2]")
-    _on_device(freqs, "freqs", torch.float64, freqs.shape, dev)
-    n_pos = 0
+    half = freqs.shape[0]
+    _on_device(freqs, "freqs", torch.float64, (half,), dev)
+    n_pos, at = 0, None
     if positions is not None:
         _on_device(positions, "positions", torch.int32, positions.shape, dev)
-        n_pos = positions.numel()
-        if tuple(positions.shape) not in ((T,), tuple(q.shape[:-2])):
+        n_pos, at = positions.numel(), positions.data_ptr()
+        if positions.dim() < 1 or positions.shape[-1] != T or (n_pos != N and n_pos != T):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(T,)} or {tuple(q.shape[:-2])}")
     if N:
-        _check(call(q.data_ptr(), _addr(k), qo.data_ptr(), _addr(ko), freqs.data_ptr(), _addr(positions),
-                    n_pos, q_ld, k_ld, qo_ld, ko_ld, N, T, Hq, Hkv, D, 2 * freqs.numel(), bool(interleaved),
-                    q.dtype is torch.float32, mscale, _stream()), where)
+        _check(call(q.data_ptr(), _addr(k), qo.data_ptr(), _addr(ko), freqs.data_ptr(), at, n_pos, q_ld, k_ld,
+                    qo_ld, ko_ld, N, T, Hq, Hkv, D, 2 * half, bool(interleaved), q.dtype is torch.float32,
+                    mscale, _stream()), where)
     return qo, ko
 
 

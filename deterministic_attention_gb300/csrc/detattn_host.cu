@@ -1416,8 +1416,8 @@ CeBwdLayout ce_bwd_layout(int N, int V, int d) {
   size_t part = 0;
   const int last = V % l.width == 0 ? l.width : V % l.width;
   for (int w : {l.width, last}) {
-    part = std::max(part, product_partial_bytes(product_plan(2, N, d, w, 1, false, true), 2));
-    part = std::max(part, product_partial_bytes(product_plan(2, w, d, N, 1, false, true), 2));
+    part = std::max(part, product_partial_bytes(product_plan(2, N, d, w, 1, true), 2));
+    part = std::max(part, product_partial_bytes(product_plan(2, w, d, N, 1, true), 2));
   }
   l.total = l.partial + up256(part) + 256;  // (a start on 256 bytes within the caller's)
   return l;
@@ -1435,7 +1435,9 @@ int check_muon_shape(int batch, int m, int n) {
 struct MuonLayout {
   int side, blocks;        // the shorter side; blocks per matrix that sum squares
   long ld;                 // of the side x side matrices
-  size_t x0, x1, gram, poly, total;
+  MuonPlan plan;
+  int n_counts;
+  size_t counts, x0, x1, gram, poly, total;
 };
 MuonLayout muon_layout(int batch, int m, int n) {
   MuonLayout l{};
@@ -1444,7 +1446,10 @@ MuonLayout muon_layout(int batch, int m, int n) {
   l.blocks = muon_sum_blocks(batch, static_cast<long>(m) * n);
   const size_t x = up256(static_cast<size_t>(batch) * m * n * 2);
   const size_t s = up256(static_cast<size_t>(batch) * l.side * l.ld * 2);
-  l.x0 = up256(static_cast<size_t>(batch) * l.blocks * sizeof(double));
+  l.plan = muon_plan(batch, m, n);
+  l.n_counts = batch * 3 * l.plan.tiles_s * kMuonCountStride;
+  l.counts = up256(static_cast<size_t>(batch) * l.blocks * sizeof(double));
+  l.x0 = l.counts + up256(static_cast<size_t>(l.n_counts) * sizeof(unsigned));
   l.x1 = l.x0 + x;
   l.gram = l.x1 + x;
   l.poly = l.gram + s;
@@ -2167,7 +2172,7 @@ int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss,
   CUtensorMap mx, mw;
   if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, static_cast<long>(N) * d, "x")) != DETATTN_OK) return rc;
   if ((rc = encode_rows_of_k(&mw, w, d, V, 1, d, static_cast<long>(V) * d, "w")) != DETATTN_OK) return rc;
-  ProductPlan p = product_plan(2, N, V, d, 1, false, false);
+  ProductPlan p = product_plan(2, N, V, d, 1, false);
   p.band = 16;
   p.wait_ns = g_wait_ns;
   char* ws = static_cast<char*>(workspace);
@@ -2226,15 +2231,15 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
     if ((rc = encode_k_rows(&mwk, wp, d, width, 1, d, wd, "w")) != DETATTN_OK) return rc;
     if ((rc = encode_rows_of_k(&mz, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
     if ((rc = encode_k_rows(&mzk, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
-    ProductPlan p = product_plan(2, N, width, d, 1, false, false);
+    ProductPlan p = product_plan(2, N, width, d, 1, false);
     p.wait_ns = g_wait_ns;
     CeGradArgs ga{targets, lse, dloss, dlse, unit, ws, N, V, v0, width, l.ld};
     if ((rc = launched(launch_ce_dz(mx, mw, p, ga, st), "linear_ce_bwd (dz)")) != DETATTN_OK) return rc;
-    p = product_plan(2, N, d, width, 1, false, true);
+    p = product_plan(2, N, d, width, 1, true);
     p.wait_ns = g_wait_ns;
     CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0, d % 16 == 0 && on32(dx)};
     if ((rc = launched(launch_ce_dx(mz, mwk, p, sa, st), "linear_ce_bwd (dx)")) != DETATTN_OK) return rc;
-    p = product_plan(2, width, d, N, 1, false, true);
+    p = product_plan(2, width, d, N, 1, true);
     p.wait_ns = g_wait_ns;
     sa = {unit, static_cast<char*>(dw) + static_cast<size_t>(v0) * d * dw_size, nullptr, partial, width, d, 0, dw_fp32,
           d % 16 == 0 && on32(dw)};
@@ -2272,7 +2277,7 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
   char* ws = static_cast<char*>(workspace) + (256 - (reinterpret_cast<uintptr_t>(workspace) & 255)) % 256;
   const bool wide = m <= n;
   const int s = l.side;
-  const long mn = static_cast<long>(m) * n, ss = static_cast<long>(s) * l.ld;
+  const long mn = static_cast<long>(m) * n;
   MuonInArgs in{};
   in.g = g;
   in.momentum = momentum;
@@ -2285,43 +2290,41 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
   in.nesterov = nesterov != 0;
   in.beta = beta;
   in.eps = eps;
-  // X in either buffer, as rows and as columns of K; the symmetric matrices.
-  CUtensorMap xr[2], xk[2], mg, mp;
-  for (int i = 0; i < 2; ++i) {
-    const void* x = ws + (i ? l.x1 : l.x0);
-    if ((rc = encode_rows_of_k(&xr[i], x, n, m, batch, n, mn, "X")) != DETATTN_OK) return rc;
-    if ((rc = encode_k_rows(&xk[i], x, n, m, batch, n, mn, "X")) != DETATTN_OK) return rc;
-  }
-  if ((rc = encode_rows_of_k(&mg, ws + l.gram, s, s, batch, l.ld, ss, "X X^T")) != DETATTN_OK) return rc;
-  if ((rc = encode_rows_of_k(&mp, ws + l.poly, s, s, batch, l.ld, ss, "P")) != DETATTN_OK) return rc;
-  ProductPlan gram = muon_plan(s, s, wide ? n : m, batch, true);
-  ProductPlan poly = muon_plan(s, s, s, batch, true);
-  ProductPlan full = muon_plan(m, n, s, batch, false);
-  gram.wait_ns = poly.wait_ns = full.wait_ns = g_wait_ns;
+  in.counts = reinterpret_cast<unsigned*>(ws + l.counts);
+  in.n_counts = l.n_counts;
+  MuonChainArgs c{};
+  auto both = [&](CUtensorMap* to, const void* p, long cols, long rows, long ld, const char* what) {
+    const int r = encode_rows_of_k(&to[0], p, cols, rows, batch, ld, rows * ld, what);
+    return r != DETATTN_OK ? r : encode_k_rows(&to[1], p, cols, rows, batch, ld, rows * ld, what);
+  };
+  c.x_out[0] = ws + l.x0;
+  c.x_out[1] = ws + l.x1;
+  for (int i = 0; i < 2; ++i)
+    if ((rc = both(c.x[i], c.x_out[i], n, m, n, "X")) != DETATTN_OK) return rc;
+  if ((rc = both(c.gram, ws + l.gram, s, s, l.ld, "X X^T")) != DETATTN_OK) return rc;
+  if ((rc = both(c.poly, ws + l.poly, s, s, l.ld, "P")) != DETATTN_OK) return rc;
+  c.gram_out = ws + l.gram;
+  c.poly_out = ws + l.poly;
+  c.o = o;
+  c.counts = in.counts;
+  c.batch = batch;
+  c.m = m;
+  c.n = n;
+  c.side = s;
+  c.ld = l.ld;
+  c.steps = steps;
+  c.tiles_s = l.plan.tiles_s;
+  c.tiles_o = l.plan.tiles_o;
+  c.sym_tiles = l.plan.sym_tiles;
+  c.lower = l.plan.lower;
+  c.wide = wide ? 1 : 0;
+  c.o_on32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+  c.wait_ns = g_wait_ns;
+  constexpr float kCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
+  for (int i = 0; i < 3 * steps; ++i) c.coeffs[i / 3][i % 3] = coeffs ? coeffs[i] : kCoeffs[i % 3];
   if ((rc = launched(launch_muon_momentum(in, st), "muon_update (momentum)")) != DETATTN_OK) return rc;
   if ((rc = launched(launch_muon_scale(in, st), "muon_update (scale)")) != DETATTN_OK) return rc;
-  for (int i = 0; i < steps; ++i) {
-    const float c[3] = {coeffs ? coeffs[3 * i] : 3.4445f, coeffs ? coeffs[3 * i + 1] : -4.7750f,
-                        coeffs ? coeffs[3 * i + 2] : 2.0315f};
-    const int cur = i & 1;
-    const bool last = i == steps - 1;
-    // A (stored times kMuonX) = X X^T; P (times kMuonP) = a I + b A + c A A.
-    MuonStoreArgs a{ws + l.gram, nullptr, ss, s, s, l.ld, 1.0f / kMuonX, 0.0f, 0.0f, 0, l.ld % 16 == 0};
-    const CUtensorMap& x = wide ? xr[cur] : xk[cur];
-    if ((rc = launched(launch_muon_product(x, x, !wide, !wide, gram, a, st), "muon_update (gram)")) != DETATTN_OK)
-      return rc;
-    a = {ws + l.poly, ws + l.gram, ss, s, s, l.ld, c[2] * kMuonP / (kMuonX * kMuonX), c[1] * kMuonP / kMuonX,
-         c[0] * kMuonP, 0, l.ld % 16 == 0};
-    if ((rc = launched(launch_muon_product(mg, mg, false, false, poly, a, st), "muon_update (polynomial)")) !=
-        DETATTN_OK)
-      return rc;
-    a = {last ? o : ws + (cur ? l.x0 : l.x1), nullptr, mn, m, n, n, last ? 1.0f / (kMuonX * kMuonP) : 1.0f / kMuonP,
-         0.0f, 0.0f, last ? 1 : 0, n % 16 == 0 && (!last || (reinterpret_cast<uintptr_t>(o) & 31) == 0)};
-    rc = wide ? launched(launch_muon_product(mp, xk[cur], false, true, full, a, st), "muon_update (P X)")
-              : launched(launch_muon_product(xr[cur], mp, false, false, full, a, st), "muon_update (X P)");
-    if (rc != DETATTN_OK) return rc;
-  }
-  return ok_status();
+  return launched(launch_muon_chain(c, l.plan.ctas, l.plan.units, st), "muon_update (products)");
 }
 
 int detattn_check_status(void* stream) {

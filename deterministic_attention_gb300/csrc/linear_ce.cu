@@ -303,19 +303,15 @@ cudaError_t launch_sum(const CeStoreArgs& a, const ProductPlan& p, cudaStream_t 
 
 }  // namespace
 
-ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool lower, bool cut) {
+ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool cut) {
   const int tile = 128 * ctas;
   ProductPlan p{};
-  p.ctas = ctas;
   p.band = 8;
   p.tiles_m = static_cast<int>((M + tile - 1) / tile);
   p.tiles_n = static_cast<int>((N + tile - 1) / tile);
   p.batch = batch;
   p.n_k = static_cast<int>((K + product::kBK - 1) / product::kBK);
-  p.lower = lower ? 1 : 0;
-  const long per = lower ? static_cast<long>(p.tiles_m) * (p.tiles_m + 1) / 2
-                         : static_cast<long>(p.tiles_m) * p.tiles_n;
-  const long tiles = per * batch;
+  const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n * batch;
   const int teams = product_teams(ctas);
   p.splits = 1;
   p.whole = static_cast<int>(tiles);

@@ -8,8 +8,8 @@
 //
 //   A = X X^T,   P = a I + b A + c A A,   X <- P X       (m <= n; X <- X P by columns else)
 //
-// A and P are symmetric: their tiles on and below the diagonal are computed and
-// written twice.  Between the products the matrices are fp16, scaled by powers
+// A and P are symmetric: their tiles on and below the diagonal are computed, and
+// what lies above is read as the transpose of what lies below.  Between the products the matrices are fp16, scaled by powers
 // of two (kMuonX, kMuonP): the singular values stay below about 1.2, so fp16's
 // eleven bits cost a step 2^-12 of a value where bf16 costs 2^-9, at the same
 // rate; five steps leave 1.2e-3 of the result's norm (768 x 768 of normal
@@ -20,6 +20,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "product.cuh"
 
@@ -79,6 +80,8 @@ struct Squares {
 __global__ void __launch_bounds__(kInThreads) muon_momentum_kernel(const MuonInArgs a) {
   __shared__ double sh[kInThreads / 32];
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.n_counts; i += kInThreads) a.counts[i] = 0u;
   const size_t base = static_cast<size_t>(blockIdx.y) * a.count;
   const long vecs = a.count / 8;
   double total = 0.0;
@@ -162,105 +165,481 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
 }
 
 // ------------------------------------------------------------ products
-template <int CTAS>
-struct MuonEpi {
-  static constexpr int kCols = 64 * CTAS;
-  using Args = MuonStoreArgs;
-  const Args& a;
-  int row, col;
-  bool mirror;
-  size_t base, at;
-  uint4 add[kCols / 8];
-  __device__ __forceinline__ MuonEpi(const Args& args, const product::Unit& w, int r, int c, int)
-      : a(args), row(r), col(c), mirror(w.mt != w.nt) {
-    base = static_cast<size_t>(w.batch) * args.batch_stride;
-    at = base + static_cast<size_t>(row) * a.ld + col;
-    // What is added is under way while the tile is computed.
-    if (a.add != nullptr) {
-      const __half* p = static_cast<const __half*>(a.add) + at;
-#pragma unroll
-      for (int i = 0; i < kCols / 8; ++i)
-        add[i] = row < a.rows && col + 8 * i < a.cols ? *reinterpret_cast<const uint4*>(p + 8 * i)
-                                                      : make_uint4(0, 0, 0, 0);
+// All products of all steps in one launch: tiles in one order (step by step; in a
+// step the tiles of A, of P, of the next X, matrix by matrix), dealt to teams in
+// turn.  What a tile needs is counted: a finished tile of A or P adds to the
+// counts of its row block and its column block, a finished tile of X to that of
+// its block along the shorter side, and a tile starts when the counts of the
+// blocks it reads are complete.  That one X is complete follows from any complete
+// block of P (all blocks of A, so all blocks of X, went into it), and so does that
+// nobody still reads what a tile overwrites: A(i, j) of the next step is written
+// after blocks i and j of the next X, so after blocks i and j of P, which every
+// reader of blocks i and j of A has added to.  The launch is cooperative: all
+// blocks are resident, each takes its tiles in order, and a tile waits only for
+// tiles before it, so every wait ends (they are bounded all the same).
+//
+// Against a launch for each product this fills rounds (4096 x 6144 has 136, 136 and
+// 384 tiles a step for 76 teams) and starts a tile as soon as its own inputs are
+// there: 12 x 768 x 1280 takes 226 us and did 331, 4096 x 6144 1,190 and 1,258, 768 x
+// 768 109 and 115.  A tile is ready 3 to 4 us after its last product (the queue of
+// products 0.3 to 1.3, its stores 1 to 3, the fence before the count 0.7) and seen
+// 1.2 us later: with at most a dozen matrices that chain, not the rate of the
+// products, is the time.  Measured and not kept: a warp that looks at the counts ahead
+// of the producer (768 x 768: 122 us); two groups of matrices by turns (12 x 768 x 1280:
+// 250 us); the tiles above the diagonal written too (258 us); how an operand lies in
+// memory chosen step by step and not in runs (the issue of a product then takes
+// longer than the product: 258 us).
+enum : int { kGram = 0, kPoly = 1, kNext = 2 };
+
+struct MuonUnit {
+  int batch, mt, nt, kind, step, n_k;
+};
+__device__ __forceinline__ MuonUnit muon_unit(const MuonChainArgs& a, int u) {
+  MuonUnit w;
+  const int sym = a.batch * a.sym_tiles, full = a.tiles_s * a.tiles_o, per = 2 * sym + a.batch * full;
+  w.step = u / per;
+  int r = u - w.step * per;
+  w.kind = r < sym ? kGram : r < 2 * sym ? kPoly : kNext;
+  r -= w.kind * sym;
+  if (w.kind == kNext) {
+    w.batch = r / full;
+    r -= w.batch * full;
+    // Along the shorter side first: few columns (rows) of X at a time.
+    const int s = r % a.tiles_s, o = r / a.tiles_s;
+    w.mt = a.wide ? s : o;
+    w.nt = a.wide ? o : s;
+    w.n_k = (a.side + product::kBK - 1) / product::kBK;
+  } else {
+    w.batch = r / a.sym_tiles;
+    r -= w.batch * a.sym_tiles;
+    if (a.lower) {
+      // Tiles (i, j), j <= i, in order of i: i (i + 1) / 2 + j = r.
+      int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+      while (i * (i + 1) / 2 > r) --i;
+      while ((i + 1) * (i + 2) / 2 <= r) ++i;
+      w.mt = i;
+      w.nt = r - i * (i + 1) / 2;
+    } else {
+      w.mt = r % a.tiles_s;
+      w.nt = r / a.tiles_s;
     }
+    w.n_k = ((w.kind == kPoly ? a.side : a.wide ? a.n : a.m) + product::kBK - 1) / product::kBK;
   }
-  template <bool LOWER>
-  __device__ __forceinline__ void take_as(uint32_t taddr) {
+  return w;
+}
+__device__ __forceinline__ unsigned* muon_count(const MuonChainArgs& a, int batch, int kind, int block) {
+  return a.counts + ((static_cast<size_t>(batch) * 3 + kind) * a.tiles_s + block) * kMuonCountStride;
+}
+// Waits (bounded) until both counts have reached `target`; what was counted is then visible.
+__device__ __forceinline__ bool wait_counts(const unsigned* p, const unsigned* q, unsigned target,
+                                            uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
+    unsigned v, x;
+    asm volatile(
+        "ld.relaxed.gpu.global.u32 %0, [%2];\n\t"
+        "ld.relaxed.gpu.global.u32 %1, [%3];"
+        : "=r"(v), "=r"(x)
+        : "l"(p), "l"(q)
+        : "memory");
+    if (v >= target && x >= target) {
+      asm volatile("fence.acq_rel.gpu;" ::: "memory");
+      return true;
+    }
+    if ((it & 15u) == 0u) {
+      const uint64_t t = globaltimer_ns();
+      if (it == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
+    }
+    __nanosleep(20);
+  }
+  return false;
+}
+// Waits (bounded) until this block's producer has seen the inputs of `n` tiles.
+__device__ __forceinline__ bool wait_ready(uint32_t ready, int n, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(ready) : "memory");
+    if (v >= n) return true;
+    if ((it & 63u) == 0u) {
+      const uint64_t t = globaltimer_ns();
+      if (it == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
+    }
+    __nanosleep(40);
+  }
+  return false;
+}
+// Until everything that tile `w` reads is there.
+template <int CTAS>
+__device__ __forceinline__ bool wait_inputs(const MuonChainArgs& a, const MuonUnit& w) {
+  constexpr unsigned kArrivals = CTAS * product::kEpiWarps;
+  if (w.kind == kGram && w.step == 0) return true;  // X is the kernel before's
+  const unsigned target = kArrivals * (w.kind == kGram ? a.tiles_o * w.step
+                                                       : (a.lower ? 1 : 2) * a.tiles_s * (w.step + 1));
+  const int kind = w.kind == kGram ? kNext : w.kind - 1;
+  const int s = w.kind == kNext ? (a.wide ? w.mt : w.nt) : w.mt;
+  const bool ok = wait_counts(muon_count(a, w.batch, kind, s),
+                              muon_count(a, w.batch, kind, w.kind == kNext ? s : w.nt), target, a.wait_ns);
+  // The tiles were written by ordinary stores and are read by TMA.
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return ok;
+}
+// The steps of a tile in runs whose operands lie alike in memory: f(first step,
+// end, A with K along its rows, the same of B).  Of a symmetric matrix whose
+// tiles above the diagonal are not written, block i's part beyond the diagonal
+// is read as the transpose of what is written.
+template <int CTAS, class F>
+__device__ __forceinline__ void muon_runs(const MuonChainArgs& a, const MuonUnit& w, F&& f) {
+  constexpr std::bool_constant<false> rows;
+  constexpr std::bool_constant<true> cols;
+  constexpr int kPer = 128 * CTAS / product::kBK;  // steps of a tile's width
+  if (w.kind == kGram) {
+    if (a.wide)
+      f(0, w.n_k, rows, rows);
+    else
+      f(0, w.n_k, cols, cols);
+    return;
+  }
+  const int past_m = a.lower ? min((w.mt + 1) * kPer, w.n_k) : w.n_k;  // steps up to A's diagonal tile
+  const int past_n = a.lower ? min((w.nt + 1) * kPer, w.n_k) : w.n_k;
+  if (w.kind == kPoly) {  // (nt <= mt where only tiles on and below the diagonal are)
+    f(0, past_n, rows, rows);
+    f(past_n, past_m, rows, cols);
+    f(past_m, w.n_k, cols, cols);
+  } else if (a.wide) {
+    f(0, past_m, rows, cols);
+    f(past_m, w.n_k, cols, cols);
+  } else {
+    f(0, past_n, rows, rows);
+    f(past_n, w.n_k, rows, cols);
+  }
+}
+
+// A thread's part of a tile: row `row`, kCols columns from `col`.
+template <int CTAS>
+struct MuonTile {
+  static constexpr int kCols = 64 * CTAS;
+  const MuonChainArgs& a;
+  const int kind, row, col;
+  const bool last, diagonal;
+  int rows, cols;
+  long ld;
+  size_t at;
+  float alpha, beta, diag;
+  uint4 add[kCols / 8];
+  __device__ __forceinline__ MuonTile(const MuonChainArgs& args, const MuonUnit& w, int r, int c)
+      : a(args), kind(w.kind), row(r), col(c), last(w.kind == kNext && w.step == args.steps - 1),
+        diagonal(w.kind == kPoly && w.mt == w.nt) {
+    rows = kind == kNext ? a.m : a.side;
+    cols = kind == kNext ? a.n : a.side;
+    ld = kind == kNext ? a.n : a.ld;
+    at = (static_cast<size_t>(w.batch) * rows + row) * ld + col;
+    const float* k = a.coeffs[w.step];
+    alpha = kind == kGram ? 1.0f / kMuonX : kind == kPoly ? k[2] * (kMuonP / (kMuonX * kMuonX))
+            : last        ? 1.0f / (kMuonX * kMuonP)
+                          : 1.0f / kMuonP;
+    beta = k[1] * (kMuonP / kMuonX);
+    diag = k[0] * kMuonP;
+  }
+  // What is added to A A: from L2, where other blocks' stores are.
+  __device__ __forceinline__ void fetch() {
+    const __half* p = static_cast<const __half*>(a.gram_out) + at;
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i)
+      add[i] = row < rows && col + 8 * i < cols ? __ldcg(reinterpret_cast<const uint4*>(p + 8 * i))
+                                                : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void take(uint32_t taddr, int next) {
+    void* out = kind == kGram ? a.gram_out : kind == kPoly ? a.poly_out : last ? a.o : a.x_out[next];
+    const bool on32 = ld % 16 == 0 && (!last || a.o_on32);
     each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float x = a.alpha * __uint_as_float(v[2 * i]), y = a.alpha * __uint_as_float(v[2 * i + 1]);
-        if (a.add != nullptr) {
+        float x = alpha * __uint_as_float(v[2 * i]), y = alpha * __uint_as_float(v[2 * i + 1]);
+        if (kind == kPoly) {
           const uint4 q = add[c / 8 + i / 4];
           const uint32_t s = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
-          x = fmaf(a.beta, f.x, x);
-          y = fmaf(a.beta, f.y, y);
-          if (row == col + c + 2 * i) x += a.diag;
-          if (row == col + c + 2 * i + 1) y += a.diag;
+          x = fmaf(beta, f.x, x);
+          y = fmaf(beta, f.y, y);
+          if (diagonal) {
+            if (row == col + c + 2 * i) x += diag;
+            if (row == col + c + 2 * i + 1) y += diag;
+          }
         }
-        if (a.bf16) {
+        if (last) {
           w[i] = pack_bf16x2(x, y);
         } else {
           const __half2 h = __floats2half2_rn(x, y);
           w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      const bool mine = row < a.rows;
-      __half* dst = static_cast<__half*>(a.out) + at + c;
-      if (mine) {
-        if (a.wide && col + c + 32 <= a.cols) {
+      if (row < rows) {
+        __half* dst = static_cast<__half*>(out) + at + c;
+        if (on32 && col + c + 32 <= cols) {
           store32(dst, w);
           store32(dst + 16, w + 8);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (col + c + 8 * i < a.cols)
+            if (col + c + 8 * i < cols)
               *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
-      }
-      if (LOWER && mirror) {
-        // The tile's transpose: lanes 2 k and 2 k + 1 exchange, so that each has
-        // two neighbouring rows of one column (rows of the result are whole
-        // vectors: a row past the last is never read).
-        const int odd = row & 1;
-        __half* to = static_cast<__half*>(a.out) + base + (row & ~1);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, w[i], 1);
-          const uint32_t two = odd ? __byte_perm(other, w[i], 0x7632) : __byte_perm(w[i], other, 0x5410);
-          const int k = col + c + 2 * i + odd;
-          if (k < a.rows && (row & ~1) < a.rows)
-            *reinterpret_cast<uint32_t*>(to + static_cast<size_t>(k) * a.ld) = two;
         }
       }
     });
   }
 };
-// All tiles of a result, and those of a symmetric one on and below the
-// diagonal, written twice.
-template <int CTAS>
-struct FullEpi : MuonEpi<CTAS> {
-  using MuonEpi<CTAS>::MuonEpi;
-  __device__ __forceinline__ void take(uint32_t t) { this->template take_as<false>(t); }
-};
-template <int CTAS>
-struct LowerEpi : MuonEpi<CTAS> {
-  using MuonEpi<CTAS>::MuonEpi;
-  __device__ __forceinline__ void take(uint32_t t) { this->template take_as<true>(t); }
-};
 
 template <int CTAS>
-cudaError_t launch_product_t(const CUtensorMap& ma, const CUtensorMap& mb, bool mn_a, bool mn_b,
-                             const ProductPlan& p, const MuonStoreArgs& a, cudaStream_t st) {
-  using product::launch;
-  if (p.lower)
-    return mn_a ? launch<CTAS, true, true, true, LowerEpi<CTAS>>(ma, mb, p, a, true, st)
-                : launch<CTAS, false, false, true, LowerEpi<CTAS>>(ma, mb, p, a, true, st);
-  if (mn_a) return launch<CTAS, true, true, true, FullEpi<CTAS>>(ma, mb, p, a, true, st);
-  return mn_b ? launch<CTAS, false, true, true, FullEpi<CTAS>>(ma, mb, p, a, true, st)
-              : launch<CTAS, false, false, true, FullEpi<CTAS>>(ma, mb, p, a, true, st);
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(product::kThreads, 1)
+    muon_chain_kernel(const __grid_constant__ MuonChainArgs a) {
+  using namespace product;
+  constexpr int kTile = 128 * CTAS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kNumBars];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int ready;  // this block's tiles whose inputs are there
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CTAS == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int team = blockIdx.x / CTAS, teams = gridDim.x / CTAS;
+  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto lead_bar = [&](int i) {
+    return CTAS == 2 ? map_shared_rank(smem_u32(&bars[i]), 0) : smem_u32(&bars[i]);
+  };
+  if (warp == 1) {
+    if constexpr (CTAS == 2) {
+      tmem_alloc_pair(smem_u32(&tmem_slot), 2 * kTile);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+  }
+  if (threadIdx.x == 0) {
+    ready = 0;
+    init_barriers<CTAS>(bars);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int units = a.steps * a.batch * (2 * a.sym_tiles + a.tiles_s * a.tiles_o);
+  bool ok = true;
+  int steps = 0;  // warp 1: products issued (even block), or to be issued (odd block)
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring r;
+      int it = 0, tile = 0;
+      for (int u = team; u < units && ok; u += teams) {
+        const MuonUnit w = muon_unit(a, u);
+        if (!(ok = wait_inputs<CTAS>(a, w))) break;
+        asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(&ready)), "r"(++tile) : "memory");
+        const int cur = w.step & 1;
+        // Each operand's matrix: [K contiguous, K along the rows].
+        const CUtensorMap* ma = w.kind == kPoly ? a.gram : w.kind == kNext && a.wide ? a.poly : a.x[cur];
+        const CUtensorMap* mb = w.kind == kPoly ? a.gram : w.kind == kNext && !a.wide ? a.poly : a.x[cur];
+        const int m = w.mt * kTile + rank * 128, n = w.nt * kTile + rank * 128;
+        muon_runs<CTAS>(a, w, [&](int kb0, int kb1, auto a_mn, auto b_mn) {
+          for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+            if (it >= kStages && !(ok = mbar_wait_hint(bar(kBarEmpty + r.s), r.parity ^ 1u, a.wait_ns))) break;
+            if (rank == 0) mbar_arrive_expect_tx(bar(kBarFull + r.s), CTAS * kStageBytes);
+            const uint32_t to = lead_bar(kBarFull + r.s), da = s0 + r.s * kStageBytes, db = da + kOperandBytes;
+            const int k = kb * kBK;
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+              if constexpr (CTAS == 2)
+                tma_load_3d_pair(dst, map, to, c0, c1, w.batch);
+              else
+                tma_load_3d(dst, map, to, c0, c1, w.batch);
+            };
+            if constexpr (a_mn.value) {
+              load(da, ma + 1, m, k);
+              load(da + 8192, ma + 1, m + 64, k);
+            } else {
+              load(da, ma, k, m);
+            }
+            if constexpr (b_mn.value) {
+              load(db, mb + 1, n, k);
+              load(db + 8192, mb + 1, n + 64, k);
+            } else {
+              load(db, mb, k, n);
+            }
+            r.next();
+          }
+        });
+      }
+      bool landed = true;
+      if (rank == 0)
+        for (int k = it > kStages ? it - kStages : 0; k < it && landed; ++k)
+          landed = mbar_wait_hint(bar(kBarFull + k % kStages), (k / kStages) & 1, a.wait_ns);
+      if (!ok || !landed) atomicOr(&g_product_status, 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank != 0) {
+    for (int u = team; u < units; u += teams) steps += muon_unit(a, u).n_k;
+  } else if (warp == 1) {
+    Ring r;
+    int n = 0;
+    for (int u = team; u < units && ok; u += teams, ++n) {
+      const MuonUnit w = muon_unit(a, u);
+      const int acc = n & 1;
+      if (n >= 2 &&
+          !(ok = warp_all(mbar_wait_hint<CTAS == 2>(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, a.wait_ns))))
+        break;
+      tc_fence_after();
+      muon_runs<CTAS>(a, w, [&](int kb0, int kb1, auto a_mn, auto b_mn) {
+        constexpr uint32_t kId = idesc(kTile, kTile, a_mn.value, b_mn.value, true);
+        constexpr uint32_t kStepA = a_mn.value ? 2048u : 32u, kStepB = b_mn.value ? 2048u : 32u;
+        const uint64_t dA0 = sdesc_sw128(s0, a_mn.value ? 8192 : 16, 1024);
+        const uint64_t dB0 = sdesc_sw128(s0 + kOperandBytes, b_mn.value ? 8192 : 16, 1024);
+        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+          // A tile's first operands wait for other blocks' tiles, as long as their
+          // copies' producer does and a little longer.
+          if (!(ok = warp_all(mbar_wait_hint(bar(kBarFull + r.s), r.parity, kb == 0 ? 3 * a.wait_ns : a.wait_ns)))) break;
+          tc_fence_after();
+          const uint64_t da = desc_add(dA0, r.s * kStageBytes), db = desc_add(dB0, r.s * kStageBytes);
+          if constexpr (CTAS == 2) {
+            mma_ss_x4_pair(tmem + acc * kTile, da, desc_add(da, kStepA), desc_add(da, 2 * kStepA),
+                           desc_add(da, 3 * kStepA), db, desc_add(db, kStepB), desc_add(db, 2 * kStepB),
+                           desc_add(db, 3 * kStepB), kId, kb > 0 ? 1u : 0u);
+            mma_commit_pair(bar(kBarEmpty + r.s));
+          } else {
+            mma_ss_x4(tmem + acc * kTile, da, desc_add(da, kStepA), desc_add(da, 2 * kStepA),
+                      desc_add(da, 3 * kStepA), db, desc_add(db, kStepB), desc_add(db, 2 * kStepB),
+                      desc_add(db, 3 * kStepB), kId, kb > 0 ? 1u : 0u);
+            mma_commit(bar(kBarEmpty + r.s));
+          }
+          r.next();
+          ++steps;
+        }
+      });
+      if (ok) {
+        if constexpr (CTAS == 2)
+          mma_commit_pair(bar(kBarAcc + acc));
+        else
+          mma_commit(bar(kBarAcc + acc));
+      }
+    }
+    if constexpr (CTAS == 2)
+      mma_commit_pair(bar(kBarDrain));
+    else
+      mma_commit(bar(kBarDrain));
+  } else if (warp >= kFirstEpiWarp) {
+    const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+    const uint32_t tl = tmem + half * MuonTile<CTAS>::kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    int n = 0;
+    for (int u = team; u < units; u += teams, ++n) {
+      const MuonUnit w = muon_unit(a, u);
+      const int acc = n & 1;
+      MuonTile<CTAS> t(a, w, w.mt * kTile + rank * 128 + quarter * 32 + lane,
+                       w.nt * kTile + half * MuonTile<CTAS>::kCols);
+      if (w.kind == kPoly) {
+        // The producer has seen what this tile reads, and says so here.
+        if (!(ok = warp_all(wait_ready(smem_u32(&ready), n + 1, 3 * a.wait_ns)))) break;
+        t.fetch();
+      }
+      if (!(ok = warp_all(mbar_wait_hint(bar(kBarAcc + acc), (n >> 1) & 1, 4 * a.wait_ns)))) break;
+      tc_fence_after();
+      t.take(tl + acc * kTile, (w.step & 1) ^ 1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 2)
+          mbar_arrive_pair(lead_bar(kBarAccFree + acc));
+        else
+          mbar_arrive(bar(kBarAccFree + acc));
+      }
+      if (t.last) continue;
+      // Once this warp's part is there for all blocks, it counts.
+      if (lane == 0) {
+        __threadfence();
+        auto count = [&](int block) {
+          asm volatile("red.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(muon_count(a, w.batch, w.kind, block))
+                       : "memory");
+        };
+        if (w.kind == kNext) {
+          count(a.wide ? w.mt : w.nt);
+        } else {
+          count(w.mt);
+          if (w.mt != w.nt || !a.lower) count(w.nt);
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&g_product_status, 1u);
+  }
+  tc_fence_before();
+  __syncthreads();
+  // As in product_kernel: each block waits for its own copies of the last commits.
+  if (warp == 1) {
+    for (int k = steps > kStages ? steps - kStages : 0; k < steps && ok; ++k)
+      ok = warp_all(mbar_wait_hint(bar(kBarEmpty + k % kStages), (k / kStages) & 1, a.wait_ns));
+    if (!warp_all(mbar_wait_hint(bar(kBarDrain), 0, a.wait_ns)) || !ok) {
+      if (lane == 0) atomicOr(&g_product_status, 1u);
+    }
+    __syncwarp();
+  }
+  if constexpr (CTAS == 2) cluster_sync();
+  if (threadIdx.x >> 5 == 1) {
+    tc_fence_after();
+    if constexpr (CTAS == 2)
+      tmem_dealloc_pair(tmem_slot, 2 * kTile);
+    else
+      tmem_dealloc(tmem_slot, 2 * kTile);
+  }
+}
+
+template <int CTAS>
+cudaError_t launch_chain_t(const MuonChainArgs& a, long units, cudaStream_t st) {
+  // Teams that are resident at once, by device (0: not asked yet).  Their number
+  // changes no bit: a tile's sum is one team's whatever the team.
+  static int resident[64] = {};
+  static unsigned long long attr_ctx[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long ctx = current_context_id();
+  auto* kernel = muon_chain_kernel<CTAS>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = product::kThreads;
+  cfg.dynamicSmemBytes = product::kSmemBytes;
+  cfg.stream = st;
+  int teams = dev < 64 && ctx != 0 && attr_ctx[dev] == ctx ? resident[dev] : 0;
+  if (teams == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if constexpr (CTAS == 1) {
+      int per_sm = 0, sms = 0;
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, product::kThreads, product::kSmemBytes);
+      if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      teams = per_sm * sms;
+    } else {
+      cfg.gridDim = dim3(kProductSms);
+      e = cudaOccupancyMaxActiveClusters(&teams, kernel, &cfg);
+    }
+    if (e != cudaSuccess) return e;
+    if (teams < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) {
+      resident[dev] = teams;
+      attr_ctx[dev] = ctx;
+    }
+  }
+  if (teams > product_teams(CTAS)) teams = product_teams(CTAS);
+  if (teams > units) teams = static_cast<int>(units);
+  cfg.gridDim = dim3(static_cast<unsigned>(CTAS * teams));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -279,19 +658,29 @@ cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st) {
 cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st) {
   return launch_dependent(muon_scale_kernel, dim3(a.blocks, a.batch), kInThreads, st, true, a);
 }
-ProductPlan muon_plan(long M, long N, long K, int batch, bool symmetric) {
-  ProductPlan best{};
+MuonPlan muon_plan(int batch, int m, int n) {
+  const long side = m < n ? m : n, other = m < n ? n : m;
+  MuonPlan best{};
   double least = 0.0;
   for (int form = 0; form < 4; ++form) {
-    const int ctas = 1 + (form & 1);
-    const bool lower = form >= 2;
-    if (lower && !symmetric) continue;
-    const ProductPlan p = product_plan(ctas, M, N, K, batch, lower, false);
-    // Clocks: rounds of tiles, 512 a step of K for a pair, 256 for a block and a
-    // quarter more for its loads, then the last tile's epilogue.
-    const long rounds = (p.units + product_teams(ctas) - 1) / product_teams(ctas);
-    const double cost = static_cast<double>(rounds) * p.n_k * (ctas == 2 ? 512.0 : 320.0) +
-                        ctas * (lower ? 2200.0 : 1600.0);
+    MuonPlan p{};
+    p.ctas = 1 + (form & 1);
+    p.lower = form >> 1;
+    const long tile = 128 * p.ctas, teams = product_teams(p.ctas);
+    p.tiles_s = static_cast<int>((side + tile - 1) / tile);
+    p.tiles_o = static_cast<int>((other + tile - 1) / tile);
+    p.sym_tiles = p.lower ? p.tiles_s * (p.tiles_s + 1) / 2 : p.tiles_s * p.tiles_s;
+    p.units = static_cast<long>(batch) * (2l * p.sym_tiles + static_cast<long>(p.tiles_s) * p.tiles_o);
+    // Clocks of a step: a product takes its share of the teams' time and at least
+    // one tile's; a pair's step of 64 along K takes about 600, a block's 400
+    // (what L2 delivers to all of them).
+    auto product_clocks = [&](long tiles, long k) {
+      const double t = static_cast<double>((k + 63) / 64) * (p.ctas == 2 ? 600.0 : 400.0) + p.ctas * 2000.0;
+      const double all = t * static_cast<double>(tiles) * batch / static_cast<double>(teams);
+      return all > t ? all : t;
+    };
+    const double cost = product_clocks(p.sym_tiles, other) + product_clocks(p.sym_tiles, side) +
+                        product_clocks(static_cast<long>(p.tiles_s) * p.tiles_o, side);
     if (form == 0 || cost < least) {
       least = cost;
       best = p;
@@ -299,10 +688,8 @@ ProductPlan muon_plan(long M, long N, long K, int batch, bool symmetric) {
   }
   return best;
 }
-cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, bool mn_a, bool mn_b,
-                                const ProductPlan& p, const MuonStoreArgs& a, cudaStream_t st) {
-  return p.ctas == 2 ? launch_product_t<2>(ma, mb, mn_a, mn_b, p, a, st)
-                     : launch_product_t<1>(ma, mb, mn_a, mn_b, p, a, st);
+cudaError_t launch_muon_chain(const MuonChainArgs& a, int ctas, long units, cudaStream_t st) {
+  return ctas == 2 ? launch_chain_t<2>(a, units, st) : launch_chain_t<1>(a, units, st);
 }
 cudaError_t take_muon_status(cudaStream_t st, unsigned* out) { return product::take_status(st, out); }
 cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {

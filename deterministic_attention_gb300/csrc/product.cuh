@@ -86,6 +86,20 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn,
   return f16 ? (idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10))) : idesc_bf16(M, N, a_mn, b_mn);
 }
 
+template <int CTAS>
+__device__ __forceinline__ void init_barriers(uint64_t* bars) {
+  auto init = [&](int i, uint32_t count) { mbar_init(smem_u32(&bars[i]), count); };
+  for (int s = 0; s < kStages; ++s) {
+    init(kBarFull + s, 1);
+    init(kBarEmpty + s, 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    init(kBarAcc + i, 1);
+    init(kBarAccFree + i, CTAS * kEpiWarps);
+  }
+  init(kBarDrain, 1);
+}
+
 // ---------------------------------------------------------------- units of work
 struct Unit {
   int batch, mt, nt;   // tile
@@ -96,22 +110,10 @@ struct Unit {
 // in a band column by column: the teams at work at one time share few
 // rows of either operand.
 __device__ __forceinline__ void tile_at(const ProductPlan& p, int t, int* mt, int* nt) {
-  if (p.lower) {
-    // Tiles (i, j), j <= i, in order of i: i (i + 1) / 2 + j = t.
-    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > t) --i;
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    *mt = i;
-    *nt = t - i * (i + 1) / 2;
-  } else {
-    const int band = t / (p.band * p.tiles_n), m0 = band * p.band, rows = min(p.band, p.tiles_m - m0);
-    const int r = t - m0 * p.tiles_n;
-    *mt = m0 + r % rows;
-    *nt = r / rows;
-  }
-}
-__device__ __forceinline__ int tiles_of(const ProductPlan& p) {
-  return p.lower ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+  const int band = t / (p.band * p.tiles_n), m0 = band * p.band, rows = min(p.band, p.tiles_m - m0);
+  const int r = t - m0 * p.tiles_n;
+  *mt = m0 + r % rows;
+  *nt = r / rows;
 }
 __device__ __forceinline__ Unit unit_at(const ProductPlan& p, int u) {
   Unit w;
@@ -128,7 +130,7 @@ __device__ __forceinline__ Unit unit_at(const ProductPlan& p, int u) {
       w.part = r;
     }
   }
-  const int per = tiles_of(p);
+  const int per = p.tiles_m * p.tiles_n;
   w.batch = tile / per;
   tile_at(p, tile - w.batch * per, &w.mt, &w.nt);
   return w;
@@ -169,15 +171,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarAcc + i), 1);
-      mbar_init(bar(kBarAccFree + i), CTAS * kEpiWarps);
-    }
-    mbar_init(bar(kBarDrain), 1);
+    init_barriers<CTAS>(bars);
     fence_barrier_init();
   }
   if (threadIdx.x == 32) {

@@ -29,11 +29,9 @@ cudaError_t launch_turn(const TurnArgs& a, cudaStream_t st);
 // Work of one launch of the tensor-core product (product.cuh): C tiles of
 // 128 CTAS x 128 CTAS, CTAS = 1 or 2 blocks on one tile.
 struct ProductPlan {
-  int ctas;                // blocks on one tile
   int tiles_m, tiles_n, batch;
   int n_k;                 // steps of 64 along K
   int band;                // tile rows that are walked together, column by column
-  int lower;               // 1: only tiles on and below the diagonal (tiles_m = tiles_n)
   int whole;               // tiles computed by one team each
   int splits;              // K ranges of each of the other tiles (1: none cut)
   int units;               // whole + (tiles - whole) * splits
@@ -46,7 +44,7 @@ constexpr int kProductSms = 152;
 inline int product_teams(int ctas) { return kProductSms / ctas; }
 // cut: whether tiles of an incomplete last round are cut along K (the caller
 // has then room for partial tiles and adds them up).
-ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool lower, bool cut);
+ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool cut);
 inline size_t product_partial_bytes(const ProductPlan& p, int ctas) {
   const size_t cut = static_cast<size_t>(p.tiles_m) * p.tiles_n * p.batch - p.whole;
   return p.splits == 1 ? 0 : cut * p.splits * (128 * ctas) * (128 * ctas) * sizeof(float);
@@ -115,6 +113,8 @@ struct MuonInArgs {
   const void* g;           // bf16 or fp32 [batch, m * n]
   float* momentum;         // fp32 [batch, m * n] or null
   double* sums;            // [batch][blocks]
+  unsigned* counts;        // [n_counts] put to zero
+  int n_counts;
   void* x;                 // fp16 [batch, m * n]: the update over its norm, times kMuonX
   long count;              // m * n (a multiple of 8)
   int batch, blocks;       // blocks per matrix
@@ -127,24 +127,38 @@ constexpr float kMuonX = 4096.0f, kMuonP = 1024.0f;
 int muon_sum_blocks(int batch, long count);
 cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st);
 cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st);
-// The plan of a product of muon_update: one or two blocks on a tile; all of a
-// symmetric result's tiles or those on and below the diagonal.
-ProductPlan muon_plan(long M, long N, long K, int batch, bool symmetric);
-struct MuonStoreArgs {
-  void* out;               // fp16 (or, last, bf16) [batch][rows][ld]
-  const void* add;         // fp16 [batch][rows][ld] or null
-  long batch_stride;       // elements, of out and add
-  int rows, cols;
+// Counts lie on lines of their own: many blocks look at one while others add to
+// the next.
+constexpr int kMuonCountStride = 32;
+// All products of an update in one launch (muon.cu).
+struct MuonChainArgs {
+  // Of each matrix a map for operands with K contiguous and one for K along the rows.
+  CUtensorMap x[2][2];     // X in either buffer
+  CUtensorMap gram[2], poly[2];
+  void* x_out[2];          // fp16 [batch, m, n]
+  void* gram_out;          // fp16 [batch, side, ld]
+  void* poly_out;
+  void* o;                 // bf16 [batch, m, n]
+  unsigned* counts;        // [batch][3][tiles_s], zero at the start
+  int batch, m, n, side;
   long ld;
-  float alpha, beta, diag; // out = alpha * sum + beta * add + diag on the diagonal
-  int bf16;
-  int wide;                // rows of out begin on 32 bytes
+  int steps;
+  int tiles_s, tiles_o;    // tiles along the shorter side and along the other
+  int sym_tiles;           // tiles of a symmetric product that are computed
+  int lower;               // those on and below the diagonal, else all
+  int wide;                // m <= n
+  int o_on32;              // rows of o begin on 32 bytes
+  int teams;
+  unsigned long long wait_ns;
+  float coeffs[64][3];
 };
-// mn_a, mn_b: whether K runs along the operand's rows in memory (0, 0: X X^T of
-// rows; 1, 1: of columns; 0, 1: P X).
-cudaError_t launch_muon_product(const CUtensorMap& ma, const CUtensorMap& mb, bool mn_a, bool mn_b,
-                                const ProductPlan& p, const MuonStoreArgs& a,
-                                cudaStream_t st);
+struct MuonPlan {
+  int ctas;                // blocks on one tile: of 128 x 128, or two on 256 x 256
+  int tiles_s, tiles_o, lower, sym_tiles;
+  long units;              // tiles of all products of one step, all matrices
+};
+MuonPlan muon_plan(int batch, int m, int n);
+cudaError_t launch_muon_chain(const MuonChainArgs& a, int ctas, long units, cudaStream_t st);
 cudaError_t take_muon_status(cudaStream_t st, unsigned* out);
 cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
 

@@ -152,7 +152,7 @@ def test_rope_refuses_views_it_cannot_walk():
         da.rope_fwd(x, None, f.float())
     with pytest.raises(TypeError):
         da.rope_fwd(x.half(), None, f)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         da.rope_fwd(x, x[:, :, :1].float(), f)
     with pytest.raises(da.DetAttnError):
         da.rope_fwd(x[..., :32].contiguous(), None, f)      # more components than a head has
