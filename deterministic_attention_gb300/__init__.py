@@ -831,7 +831,7 @@ def _heads(t, name, dev, dtype=None):
 def _heads_out(o, name, t, N, T, H, D, dev):
     """(result like t, token stride): o, or a new contiguous tensor."""
     if o is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device), H * D
+        return torch.empty_like(t, memory_format=torch.contiguous_format), H * D
     No, To, Ho, Do, ld = _heads(o, name, dev, t.dtype)
     if No != N or To != T or Ho != H or Do != D:
         raise ValueError(f"{name} is {tuple(o.shape)}, expected {tuple(t.shape)}")

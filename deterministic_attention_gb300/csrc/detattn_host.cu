@@ -2237,7 +2237,8 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
     if ((rc = launched(launch_ce_dz(mx, mw, p, ga, st), "linear_ce_bwd (dz)")) != DETATTN_OK) return rc;
     p = product_plan(2, N, d, width, 1, true);
     p.wait_ns = g_wait_ns;
-    CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0, d % 16 == 0 && on32(dx)};
+    CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0,
+                   d % 16 == 0 && (!last || on32(dx))};
     if ((rc = launched(launch_ce_dx(mz, mwk, p, sa, st), "linear_ce_bwd (dx)")) != DETATTN_OK) return rc;
     p = product_plan(2, width, d, N, 1, true);
     p.wait_ns = g_wait_ns;

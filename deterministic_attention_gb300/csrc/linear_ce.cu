@@ -37,16 +37,17 @@ constexpr int kSumThreads = 256;
 // ------------------------------------------------------------ forward
 struct StatsEpi {
   static constexpr int kCols = 128;
+  static constexpr bool kOwnInputs = true;
   using Args = CeStatsArgs;
-  const Args& a;
-  int row, col, target, part;
-  __device__ __forceinline__ StatsEpi(const Args& args, const product::Unit& w, int r, int c, int)
-      : a(args), row(r), col(c) {
-    target = row < a.N ? a.targets[row] : -1;
-    part = 2 * w.nt + (c >> 7 & 1);
-    if (target >= a.V && c == 0) atomicOr(&g_product_status, 2u);
+  const Args* args;
+  int row, col, target;
+  __device__ __forceinline__ StatsEpi(const Args& a, const product::Unit&, int r, int c)
+      : args(&a), row(r), col(c), target(row < a.N ? a.targets[row] : -1) {}
+  __device__ __forceinline__ void prepare() {
+    if (target >= args->V && col == 0) atomicOr(&g_product_status, 2u);
   }
   __device__ __forceinline__ void take(uint32_t taddr) {
+    const Args& a = *args;
     float m = -INFINITY, s = 0.0f;
     each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       const int c0 = col + c;
@@ -80,51 +81,70 @@ struct StatsEpi {
         a.z_target[row] = z;
       }
     });
-    if (row < a.N) a.part[static_cast<size_t>(part) * a.N + row] = make_float2(m, s);
+    if (row < a.N) a.part[static_cast<size_t>(col / kCols) * a.N + row] = make_float2(m, s);
   }
 };
 
-// A block merges kFinishRows rows; kFinishGroups threads share a row's parts:
-// first the largest logit of all, then the sums brought to it.  A part's sum is
-// 2^r times what its largest logit asks for, r the rounding of m log2e: it is
-// taken back here, so that loss does not lose what lse does.
-constexpr int kFinishRows = 8, kFinishGroups = 64;
-__global__ void __launch_bounds__(kFinishRows* kFinishGroups) ce_finish_kernel(const CeFinishArgs a) {
-  __shared__ float sh[kFinishGroups][kFinishRows];
+// A block merges kFinishRows rows; the threads that share a row take its parts
+// eight at a time.  A part's sum is 2^r times what its largest logit asks for, r
+// the rounding of m log2e: it is taken back here, so that loss does not lose what
+// lse does.
+constexpr int kFinishRows = 8, kFinishWarps = 16, kFinishGroups = kFinishWarps * 32 / kFinishRows;
+struct Merged {
+  float m = -INFINITY, s = 0.0f;
+  __device__ __forceinline__ void add(float m1, float s1) {
+    const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
+    s = s * exp2f((m - base) * kLog2e) + s1 * exp2f((m1 - base) * kLog2e);
+    m = top;
+  }
+};
+__global__ void __launch_bounds__(kFinishWarps * 32) ce_finish_kernel(const CeFinishArgs a) {
+  __shared__ float2 sh[kFinishWarps][kFinishRows];
   griddep_launch_dependents();
-  griddep_wait();
   const int lane = threadIdx.x % kFinishRows, group = threadIdx.x / kFinishRows;
-  const int row = blockIdx.x * kFinishRows + lane;
-  const float2* p = a.part + min(row, a.N - 1);
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = group; i < a.parts; i += kFinishGroups) m = fmaxf(m, p[static_cast<size_t>(i) * a.N].x);
-  sh[group][lane] = m;
-  for (int o = kFinishGroups / 2; o > 0; o >>= 1) {
-    __syncthreads();
-    if (group < o) sh[group][lane] = fmaxf(sh[group][lane], sh[group + o][lane]);
-  }
-  __syncthreads();
-  m = sh[0][lane];
-  __syncthreads();
-  const float base = m == -INFINITY ? 0.0f : m;
-  float s = 0.0f;
-#pragma unroll 8
-  for (int i = group; i < a.parts; i += kFinishGroups) {
-    const float2 x = p[static_cast<size_t>(i) * a.N];
-    const float r = x.x == -INFINITY ? 0.0f : fmaf(x.x, kLog2e, -(x.x * kLog2e));
-    s += x.y * exp2f((x.x - base) * kLog2e - r);
-  }
-  sh[group][lane] = s;
-  for (int o = kFinishGroups / 2; o > 0; o >>= 1) {
-    __syncthreads();
-    if (group < o) sh[group][lane] += sh[group + o][lane];
-  }
-  if (group != 0 || row >= a.N) return;
-  const float ln = logf(sh[0][lane]);
+  const int row = min(blockIdx.x * kFinishRows + lane, a.N - 1);
   const int t = a.targets[row];
-  a.lse[row] = m + ln;
-  a.loss[row] = t >= 0 && t < a.V ? (m - a.z_target[row]) + ln : 0.0f;
+  griddep_wait();
+  const float2* p = a.part + row;
+  Merged all;
+  for (int i0 = group; i0 < a.parts; i0 += 8 * kFinishGroups) {
+    float2 x[8];
+    float m = all.m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kFinishGroups;
+      x[k] = i < a.parts ? p[static_cast<size_t>(i) * a.N] : make_float2(-INFINITY, 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, x[k].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s = all.s * exp2f((all.m - base) * kLog2e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float r = x[k].x == -INFINITY ? 0.0f : fmaf(x[k].x, kLog2e, -(x[k].x * kLog2e));
+      s += x[k].y * exp2f((x[k].x - base) * kLog2e - r);
+    }
+    all.m = m;
+    all.s = s;
+  }
+#pragma unroll
+  for (int o = kFinishRows; o < 32; o <<= 1) {
+    const float m1 = __shfl_xor_sync(0xFFFFFFFFu, all.m, o), s1 = __shfl_xor_sync(0xFFFFFFFFu, all.s, o);
+    all.add(m1, s1);
+  }
+  if ((threadIdx.x & 31) < kFinishRows) sh[threadIdx.x >> 5][lane] = make_float2(all.m, all.s);
+  __syncthreads();
+  if (threadIdx.x >= kFinishRows) return;
+  all = Merged();
+#pragma unroll
+  for (int i = 0; i < kFinishWarps; ++i) all.m = fmaxf(all.m, sh[i][lane].x);
+  const float base = all.m == -INFINITY ? 0.0f : all.m;
+#pragma unroll
+  for (int i = 0; i < kFinishWarps; ++i) all.s += sh[i][lane].y * exp2f((sh[i][lane].x - base) * kLog2e);
+  if (blockIdx.x * kFinishRows + lane >= static_cast<unsigned>(a.N)) return;
+  const float ln = logf(all.s);
+  a.lse[row] = all.m + ln;
+  a.loss[row] = t >= 0 && t < a.V ? (all.m - a.z_target[row]) + ln : 0.0f;
 }
 
 // ------------------------------------------------------------ backward: dz of a piece
@@ -150,55 +170,59 @@ __global__ void __launch_bounds__(1024) ce_unit_kernel(const int* __restrict__ t
 
 struct GradEpi {
   static constexpr int kCols = 128;
+  static constexpr bool kOwnInputs = true;
   using Args = CeGradArgs;
-  const Args& a;
+  const Args* args;
   int row, col, target;
-  float lse2, g;       // g: dloss over the unit
+  float lse2, g, gp;   // dloss and dloss + dlse, then over the unit
   uint32_t live, sign; // masks of a pair
-  __device__ __forceinline__ GradEpi(const Args& args, const product::Unit&, int r, int c, int)
-      : a(args), row(r), col(c), target(-1), lse2(0.0f), g(0.0f), live(0u), sign(0u) {
+  __device__ __forceinline__ GradEpi(const Args& a, const product::Unit&, int r, int c)
+      : args(&a), row(r), col(c), target(-1), lse2(0.0f), g(0.0f), gp(0.0f), live(0u), sign(0u) {
     if (row < a.N) {
-      const float unit = *a.unit;
       target = a.targets[row];
-      lse2 = a.lse[row] * kLog2e;
-      if (target >= a.V && c == 0 && a.v0 == 0) atomicOr(&g_product_status, 2u);
-      if (target >= a.V) target = -1;
-      if (target >= 0) g = a.dloss[row];
-      const float gp = (g + (a.dlse != nullptr ? a.dlse[row] : 0.0f)) / unit;
-      g /= unit;
-      // gp exp(z - lse) = +-2^(z log2e - (lse log2e - log2 |gp|)); a row that takes
-      // no gradient is zero whatever its logits are.
-      live = gp != 0.0f || g != 0.0f ? 0xFFFFFFFFu : 0u;
-      lse2 -= log2f(fabsf(gp));
-      if (gp < 0.0f) sign = 0x80008000u;
-      target -= a.v0;  // column of the piece (none: negative)
+      lse2 = a.lse[row];
+      g = a.dloss[row];
+      if (a.dlse != nullptr) gp = a.dlse[row];
     }
   }
+  __device__ __forceinline__ void prepare() {
+    const Args& a = *args;
+    const float unit = *a.unit;
+    if (target >= a.V && col == 0 && a.v0 == 0) atomicOr(&g_product_status, 2u);
+    if (target >= a.V) target = -1;
+    if (target < 0) g = 0.0f;
+    gp = (g + gp) / unit;
+    g /= unit;
+    // gp exp(z - lse) = +-2^(z log2e - (lse log2e - log2 |gp|)); a row that takes
+    // no gradient is zero whatever its logits are.
+    live = row < a.N && (gp != 0.0f || g != 0.0f) ? 0xFFFFFFFFu : 0u;
+    lse2 = lse2 * kLog2e - log2f(fabsf(gp));
+    if (gp < 0.0f) sign = 0x80008000u;
+    target -= a.v0;  // column of the piece (none: negative)
+  }
   __device__ __forceinline__ void take(uint32_t taddr) {
+    const Args& a = *args;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dz) + static_cast<size_t>(row) * a.ld + col;
     const uint64_t nb = f2_make(-lse2, -lse2), l2 = f2_make(kLog2e, kLog2e);
     each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
-      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 32; i += 2) {
         float p, q;
-        f2_split(f2_fma(f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), l2, nb), p, q);
-        p = ex2_approx(p);
-        q = ex2_approx(q);
-        v[2 * i] = __float_as_uint(p);
-        v[2 * i + 1] = __float_as_uint(q);
-        w[i] = (pack_bf16x2(p, q) ^ sign) & live;
+        f2_split(f2_fma(f2_make(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), l2, nb), p, q);
+        v[i] = __float_as_uint(ex2_approx(p));
+        v[i + 1] = __float_as_uint(ex2_approx(q));
       }
       const unsigned at = static_cast<unsigned>(target - (col + c));
       if (at < 32u) {
-        // The target's pair again, with -g.
-        const float s = sign ? -1.0f : 1.0f;
+        const float s = sign ? -g : g;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = s * __uint_as_float(v[2 * i]), q = s * __uint_as_float(v[2 * i + 1]);
-          if (at >> 1 == static_cast<unsigned>(i)) w[i] = pack_bf16x2(at & 1 ? p : p - g, at & 1 ? q - g : q) & live;
-        }
+        for (int i = 0; i < 32; ++i)
+          v[i] = __float_as_uint(__uint_as_float(v[i]) - (at == static_cast<unsigned>(i) ? s : 0.0f));
       }
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = (pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])) ^ sign) & live;
       // (Rows of the workspace are whole sectors; what lies behind the piece is never read.)
       if (row < a.N) {
         if (col + c < a.width) store32(dst + c, w);
@@ -228,44 +252,67 @@ __device__ __forceinline__ void store4(const CeStoreArgs& a, int row, int col, f
 
 struct StoreEpi {
   static constexpr int kCols = 128;
+  static constexpr bool kOwnInputs = false;
   using Args = CeStoreArgs;
-  const Args& a;
+  const Args* args;
   int row, col, part, tile_row, tile_col;
   float unit;
-  __device__ __forceinline__ StoreEpi(const Args& args, const product::Unit& w, int r, int c, int)
-      : a(args), row(r), col(c), part(w.part), tile_row(r - w.mt * kCeTile), tile_col(c - w.nt * kCeTile),
-        unit(*args.unit) {}
+  __device__ __forceinline__ StoreEpi(const Args& a, const product::Unit& w, int r, int c)
+      : args(&a), row(r), col(c), part(w.part), tile_row(r - w.mt * kCeTile), tile_col(c - w.nt * kCeTile),
+        unit(*a.unit) {}
+  __device__ __forceinline__ void prepare() {}
   __device__ __forceinline__ void take(uint32_t taddr) {
+    const Args& a = *args;
     each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
-      auto four = [&](int i) {
-        return make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
-                           __uint_as_float(v[i + 3]));
-      };
       if (part >= 0) {
         float* dst = a.partial + (static_cast<size_t>(part) * kCeTile + tile_row) * kCeTile + tile_col + c;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) store32(dst + i, v + i);
-      } else if (row < a.rows) {
-        const size_t at = static_cast<size_t>(row) * a.cols + col + c;
-        if (!a.add && a.out != nullptr && !a.out_fp32) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at;
-          uint32_t w[16];
+        return;
+      }
+      if (row >= a.rows) return;
+      const size_t at = static_cast<size_t>(row) * a.cols + col + c;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * unit, __uint_as_float(v[2 * i + 1]) * unit);
-          if (a.wide && col + c + 32 <= a.cols) {
-            store32(dst, w);
-            store32(dst + 16, w + 8);
-          } else {
+      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * unit);
+      if (a.add) {
+        // All of the loads, then the sums: one latency for 32 columns.
+        float4 o[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + c + 8 * i < a.cols)
-                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          }
+        for (int i = 0; i < 8; ++i)
+          o[i] = col + c + 4 * i < a.cols ? *reinterpret_cast<const float4*>(a.acc + at + 4 * i)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + o[i].x);
+          v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + o[i].y);
+          v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + o[i].z);
+          v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + o[i].w);
+        }
+      }
+      const bool whole = col + c + 32 <= a.cols;
+      if (a.out == nullptr || a.out_fp32) {
+        float* dst = (a.out == nullptr ? a.acc : static_cast<float*>(a.out)) + at;
+        if (whole && a.wide) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) store32(dst + i, v + i);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            if (col + c + i < a.cols) store4(a, row, col + c + i, four(i), unit);
+            if (col + c + i < a.cols) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        if (whole && a.wide) {
+          store32(dst, w);
+          store32(dst + 16, w + 8);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + c + 8 * i < a.cols)
+              *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
     });
@@ -344,7 +391,7 @@ cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const 
 
 cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st) {
   return launch_dependent(ce_finish_kernel, dim3(static_cast<unsigned>((a.N + kFinishRows - 1) / kFinishRows)),
-                          kFinishRows * kFinishGroups, st, true, a);
+                          kFinishWarps * 32, st, true, a);
 }
 
 cudaError_t launch_ce_unit(const int* targets, const float* dloss, float* unit, int N, int V,

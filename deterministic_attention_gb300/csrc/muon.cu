@@ -85,28 +85,44 @@ __global__ void __launch_bounds__(kInThreads) muon_momentum_kernel(const MuonInA
   const size_t base = static_cast<size_t>(blockIdx.y) * a.count;
   const long vecs = a.count / 8;
   double total = 0.0;
-  for (long i = static_cast<long>(blockIdx.x) * kInThreads + threadIdx.x; i < vecs;
-       i += static_cast<long>(a.blocks) * kInThreads) {
-    const size_t at = base + static_cast<size_t>(i) * 8;
-    float g[8];
-    load8(a, at, g);
-    if (a.momentum != nullptr) {
-      float m[8];
-      load_momentum(a, at, m);
+  Squares sq;
+  int n = 0;
+  const long step = static_cast<long>(a.blocks) * kInThreads;
+  // Two vectors at a time: the loads of both, then the rest.
+  for (long i = static_cast<long>(blockIdx.x) * kInThreads + threadIdx.x; i < vecs; i += 2 * step) {
+    float g[2][8], m[2][8];
+    const size_t at[2] = {base + static_cast<size_t>(i) * 8, base + static_cast<size_t>(i + step) * 8};
+    const bool both = i + step < vecs;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = fmaf(a.beta, m[j], g[j]);
-        g[j] = a.nesterov ? fmaf(a.beta, m[j], g[j]) : m[j];
+    for (int k = 0; k < 2; ++k)
+      if (k == 0 || both) {
+        load8(a, at[k], g[k]);
+        if (a.momentum != nullptr) load_momentum(a, at[k], m[k]);
       }
-      float4* p = reinterpret_cast<float4*>(a.momentum + at);
-      p[0] = make_float4(m[0], m[1], m[2], m[3]);
-      p[1] = make_float4(m[4], m[5], m[6], m[7]);
-    }
-    Squares sq;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq.add(g[j]);
-    total += sq.total();
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !both) continue;
+      if (a.momentum != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          m[k][j] = fmaf(a.beta, m[k][j], g[k][j]);
+          g[k][j] = a.nesterov ? fmaf(a.beta, m[k][j], g[k][j]) : m[k][j];
+        }
+        float4* p = reinterpret_cast<float4*>(a.momentum + at[k]);
+        p[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
+        p[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq.add(g[k][j]);
+    }
+    // In fp32 for 256 squares at most, then in double (whose rate is 1/64 of fp32's).
+    if (++n == 16) {
+      total += sq.total();
+      sq = Squares();
+      n = 0;
+    }
   }
+  total += sq.total();
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = total;
   __syncthreads();
@@ -120,6 +136,7 @@ __global__ void __launch_bounds__(kInThreads) muon_momentum_kernel(const MuonInA
 // X = kMuonX u / (|u| + eps) in fp16.
 __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs a) {
   __shared__ double sh[kInThreads / 32];
+  __shared__ float factors[2];
   griddep_launch_dependents();
   griddep_wait();
   double total = 0.0;
@@ -128,39 +145,47 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = total;
   __syncthreads();
-  total = 0.0;
-  for (int i = 0; i < kInThreads / 32; ++i) total += sh[i];
-  // In two factors: neither the norm's inverse nor the values overflow.
-  const double norm = sqrt(total) + static_cast<double>(a.eps);
-  int e = 0;
-  const double part = frexp(norm, &e);  // norm = part 2^e
-  const float f0 = static_cast<float>(static_cast<double>(kMuonX) / part);
-  const int e0 = -e / 2, e1 = -e - e0;
-  const float s0 = exp2f(static_cast<float>(e0)), s1 = exp2f(static_cast<float>(e1)) * f0;
+  if (threadIdx.x == 0) {
+    total = 0.0;
+    for (int i = 0; i < kInThreads / 32; ++i) total += sh[i];
+    // In two factors: neither the norm's inverse nor the values overflow.
+    const double norm = sqrt(total) + static_cast<double>(a.eps);
+    int e = 0;
+    const double part = frexp(norm, &e);  // norm = part 2^e
+    const int e0 = -e / 2, e1 = -e - e0;
+    factors[0] = exp2f(static_cast<float>(e0));
+    factors[1] = exp2f(static_cast<float>(e1)) * static_cast<float>(static_cast<double>(kMuonX) / part);
+  }
+  __syncthreads();
+  const float s0 = factors[0], s1 = factors[1];
   const size_t base = static_cast<size_t>(blockIdx.y) * a.count;
   const long vecs = a.count / 8;
-  for (long i = static_cast<long>(blockIdx.x) * kInThreads + threadIdx.x; i < vecs;
-       i += static_cast<long>(a.blocks) * kInThreads) {
-    const size_t at = base + static_cast<size_t>(i) * 8;
-    float g[8];
-    if (a.momentum != nullptr && !a.nesterov) {
-      load_momentum(a, at, g);
-    } else {
-      load8(a, at, g);
-      if (a.momentum != nullptr) {
-        float m[8];
-        load_momentum(a, at, m);
+  const long step = static_cast<long>(a.blocks) * kInThreads;
+  for (long i = static_cast<long>(blockIdx.x) * kInThreads + threadIdx.x; i < vecs; i += 2 * step) {
+    const size_t at[2] = {base + static_cast<size_t>(i) * 8, base + static_cast<size_t>(i + step) * 8};
+    const bool both = i + step < vecs;
+    float g[2][8], m[2][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = fmaf(a.beta, m[j], g[j]);
+    for (int k = 0; k < 2; ++k)
+      if (k == 0 || both) {
+        if (a.momentum == nullptr || a.nesterov) load8(a, at[k], g[k]);
+        if (a.momentum != nullptr) load_momentum(a, at[k], m[k]);
       }
-    }
-    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(g[2 * j] * s0 * s1, g[2 * j + 1] * s0 * s1);
-      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !both) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        float u[2];
+#pragma unroll
+        for (int l = 0; l < 2; ++l)
+          u[l] = a.momentum == nullptr ? g[k][j + l] : a.nesterov ? fmaf(a.beta, m[k][j + l], g[k][j + l]) : m[k][j + l];
+        const __half2 h = __floats2half2_rn(u[0] * s0 * s1, u[1] * s0 * s1);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(static_cast<__half*>(a.x) + at[k]) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(static_cast<__half*>(a.x) + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

@@ -138,9 +138,14 @@ __device__ __forceinline__ Unit unit_at(const ProductPlan& p, int u) {
 
 // Epi: a class with
 //   static constexpr int kCols: columns of a thread's part of the tile (64 CTAS)
+//   static constexpr bool kOwnInputs: the operands are what the call got, not what
+//       the kernel before wrote: their copies need not wait for it
 //   struct Args
-//   __device__ Epi(const Args&, const Unit&, int row, int col, int lane)
-//       row: this thread's row of C; col: its first column; may start loads
+//   __device__ Epi(const Args&, const Unit&, int row, int col)
+//       row: this thread's row of C; col: its first column; starts loads (it runs
+//       before the tile before it is taken)
+//   __device__ void prepare()
+//       what follows from them
 //   __device__ void take(uint32_t taddr)
 //       reads kCols columns of TMEM at taddr and stores them
 template <int CTAS, bool A_MN, bool B_MN, bool F16, class Epi>
@@ -188,7 +193,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      griddep_wait();
+      if constexpr (!Epi::kOwnInputs) griddep_wait();
       Ring r;
       int it = 0;  // steps so far, over all units
       for (int u = team; u < p.units && ok; u += teams) {
@@ -286,11 +291,17 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
     const uint32_t tl = tmem + half * Epi::kCols + (static_cast<uint32_t>(quarter * 32) << 16);
     griddep_wait();
-    int n = 0;
-    for (int u = team; u < p.units; u += teams, ++n) {
+    auto part = [&](int u) {
       const Unit w = unit_at(p, u);
+      return Epi(ea, w, w.mt * kTile + rank * 128 + quarter * 32 + lane, w.nt * kTile + half * Epi::kCols);
+    };
+    int n = 0;
+    Epi next = part(team < p.units ? team : 0);
+    for (int u = team; u < p.units; u += teams, ++n) {
       const int acc = n & 1;
-      Epi e(ea, w, w.mt * kTile + rank * 128 + quarter * 32 + lane, w.nt * kTile + half * Epi::kCols, lane);
+      Epi e = next;
+      e.prepare();
+      if (u + teams < p.units) next = part(u + teams);
       if (!(ok = warp_all(mbar_wait_hint(bar(kBarAcc + acc), (n >> 1) & 1, p.wait_ns)))) break;
       tc_fence_after();
       e.take(tl + acc * kTile);
