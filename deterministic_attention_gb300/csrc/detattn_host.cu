@@ -2317,7 +2317,6 @@ int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t
   c.tiles_s = l.plan.tiles_s;
   c.tiles_o = l.plan.tiles_o;
   c.sym_tiles = l.plan.sym_tiles;
-  c.lower = l.plan.lower;
   c.wide = wide ? 1 : 0;
   c.o_on32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
   c.wait_ns = g_wait_ns;

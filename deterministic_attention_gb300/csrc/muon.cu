@@ -80,8 +80,9 @@ struct Squares {
 __global__ void __launch_bounds__(kInThreads) muon_momentum_kernel(const MuonInArgs a) {
   __shared__ double sh[kInThreads / 32];
   griddep_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < a.n_counts; i += kInThreads) a.counts[i] = 0u;
+  const int block = blockIdx.y * a.blocks + blockIdx.x;
+  for (int i = block * kInThreads + threadIdx.x; i < a.n_counts; i += a.batch * a.blocks * kInThreads)
+    a.counts[i] = 0u;
   const size_t base = static_cast<size_t>(blockIdx.y) * a.count;
   const long vecs = a.count / 8;
   double total = 0.0;
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
 // products 0.3 to 1.3, its stores 1 to 3, the fence before the count 0.7) and seen
 // 1.2 us later: with at most a dozen matrices that chain, not the rate of the
 // products, is the time.  Measured and not kept: a warp that looks at the counts ahead
-// of the producer (768 x 768: 122 us); two groups of matrices by turns (12 x 768 x 1280:
+// of the producer (768 x 768: 122 us); all tiles of a symmetric result computed
+// where the teams are idle anyway (768 x 768: 109.4 us against 110.4); two groups of matrices by turns (12 x 768 x 1280:
 // 250 us); the tiles above the diagonal written too (258 us); how an operand lies in
 // memory chosen step by step and not in runs (the issue of a product then takes
 // longer than the product: 258 us).
@@ -237,17 +239,12 @@ __device__ __forceinline__ MuonUnit muon_unit(const MuonChainArgs& a, int u) {
   } else {
     w.batch = r / a.sym_tiles;
     r -= w.batch * a.sym_tiles;
-    if (a.lower) {
-      // Tiles (i, j), j <= i, in order of i: i (i + 1) / 2 + j = r.
-      int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-      while (i * (i + 1) / 2 > r) --i;
-      while ((i + 1) * (i + 2) / 2 <= r) ++i;
-      w.mt = i;
-      w.nt = r - i * (i + 1) / 2;
-    } else {
-      w.mt = r % a.tiles_s;
-      w.nt = r / a.tiles_s;
-    }
+    // Tiles (i, j), j <= i, in order of i: i (i + 1) / 2 + j = r.
+    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > r) --i;
+    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    w.mt = i;
+    w.nt = r - i * (i + 1) / 2;
     w.n_k = ((w.kind == kPoly ? a.side : a.wide ? a.n : a.m) + product::kBK - 1) / product::kBK;
   }
   return w;
@@ -304,7 +301,7 @@ __device__ __forceinline__ bool wait_inputs(const MuonChainArgs& a, const MuonUn
   constexpr unsigned kArrivals = CTAS * product::kEpiWarps;
   if (w.kind == kGram && w.step == 0) return true;  // X is the kernel before's
   const unsigned target = kArrivals * (w.kind == kGram ? a.tiles_o * w.step
-                                                       : (a.lower ? 1 : 2) * a.tiles_s * (w.step + 1));
+                                                       : a.tiles_s * (w.step + 1));
   const int kind = w.kind == kGram ? kNext : w.kind - 1;
   const int s = w.kind == kNext ? (a.wide ? w.mt : w.nt) : w.mt;
   const bool ok = wait_counts(muon_count(a, w.batch, kind, s),
@@ -329,9 +326,9 @@ __device__ __forceinline__ void muon_runs(const MuonChainArgs& a, const MuonUnit
       f(0, w.n_k, cols, cols);
     return;
   }
-  const int past_m = a.lower ? min((w.mt + 1) * kPer, w.n_k) : w.n_k;  // steps up to A's diagonal tile
-  const int past_n = a.lower ? min((w.nt + 1) * kPer, w.n_k) : w.n_k;
-  if (w.kind == kPoly) {  // (nt <= mt where only tiles on and below the diagonal are)
+  // Steps up to the end of A's and of B's tile on the diagonal.
+  const int past_m = min((w.mt + 1) * kPer, w.n_k), past_n = min((w.nt + 1) * kPer, w.n_k);
+  if (w.kind == kPoly) {  // (nt <= mt)
     f(0, past_n, rows, rows);
     f(past_n, past_m, rows, cols);
     f(past_m, w.n_k, cols, cols);
@@ -594,7 +591,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(product::kThreads
           count(a.wide ? w.mt : w.nt);
         } else {
           count(w.mt);
-          if (w.mt != w.nt || !a.lower) count(w.nt);
+          if (w.mt != w.nt) count(w.nt);
         }
       }
     }
@@ -687,18 +684,19 @@ MuonPlan muon_plan(int batch, int m, int n) {
   const long side = m < n ? m : n, other = m < n ? n : m;
   MuonPlan best{};
   double least = 0.0;
-  for (int form = 0; form < 4; ++form) {
+  for (int ctas = 1; ctas <= 2; ++ctas) {
     MuonPlan p{};
-    p.ctas = 1 + (form & 1);
-    p.lower = form >> 1;
+    p.ctas = ctas;
     const long tile = 128 * p.ctas, teams = product_teams(p.ctas);
     p.tiles_s = static_cast<int>((side + tile - 1) / tile);
     p.tiles_o = static_cast<int>((other + tile - 1) / tile);
-    p.sym_tiles = p.lower ? p.tiles_s * (p.tiles_s + 1) / 2 : p.tiles_s * p.tiles_s;
+    p.sym_tiles = p.tiles_s * (p.tiles_s + 1) / 2;
     p.units = static_cast<long>(batch) * (2l * p.sym_tiles + static_cast<long>(p.tiles_s) * p.tiles_o);
     // Clocks of a step: a product takes its share of the teams' time and at least
     // one tile's; a pair's step of 64 along K takes about 600, a block's 400
-    // (what L2 delivers to all of them).
+    // (what L2 delivers to all of them), and a tile's start and end
+    // 2000 for each.  (768 x 768: 110 us with single blocks, 138 with pairs; 12 x 768 x
+    // 1280 276 and 226; 4096 x 6144 1,745 and 1,190.)
     auto product_clocks = [&](long tiles, long k) {
       const double t = static_cast<double>((k + 63) / 64) * (p.ctas == 2 ? 600.0 : 400.0) + p.ctas * 2000.0;
       const double all = t * static_cast<double>(tiles) * batch / static_cast<double>(teams);
@@ -706,7 +704,7 @@ MuonPlan muon_plan(int batch, int m, int n) {
     };
     const double cost = product_clocks(p.sym_tiles, other) + product_clocks(p.sym_tiles, side) +
                         product_clocks(static_cast<long>(p.tiles_s) * p.tiles_o, side);
-    if (form == 0 || cost < least) {
+    if (ctas == 1 || cost < least) {
       least = cost;
       best = p;
     }

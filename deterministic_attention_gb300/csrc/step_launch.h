@@ -144,8 +144,7 @@ struct MuonChainArgs {
   long ld;
   int steps;
   int tiles_s, tiles_o;    // tiles along the shorter side and along the other
-  int sym_tiles;           // tiles of a symmetric product that are computed
-  int lower;               // those on and below the diagonal, else all
+  int sym_tiles;           // tiles on and below the diagonal of a symmetric product
   int wide;                // m <= n
   int o_on32;              // rows of o begin on 32 bytes
   int teams;
@@ -154,7 +153,7 @@ struct MuonChainArgs {
 };
 struct MuonPlan {
   int ctas;                // blocks on one tile: of 128 x 128, or two on 256 x 256
-  int tiles_s, tiles_o, lower, sym_tiles;
+  int tiles_s, tiles_o, sym_tiles;
   long units;              // tiles of all products of one step, all matrices
 };
 MuonPlan muon_plan(int batch, int m, int n);

@@ -412,6 +412,39 @@ def test_muon_update_of_any_size(std):
     _muon_check(_muon_grad((70, 64), 5, F32, std), eps=1e-30)
 
 
+@pytest.mark.parametrize("shape", [(20, 300, 328), (9, 700, 520), (12, 704, 1304), (16, 1300, 704), (1, 1999, 2304),
+                                   (3, 1536, 1544), (2, 40, 8200), (2, 4100, 40), (200, 24, 24)])
+def test_muon_update_many_tiles(shape):
+    """Several tiles a side (of one block, and of pairs), ragged last ones, more
+    tiles than teams; against the formula in 64 bits on the GPU."""
+    g, m = _muon_grad(shape, 21, BF).cuda(), _muon_grad(shape, 22, F32, 3e-3).cuda()
+    m1, m2 = m.clone(), m.clone()
+    o, o2 = da.muon_update(g, momentum=m1), da.muon_update(g, momentum=m2)
+    _done()
+    assert torch.equal(o, o2) and torch.equal(m1, m2)
+    w = 0.95 * m.double() + g.double()
+    assert float((m1 - w).abs().max()) <= 2.0 ** -21 * float(w.abs().max())
+    u = g.double() + 0.95 * w
+    x = u / (torch.linalg.vector_norm(u, dim=(1, 2), keepdim=True) + 1e-7)
+    tall = shape[1] > shape[2]
+    x = x.mT if tall else x
+    held = lambda v, s: (v * s).half().double() / s
+    y = held(x, 4096.0)
+    for k in range(5):
+        gram = x @ x.mT
+        x = 3.4445 * x + (-4.7750 * gram + 2.0315 * gram @ gram) @ x
+        gram = held(y @ y.mT, 4096.0)
+        eye = torch.eye(gram.shape[-1], dtype=torch.float64, device="cuda")
+        y = held(3.4445 * eye - 4.7750 * gram + 2.0315 * gram @ gram, 1024.0) @ y
+        y = held(y, 4096.0) if k < 4 else y
+    # As in _muon_check, matrix by matrix.
+    got, want, near = o.double(), (x.mT if tall else x), (y.mT if tall else y)
+    norm = torch.linalg.vector_norm(want, dim=(1, 2))
+    off = torch.linalg.vector_norm(got - want, dim=(1, 2))
+    tol = 2 * torch.linalg.vector_norm(near - want, dim=(1, 2)) + 2.0 ** -8 * norm
+    assert bool((off <= tol).all()), (off / norm).max()
+
+
 def test_muon_update_zero_and_bad_matrices():
     g = _muon_grad((4, 64, 72), 6, F32)
     good = da.muon_update(g.cuda())
@@ -554,6 +587,54 @@ def test_step_on_two_streams_at_once():
     for w, g in zip(want, got):
         for x, y in zip(w, g):
             assert torch.equal(x, y)
+
+
+def test_updates_on_two_streams_at_once():
+    """Two launches whose blocks wait on one another share the GPU, and one the GPU with
+    other work."""
+    a, b = (_muon_grad(s, 30, BF).cuda() for s in ((6, 512, 640), (1, 900, 1000)))
+    x, w, t = (v.cuda() for v in _ce_inputs(512, 256, 5000, seed=31))
+    want = [da.muon_update(a), da.muon_update(b), *da.linear_ce_fwd(x, w, t)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [None] * 4
+    for _ in range(10):
+        with torch.cuda.stream(streams[0]):
+            got[0] = da.muon_update(a)
+        with torch.cuda.stream(streams[1]):
+            got[1] = da.muon_update(b)
+        with torch.cuda.stream(streams[2]):
+            got[2], got[3] = da.linear_ce_fwd(x, w, t)
+    torch.cuda.synchronize()
+    da.check_status()
+    for p, q in zip(want, got):
+        assert torch.equal(p, q)
+
+
+def test_two_updates_in_one_graph_share_a_workspace():
+    g = _muon_grad((2, 300, 520), 32, BF).cuda()
+    m1, m2 = (torch.zeros((2, 300, 520), device="cuda") for _ in range(2))
+    ws = torch.empty((da.muon_update_workspace_bytes(2, 300, 520),), dtype=torch.uint8, device="cuda")
+    o1, o2 = torch.empty_like(g), torch.empty_like(g)
+    want = da.muon_update(g, momentum=m1, workspace=ws)
+    want2 = da.muon_update(2 * g, momentum=m2, workspace=ws)
+    torch.cuda.synchronize()
+    g2 = 2 * g
+    st = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        m1.zero_(), m2.zero_()
+        st.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            m1.zero_(), m2.zero_()
+            da.muon_update(g, momentum=m1, out=o1, workspace=ws)
+            da.muon_update(g2, momentum=m2, out=o2, workspace=ws)
+    for _ in range(3):
+        o1.zero_(), o2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, want) and torch.equal(o2, want2)
+    da.check_status()
 
 
 def test_step_waits_that_run_out_are_named():

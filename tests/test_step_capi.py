@@ -131,7 +131,7 @@ def test_muon_update_valid_forms(L):
     assert L.muon_update_workspace_bytes(2, 30, 63) == 0
     x, s = 2 * 30 * 64 * 2, 2 * 30 * 32 * 2
     up = lambda b: (b + 255) // 256 * 256
-    assert L.muon_update_workspace_bytes(2, 30, 64) == 256 + 256 + 2 * up(x) + 2 * up(s) + 256
+    assert L.muon_update_workspace_bytes(2, 30, 64) == 256 + 2 * 3 * 128 + 2 * up(x) + 2 * up(s) + 256
     if not torch.cuda.is_available():
         assert L.muon_update(*dict(MUON, m=None).values(), None) == -6
 
