@@ -15,8 +15,9 @@
 // few tokens, forms their cosines and sines once in shared memory for all heads
 // of q and k while its first vectors are under way, and then moves 16-byte
 // vectors, the next loaded before the last is stored.  32 + 8 heads of 128 over
-// 65,536 positions: 209 us, 6.4 TB/s, 94 % of the copy rate (two vectors a thread at
-// once 232 us, four 261: fewer blocks fit an SM; one round of vectors a block 239).
+// 65,536 positions: 200 us, 6.7 TB/s, 99 % of the copy rate.  (Before that order of
+// loads 209 us; two vectors a thread at once 232, four 261: fewer blocks fit an
+// SM; one round of vectors a block 239; the table before the first load 363.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,37 +38,46 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& y, float x) { y = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
-// 16 bytes as floats and back.
-template <class T>
-struct Vec;
+// N elements (16, 8 or 4 bytes) as floats and back.
+template <int BYTES>
+struct Words;
 template <>
-struct Vec<float> {
-  static constexpr int n = 4;
-  static __device__ __forceinline__ void get(uint4 v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
-  }
-  static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
+struct Words<16> {
+  using type = uint4;
 };
 template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int n = 8;
-  static __device__ __forceinline__ void get(uint4 v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Words<8> {
+  using type = uint2;
+};
+template <>
+struct Words<4> {
+  using type = unsigned int;
+};
+template <class T, int N>
+struct Vec {
+  using Raw = typename Words<N * static_cast<int>(sizeof(T))>::type;
+  static constexpr int kWords = static_cast<int>(sizeof(Raw)) / 4;
+  static __device__ __forceinline__ void get(const Raw& v, float (&f)[N]) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < kWords; ++i)
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
   }
-  static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+  static __device__ __forceinline__ Raw put(const float (&f)[N]) {
+    Raw v;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(f[i]);
+      else
+        w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    return v;
   }
 };
 
@@ -87,8 +97,9 @@ __device__ __forceinline__ Head<T> head_at(const TurnArgs& a, long token, int h)
           static_cast<T*>(a.k_out) + token * a.k_out_ld + static_cast<long>(h) * a.D};
 }
 
-// VEC: rows, heads and halves begin on 16 bytes; else element by element.
-template <class T, bool INTERLEAVED, bool VEC>
+// Vectors of N elements, with which rows, heads and halves begin; N = 1: element
+// by element.
+template <class T, bool INTERLEAVED, int N>
 __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int tokens_per_block) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][rot / 2]: m cos, m sin
   __shared__ unsigned long long turn[kMaxPairs];
@@ -107,7 +118,10 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int to
     for (int idx = threadIdx.x; idx < here * half; idx += kThreads) {
       const int k = idx / half;
       const long token = first + k;
-      const int t = a.positions != nullptr ? a.positions[token % a.n_pos] : static_cast<int>(token % a.T);
+      // (Tokens are at most 2^30.)
+      const unsigned at = static_cast<unsigned>(token);
+      const int t = a.positions != nullptr ? a.positions[at % static_cast<unsigned>(a.n_pos)]
+                                           : static_cast<int>(at % static_cast<unsigned>(a.T));
       const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(t)) * turn[idx - k * half];
       float s, c;
       sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);
@@ -115,13 +129,14 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int to
     }
     __syncthreads();
   };
-  if constexpr (VEC) {
-    constexpr int n = Vec<T>::n;
+  if constexpr (N > 1) {
+    using V = Vec<T, N>;
+    using Raw = typename V::Raw;
     // Items of one head: pieces that turn (halves: two vectors each), then
     // vectors that pass.
-    const int turning = INTERLEAVED ? a.rot / n : half / n, per = turning + (a.D - a.rot) / n;
+    const int turning = INTERLEAVED ? a.rot / N : half / N, per = turning + (a.D - a.rot) / N;
     const int items = here * H * per;
-    uint4 x = {}, y = {};
+    Raw x = {}, y = {};
     T* dst = nullptr;
     int cs_at = 0;  // -1: the vector passes
     auto load = [&](int i) {
@@ -129,12 +144,12 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int to
       const int piece = i % per, th = i / per, k = th / H;
       const Head<T> at = head_at<T>(a, first + k, th - k * H);
       const bool turns = piece < turning;
-      const int from = turns ? piece * n : a.rot + (piece - turning) * n;
+      const int from = turns ? piece * N : a.rot + (piece - turning) * N;
       dst = at.dst + from;
-      cs_at = turns ? k * half + piece * (INTERLEAVED ? n / 2 : n) : -1;
-      x = __ldcs(reinterpret_cast<const uint4*>(at.src + from));
+      cs_at = turns ? k * half + piece * (INTERLEAVED ? N / 2 : N) : -1;
+      x = __ldcs(reinterpret_cast<const Raw*>(at.src + from));
       if constexpr (!INTERLEAVED)
-        if (turns) y = __ldcs(reinterpret_cast<const uint4*>(at.src + half + from));
+        if (turns) y = __ldcs(reinterpret_cast<const Raw*>(at.src + half + from));
     };
     // The first vectors are under way while the table is formed.
     load(threadIdx.x);
@@ -142,40 +157,46 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int to
     for (int i = threadIdx.x; i < items; i += kThreads) {
       T* const to = dst;
       const int at = cs_at;
-      const uint4 px = x, py = y;
+      const Raw px = x, py = y;
       load(i + kThreads);
       if (at < 0) {
-        __stcs(reinterpret_cast<uint4*>(to), px);
+        __stcs(reinterpret_cast<Raw*>(to), px);
         continue;
       }
-      const float4* w = reinterpret_cast<const float4*>(cs + at);
-      float f[n];
-      Vec<T>::get(px, f);
-      if constexpr (INTERLEAVED) {
+      // The table's entries: two at a time where a vector has an even number.
+      constexpr int kPairs = INTERLEAVED ? N / 2 : N;
+      float2 w[kPairs];
+      if constexpr (kPairs % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < n; j += 4) {
-          const float4 t = w[j / 4];
-          const float u0 = f[j], v0 = f[j + 1], u1 = f[j + 2], v1 = f[j + 3];
-          f[j] = u0 * t.x - v0 * t.y;
-          f[j + 1] = v0 * t.x + u0 * t.y;
-          f[j + 2] = u1 * t.z - v1 * t.w;
-          f[j + 3] = v1 * t.z + u1 * t.w;
+        for (int j = 0; j < kPairs; j += 2) {
+          const float4 t = reinterpret_cast<const float4*>(cs + at)[j / 2];
+          w[j] = make_float2(t.x, t.y);
+          w[j + 1] = make_float2(t.z, t.w);
         }
       } else {
-        float g[n];
-        Vec<T>::get(py, g);
-#pragma unroll
-        for (int j = 0; j < n; j += 2) {
-          const float4 t = w[j / 2];
-          const float u0 = f[j], v0 = g[j], u1 = f[j + 1], v1 = g[j + 1];
-          f[j] = u0 * t.x - v0 * t.y;
-          g[j] = v0 * t.x + u0 * t.y;
-          f[j + 1] = u1 * t.z - v1 * t.w;
-          g[j + 1] = v1 * t.z + u1 * t.w;
-        }
-        __stcs(reinterpret_cast<uint4*>(to + half), Vec<T>::put(g));
+        w[0] = cs[at];
       }
-      __stcs(reinterpret_cast<uint4*>(to), Vec<T>::put(f));
+      float f[N];
+      V::get(px, f);
+      if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float u = f[2 * j], v = f[2 * j + 1];
+          f[2 * j] = u * w[j].x - v * w[j].y;
+          f[2 * j + 1] = v * w[j].x + u * w[j].y;
+        }
+      } else {
+        float g[N];
+        V::get(py, g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float u = f[j], v = g[j];
+          f[j] = u * w[j].x - v * w[j].y;
+          g[j] = v * w[j].x + u * w[j].y;
+        }
+        __stcs(reinterpret_cast<Raw*>(to + half), V::put(g));
+      }
+      __stcs(reinterpret_cast<Raw*>(to), V::put(f));
     }
   } else {
     // Items of one head: its pairs, then the components that pass.
@@ -199,16 +220,12 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const TurnArgs a, int to
   }
 }
 
-template <class T, bool INTERLEAVED>
-cudaError_t launch_turn_t(const TurnArgs& a, cudaStream_t st) {
-  const int n = 16 / static_cast<int>(sizeof(T)), half = a.rot / 2;
-  auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  const bool vec = on16(a.q) && on16(a.k) && on16(a.q_out) && on16(a.k_out) && a.q_ld % n == 0 &&
-                   a.k_ld % n == 0 && a.q_out_ld % n == 0 && a.k_out_ld % n == 0 && a.D % n == 0 &&
-                   (INTERLEAVED ? a.rot : half) % n == 0;
+template <class T, bool INTERLEAVED, int N>
+cudaError_t launch_turn_n(const TurnArgs& a, cudaStream_t st) {
+  const int half = a.rot / 2;
   // Tokens of a block: about kRounds items a thread, at most 32 KB of cosines and
   // sines, and no fewer than about 600 blocks as long as there are tokens.
-  const long per_token = static_cast<long>(a.Hq + a.Hkv) * a.D / (INTERLEAVED ? n : 2 * n);
+  const long per_token = static_cast<long>(a.Hq + a.Hkv) * a.D / (INTERLEAVED ? N : 2 * N);
   const long most = 32768 / (static_cast<long>(half) * sizeof(float2));
   long tb = kRounds * kThreads / (per_token > 0 ? per_token : 1);
   if (tb > a.tokens / 608) tb = a.tokens / 608;
@@ -216,11 +233,30 @@ cudaError_t launch_turn_t(const TurnArgs& a, cudaStream_t st) {
   if (tb < 1) tb = 1;
   const long blocks = (a.tokens + tb - 1) / tb;
   const size_t smem = static_cast<size_t>(tb) * half * sizeof(float2);
-  if (vec)
-    turn_kernel<T, INTERLEAVED, true><<<static_cast<unsigned>(blocks), kThreads, smem, st>>>(a, static_cast<int>(tb));
-  else
-    turn_kernel<T, INTERLEAVED, false><<<static_cast<unsigned>(blocks), kThreads, smem, st>>>(a, static_cast<int>(tb));
+  turn_kernel<T, INTERLEAVED, N><<<static_cast<unsigned>(blocks), kThreads, smem, st>>>(a, static_cast<int>(tb));
   return cudaGetLastError();
+}
+
+// The widest vectors that everything begins with: 16 bytes as a rule; 8 or 4 for
+// halves or heads that are no multiples of them (20 fp32 heads of 80 with 20
+// components turned, 16,384 tokens: 64 us a call with 8 bytes, 103 element by element).
+template <class T, bool INTERLEAVED>
+cudaError_t launch_turn_t(const TurnArgs& a, cudaStream_t st) {
+  const long unit = INTERLEAVED ? a.rot : a.rot / 2;
+  auto fits = [&](int n) {
+    const uintptr_t bytes = n * sizeof(T);
+    for (const void* p : {a.q, a.k, static_cast<const void*>(a.q_out), static_cast<const void*>(a.k_out)})
+      if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;
+    for (long v : {a.q_ld, a.k_ld, a.q_out_ld, a.k_out_ld, static_cast<long>(a.D), unit})
+      if (v % n != 0) return false;
+    return true;
+  };
+  constexpr int kMost = 16 / static_cast<int>(sizeof(T));
+  if (fits(kMost)) return launch_turn_n<T, INTERLEAVED, kMost>(a, st);
+  if (fits(kMost / 2)) return launch_turn_n<T, INTERLEAVED, kMost / 2>(a, st);
+  if constexpr (kMost == 8)
+    if (fits(2)) return launch_turn_n<T, INTERLEAVED, 2>(a, st);
+  return launch_turn_n<T, INTERLEAVED, 1>(a, st);
 }
 
 }  // namespace

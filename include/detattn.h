@@ -523,7 +523,8 @@ int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss,
  * target), and dlse, that of lse (NULL: zero), both fp32 [N]:
  *   dz_nv = (dloss_n + dlse_n) exp(z_nv - lse_n) - dloss_n [v = target_n]
  *   dx = dz w  (bf16 [N, d]),  dw = dz^T x  (bf16 [V, d], or fp32 with dw_fp32)
- * dx and dw fully overwritten (dw zeros for N = 0).  lse is the forward's.  The
+ * dx and dw fully overwritten (dw zeros for N = 0); they must not overlap the
+ * inputs.  lse is the forward's.  The
  * logits are computed again, one piece of the vocabulary after another; a
  * piece's dz is in the workspace as bf16 (at most 512 MB, or N rows of 256), and
  * that rounding is in dx and dw, which are otherwise fp32 sums rounded once.  A
@@ -550,7 +551,10 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
  * neither overflows nor vanishes for any finite fp32 update.  An infinity or NaN
  * in a matrix makes its o NaN and leaves the batch's other matrices as they are.
  * batch in [0, 65535], m in [1, 32768], n a multiple of 8 in [8, 32768], batch m n
- * at most 1.7e10, steps in [1, 64], eps >= 1e-30.  16-byte aligned device pointers. */
+ * at most 1.7e10, steps in [1, 64], eps >= 1e-30.  16-byte aligned device pointers;
+ * o, momentum and g must not overlap.  The products are one cooperative launch,
+ * whose blocks wait for one another's tiles (bounded, like all waits): it
+ * starts once all of its blocks fit the GPU at the same time. */
 size_t muon_update_workspace_bytes(int batch, int m, int n);
 int muon_update(const void* g, float* momentum, void* o, void* workspace, size_t workspace_bytes,
                 int batch, int m, int n, int g_fp32, int nesterov, int steps, const float* coeffs,
