@@ -2347,17 +2347,17 @@ int detattn_check_status(void* stream) {
   if (em & 1u)
     return fail(DETATTN_ERR_INDEX,
                 "embed_grad found token ids outside [0, V); those tokens were left out of dw");
-  if (ce & 2u)
-    return fail(DETATTN_ERR_INDEX, "linear_ce found targets >= V; those rows were taken as rows without a target");
   if (b & 16u)
     return fail(DETATTN_ERR_WORKSPACE,
                 "the dQ step found its tile counter not cleared: run attn_bwd_delta on this "
                 "workspace (with the same workspace_bytes) first");
-  if (f | b | ly | wg | nm | ce | mu)
+  if (f | b | ly | wg | nm | (ce & 1u) | mu)
     return fail(DETATTN_ERR_DEVICE_TIMEOUT,
                 "a kernel gave up on a pipeline wait (fwd flags %u, bwd flags %u, layer flags %u, "
                 "act8_wgrad %u, block_norm_bwd %u, linear_ce %u, muon_update %u)",
-                f, b, ly, wg, nm, ce, mu);
+                f, b, ly, wg, nm, ce & 1u, mu);
+  if (ce & 2u)
+    return fail(DETATTN_ERR_INDEX, "linear_ce found targets >= V; those rows were taken as rows without a target");
   return ok_status();
 }
 

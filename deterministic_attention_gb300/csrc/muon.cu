@@ -206,16 +206,16 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
 //
 // Against a launch for each product this fills rounds (4096 x 6144 has 136, 136 and
 // 384 tiles a step for 76 teams) and starts a tile as soon as its own inputs are
-// there: 12 x 768 x 1280 takes 226 us and did 331, 4096 x 6144 1,190 and 1,258, 768 x
-// 768 109 and 115.  A tile is ready 3 to 4 us after its last product (the queue of
+// there: 12 x 768 x 1280 took 226 us and did 331 (214 now, with less double arithmetic
+// before it), 4096 x 6144 1,190 and 1,258, 768 x 768 109 and 115.  A tile is ready 3 to 4 us after its last product (the queue of
 // products 0.3 to 1.3, its stores 1 to 3, the fence before the count 0.7) and seen
 // 1.2 us later: with at most a dozen matrices that chain, not the rate of the
 // products, is the time.  Measured and not kept: a warp that looks at the counts ahead
 // of the producer (768 x 768: 122 us); all tiles of a symmetric result computed
-// where the teams are idle anyway (768 x 768: 109.4 us against 110.4); two groups of matrices by turns (12 x 768 x 1280:
-// 250 us); the tiles above the diagonal written too (258 us); how an operand lies in
-// memory chosen step by step and not in runs (the issue of a product then takes
-// longer than the product: 258 us).
+// where the teams are idle anyway (768 x 768: 109.4 us against 110.4); two groups of
+// matrices by turns (12 x 768 x 1280: 250 us); the tiles above the diagonal written
+// too (308 us); how an operand lies in memory chosen step by step and not in runs
+// (258 us: the issue of a product then takes longer than the product).
 enum : int { kGram = 0, kPoly = 1, kNext = 2 };
 
 struct MuonUnit {

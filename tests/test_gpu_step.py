@@ -489,6 +489,80 @@ def test_muon_update_outputs_and_workspace():
     assert da.muon_update(g[:0]).shape == (0, 130, 64)
 
 
+# ------------------------------------------------------------ alignment and large offsets
+def test_outputs_and_workspaces_on_16_bytes():
+    """Rows are stored 32 bytes at a time where outputs begin so, and workspaces
+    begin anywhere on 16 bytes."""
+    def shifted(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 64,), 7.0, dtype=dtype, device="cuda")
+        start = 16 // buf.element_size()
+        return buf, buf[start:start + n].view(shape)
+
+    def workspace(n):
+        return torch.full((n + 16,), 255, dtype=torch.uint8, device="cuda")[16:]
+    x, w, t = (a.cuda() for a in _ce_inputs(300, 64, 777, seed=41))
+    loss, lse = da.linear_ce_fwd(x, w, t, workspace=workspace(da.linear_ce_fwd_workspace_bytes(300, 777, 64)))
+    g = torch.full((300,), 0.01, device="cuda")
+    want = da.linear_ce_bwd(x, w, t, lse, g)
+    bufs, outs = zip(*(shifted(s, BF) for s in ((300, 64), (777, 64))))
+    da.linear_ce_bwd(x, w, t, lse, g, dx=outs[0], dw=outs[1],
+                     workspace=workspace(da.linear_ce_bwd_workspace_bytes(300, 777, 64)))
+    m = _muon_grad((3, 160, 320), 42, BF).cuda()
+    bo, o = shifted((3, 160, 320), BF)
+    da.muon_update(m, out=o, workspace=workspace(da.muon_update_workspace_bytes(3, 160, 320)))
+    _done()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert torch.equal(o, da.muon_update(m))
+    for b, v in zip((*bufs, bo), (*outs, o)):
+        assert (b[:8] == 7).all() and (b[8 + v.numel():] == 7).all()
+
+
+def test_rope_past_2_31_elements():
+    T = 440000
+    q = torch.empty((1, T, 40, 128), dtype=BF, device="cuda")
+    q[0, -3:] = torch.randn((3, 40, 128), generator=_gen(43)).to(BF).cuda()
+    f, _ = da.rope_freqs(128)
+    y, _ = da.rope_fwd(q, None, f, q_out=q)
+    last = _f(q[0, -3:].clone())
+    x = torch.randn((3, 40, 128), generator=_gen(43)).to(BF)
+    _done()
+    want = os_.rope(_f(x), np.arange(T - 3, T), _f(f))
+    assert (np.abs(last - want) <= _rope_tol(_f(x), want, 1.0, BF)).all()
+
+
+def test_linear_ce_past_2_31_elements():
+    N, d, V = 1400100, 1536, 300
+    x = torch.zeros((N, d), dtype=BF, device="cuda")
+    tail, w, t = (a.cuda() for a in _ce_inputs(500, d, V, seed=44))
+    x[-500:] = tail
+    targets = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    targets[-500:] = t
+    g = torch.full((N,), 1.0 / 256, device="cuda")
+    loss, lse = da.linear_ce_fwd(x, w, targets)
+    dx, dw = da.linear_ce_bwd(x, w, targets, lse, g)
+    _done()
+    ref_loss, ref_lse = da.linear_ce_fwd(tail, w, t)
+    ref_dx, ref_dw = da.linear_ce_bwd(tail, w, t, ref_lse, g[:500])
+    assert float((loss[-500:] - ref_loss).abs().max()) <= 1e-5 and not loss[:-500].any()
+    assert float((lse[:-500] - float(np.log(V))).abs().max()) <= 1e-5
+    for a, b in ((dx[-500:], ref_dx), (dw, ref_dw)):
+        assert float((a.double() - b.double()).norm() / b.double().norm()) <= 2.0 ** -8
+    assert not dx[:-500].any()
+
+
+def test_muon_update_past_2_31_elements():
+    batch, n = 520, 2048
+    g = torch.zeros((batch, n, n), dtype=BF, device="cuda")
+    g[-1] = _muon_grad((n, n), 45, BF).cuda()
+    o = da.muon_update(g)
+    want = da.muon_update(g[-1:].clone())
+    _done()
+    assert not o[:-1].any()
+    # (The tiles of one matrix alone may be other ones: equal but for the roundings' order.)
+    assert float((o[-1].double() - want[0].double()).norm() / want[0].double().norm()) <= 2.0 ** -8
+
+
 # ------------------------------------------------------------ together
 def _step(s):
     """One training step of a model of one attention layer with these ends."""
