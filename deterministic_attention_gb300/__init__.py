@@ -844,28 +844,33 @@ def _rope(call, where, q, k, freqs, positions, interleaved, mscale, q_out, k_out
     dev = _current(q, "q")
     N, T, Hq, D, q_ld = _heads(q, "q", dev)
     qo, qo_ld = _heads_out(q_out, "q_out", q, N, T, Hq, D, dev)
-    ko, Hkv, k_ld, ko_ld = None, 0, 0, 0
+    ka = koa = ko = None
+    Hkv = k_ld = ko_ld = 0
     if k is not None:
         Nk, Tk, Hkv, Dk, k_ld = _heads(k, "k", dev, q.dtype)
         if Nk != N or Tk != T or Dk != D:
             raise ValueError(f"k is {tuple(k.shape)}, q {tuple(q.shape)}")
         ko, ko_ld = _heads_out(k_out, "k_out", k, N, T, Hkv, D, dev)
+        ka, koa = k.data_ptr(), ko.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise TypeError("freqs must be a float64 tensor [rot / 2]")
-    half = freqs.shape[0]
-    _on_device(freqs, "freqs", torch.float64, (half,), dev)
+    half = freqs.numel()
+    if freqs.dtype is not torch.float64 or freqs.get_device() != dev or not freqs.is_contiguous():
+        _on_device(freqs, "freqs", torch.float64, (half,), dev)
     n_pos, at = 0, None
     if positions is not None:
-        _on_device(positions, "positions", torch.int32, positions.shape, dev)
+        if (not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32
+                or positions.get_device() != dev or not positions.is_contiguous()):
+            _on_device(positions, "positions", torch.int32, getattr(positions, "shape", ()), dev)
         n_pos, at = positions.numel(), positions.data_ptr()
         if positions.dim() < 1 or positions.shape[-1] != T or (n_pos != N and n_pos != T):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(T,)} or {tuple(q.shape[:-2])}")
     if N:
-        _check(call(q.data_ptr(), _addr(k), qo.data_ptr(), _addr(ko), freqs.data_ptr(), at, n_pos, q_ld, k_ld,
-                    qo_ld, ko_ld, N, T, Hq, Hkv, D, 2 * half, bool(interleaved), q.dtype is torch.float32,
-                    mscale, _stream()), where)
+        _check(call(q.data_ptr(), ka, qo.data_ptr(), koa, freqs.data_ptr(), at, n_pos, q_ld, k_ld, qo_ld, ko_ld,
+                    N, T, Hq, Hkv, D, 2 * half, bool(interleaved), q.dtype is torch.float32, mscale, _stream()),
+               where)
     return qo, ko
 
 

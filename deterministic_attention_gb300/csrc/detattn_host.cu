@@ -1389,10 +1389,11 @@ CeFwdLayout ce_fwd_layout(int N, int V) {
   l.total = l.z + up256(static_cast<size_t>(N) * sizeof(float));
   return l;
 }
-// The vocabulary in pieces whose dz takes at most 512 MB (or one tile's width):
-// all of it where that is enough, else pieces of nearly one size.  Their width is fixed
-// by the shape.
-constexpr double kCePieceBytes = 536870912.0;
+// The vocabulary in pieces whose dz takes at most 1 GiB (or one tile's width): all
+// of it where that is enough, else pieces of nearly one size.  Their width is fixed
+// by the shape.  (32,768 rows, d = 1536, V = 50,432: pieces of 256 MiB 9.49 ms, 512 MiB
+// 9.14, 1 GiB 8.92, 2 GiB 8.88.)
+constexpr double kCePieceBytes = 1073741824.0;
 int ce_piece_width(int N, int V) {
   const long tiles = (V + kCeTile - 1) / kCeTile;
   long most = static_cast<long>(kCePieceBytes / (2.0 * kCeTile * N));

@@ -20,9 +20,9 @@
 // 3.4e-3).
 //
 // Measured (device): 32,768 rows, d = 1536, V = 50,432: forward 2.5 ms (2.0 PFLOP/s, at
-// and above the measured bf16 peak), backward 9.4 ms (1.63 PFLOP/s, under the power
-// limit; 8.7 at best): a piece of 7,424 words takes 0.41 (dz), 0.41 to 0.45 (dx) and 0.39
-// ms (dw), 0.394 at the peak.  1,187 rows, d = 768: backward 176 us, the tensor pipe
+// and above the measured bf16 peak), backward 8.9 ms (1.71 PFLOP/s, under the power
+// limit; 7.7 at best): a piece of 25,344 words takes 1.31 (dz), 1.30 (dx) and 1.31 ms
+// (dw), 1.35 at the measured peak.  1,187 rows, d = 768: backward 176 us, the tensor pipe
 // busy 81 to 84 % of the time; forward of 128 rows 21.4 us, 13 of them the weights'
 // 77 MB at 6 TB/s.  What mattered: tiles in bands (dx and dz had read dz and x from
 // DRAM once per column tile: 573 -> 407 and 484 -> 408 us), 32-byte stores, a

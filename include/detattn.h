@@ -526,7 +526,7 @@ int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss,
  * dx and dw fully overwritten (dw zeros for N = 0); they must not overlap the
  * inputs.  lse is the forward's.  The
  * logits are computed again, one piece of the vocabulary after another; a
- * piece's dz is in the workspace as bf16 (at most 512 MB, or N rows of 256), and
+ * piece's dz is in the workspace as bf16 (at most 1 GiB, or N rows of 256), and
  * that rounding is in dx and dw, which are otherwise fp32 sums rounded once.  A
  * row without a gradient has dz = 0 whatever its logits are; its x must still be
  * finite, since dw holds 0 x. */

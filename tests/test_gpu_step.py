@@ -223,8 +223,8 @@ def test_linear_ce_large_logits_and_sure_rows():
 
 
 def test_linear_ce_over_several_pieces():
-    """More than 512 MB of dz: two pieces, the last narrower; and a padded vocabulary."""
-    N, d, V = 4200, 40, 66001
+    """More than 1 GiB of dz: two pieces, the last narrower; and a padded vocabulary."""
+    N, d, V = 4200, 40, 132001
     x, w, t = _ce_inputs(N, d, V, seed=6, std=0.2)
     g = torch.full((N,), 1.0 / N)
     dev = [a.cuda() for a in (x, w, t, g)]

@@ -98,11 +98,11 @@ def test_linear_ce_sizes(L):
     assert L.linear_ce_fwd_workspace_bytes(300, 1000, 64) == (parts + 255) // 256 * 256 + 1280
     assert L.linear_ce_fwd_workspace_bytes(0, 1000, 64) == 0
     assert L.linear_ce_bwd_workspace_bytes(300, 1000, 63) == 0
-    # A piece of dz is at most 512 MB, whatever the vocabulary; beyond it come the
+    # A piece of dz is at most 1 GiB, whatever the vocabulary; beyond it come the
     # fp32 sums of dx and partial tiles.
     for N, V in ((4096, 50432), (32768, 50432), (16384, 1 << 20)):
         extra = N * 64 * 4 + 76 * 32 * 256 * 256 * 4
-        assert L.linear_ce_bwd_workspace_bytes(N, V, 64) <= (512 << 20) + extra + 4096
+        assert L.linear_ce_bwd_workspace_bytes(N, V, 64) <= (1 << 30) + extra + 4096
     if not torch.cuda.is_available():
         assert L.linear_ce_bwd(*dict(CEB, e=None).values(), None) == -6
         assert L.linear_ce_fwd(*CE.values(), None) == -6
