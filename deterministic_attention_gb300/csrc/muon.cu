@@ -215,7 +215,10 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
 // where the teams are idle anyway (768 x 768: 109.4 us against 110.4); two groups of
 // matrices by turns (12 x 768 x 1280: 250 us); the tiles above the diagonal written
 // too (308 us); how an operand lies in memory chosen step by step and not in runs
-// (258 us: the issue of a product then takes longer than the product).
+// (258 us: the issue of a product then takes longer than the product); sixteen
+// epilogue warps (107.8, 219 and 1,174 us where eight took 109.6, 215 and 1,179); one
+// count per block and tile in the place of its warps' (106.7, 217 and 1,200 against
+// 109.4, 216 and 1,200).
 enum : int { kGram = 0, kPoly = 1, kNext = 2 };
 
 struct MuonUnit {

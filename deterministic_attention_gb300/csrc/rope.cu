@@ -15,9 +15,9 @@
 // few tokens, forms their cosines and sines once in shared memory for all heads
 // of q and k while its first vectors are under way, and then moves 16-byte
 // vectors, the next loaded before the last is stored.  32 + 8 heads of 128 over
-// 65,536 positions: 200 us, 6.7 TB/s, 99 % of the copy rate.  (Before that order of
-// loads 209 us; two vectors a thread at once 232, four 261: fewer blocks fit an
-// SM; one round of vectors a block 239; the table before the first load 363.)
+// 65,536 positions: 196 us, 6.8 TB/s, the copy rate.  (Four rounds of vectors a
+// block 200 us, two 231; without that order of loads 209; two vectors a thread at
+// once 232, four 261: fewer blocks fit an SM; the table before the first load 363.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256, kMaxPairs = 512;
 // Items of a thread in a block, about.
-constexpr int kRounds = 4;
+constexpr int kRounds = 8;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }

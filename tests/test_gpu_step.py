@@ -123,6 +123,23 @@ def test_rope_in_place_and_parts(dtype, D, rot):
     assert (out[:, :, 5:8] - before[:, :, 1:4]).abs().max() <= (0.05 if dtype is BF else 1e-5)
 
 
+@pytest.mark.parametrize("dtype,offset", [(BF, 1), (BF, 2), (BF, 4), (F32, 1), (F32, 2)])
+def test_rope_from_any_element(dtype, offset):
+    """Tensors that begin on any element: narrower vectors, the same numbers, nothing around them."""
+    f, _ = da.rope_freqs(32)
+    n = 2 * 30 * 3 * 64
+    q = torch.randn((2, 30, 3, 64), generator=_gen(50)).to(dtype).cuda()
+    src, dst = (torch.full((n + 16,), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+    src[offset:offset + n] = q.view(-1)
+    for inter in (False, True):
+        want, _ = da.rope_fwd(q, None, f, interleaved=inter)
+        got, _ = da.rope_fwd(src[offset:offset + n].view(q.shape), None, f, interleaved=inter,
+                             q_out=dst[offset:offset + n].view(q.shape))
+        _done()
+        assert torch.equal(got, want)
+        assert (dst[:offset] == 7).all() and (dst[offset + n:] == 7).all()
+
+
 def test_rope_bwd_is_the_gradient():
     f, m = da.rope_freqs(64, scaling="ramp", factor=4.0, context=64)
     q, dq = (torch.randn((1, 20, 2, 64), generator=_gen(s)).cuda() for s in (5, 6))
