@@ -59,7 +59,7 @@ struct StatsEpi {
   }
   __device__ __forceinline__ void take(uint32_t taddr) {
     const Args& a = *args;
-    float m = -INFINITY, s = 0.0f;
+    float m = -INFINITY, s = 0.0f, held = 0.0f;  // s is held over 2^held
     each32<kCols>(taddr, [&](int c, uint32_t (&v)[32]) {
       const int c0 = col + c;
       // Columns past the vocabulary, in its last tile.
@@ -71,7 +71,8 @@ struct StatsEpi {
       float top = m;
 #pragma unroll
       for (int i = 0; i < 32; i += 2) top = fmax3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-      const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+      // (Rounded by itself: base - held is 0, and s stays, where the largest does.)
+      const float base = top == -INFINITY ? 0.0f : __fmul_rn(top, kLog2e);
       const uint64_t nb = f2_make(-base, -base), l2 = f2_make(kLog2e, kLog2e);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -82,8 +83,9 @@ struct StatsEpi {
       }
       float s0, s1;
       f2_split(f2_add(sum[0], sum[1]), s0, s1);
-      s = s * ex2_approx(m == -INFINITY ? -INFINITY : m * kLog2e - base) + (s0 + s1);
+      s = s * ex2_approx(m == -INFINITY ? -INFINITY : held - base) + (s0 + s1);
       m = top;
+      held = base;
       const unsigned at = static_cast<unsigned>(target - c0);
       if (at < 32u && target < a.V) {
         float z = 0.0f;
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ce_finish_kernel(const CeFi
     float s = all.s * exp2f((all.m - base) * kLog2e);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float r = x[k].x == -INFINITY ? 0.0f : fmaf(x[k].x, kLog2e, -(x[k].x * kLog2e));
+      const float r = x[k].x == -INFINITY ? 0.0f : fmaf(x[k].x, kLog2e, -__fmul_rn(x[k].x, kLog2e));
       s += x[k].y * exp2f((x[k].x - base) * kLog2e - r);
     }
     all.m = m;
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ce_finish_kernel(const CeFi
 #pragma unroll
   for (int i = 0; i < kFinishWarps; ++i) all.s += sh[i][lane].y * exp2f((sh[i][lane].x - base) * kLog2e);
   if (blockIdx.x * kFinishRows + lane >= static_cast<unsigned>(a.N)) return;
-  const float ln = logf(all.s);
+  // The largest logit's own exponential is 1: what is below is rounding.
+  const float ln = logf(all.s < 1.0f ? 1.0f : all.s);
   a.lse[row] = all.m + ln;
   a.loss[row] = t >= 0 && t < a.V ? (all.m - a.z_target[row]) + ln : 0.0f;
 }

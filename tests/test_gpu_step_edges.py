@@ -1,0 +1,70 @@
+"""The ends of a training step on the GPU where they can go wrong.
+
+Tolerances are those of test_gpu_step.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import deterministic_attention_gb300 as da
+from test_gpu_step import BF, _done, _f
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ cross entropy: loss
+def _exact_logits(z):
+    """Inputs whose logits are the columns' bf16 numbers exactly: every row of x has a
+    single 1.  z [V, N] -> (x, w, z as they are)."""
+    w = torch.tensor(z).to(BF)
+    return torch.eye(z.shape[1]).to(BF), w, w.double().numpy().T
+
+
+def _loss_of(z, t):
+    """ln(1 + sum over the other words of exp(z - z_target)), which does not cancel."""
+    d = z - z[np.arange(len(t)), t][:, None]
+    d[np.arange(len(t)), t] = -np.inf
+    return np.logaddexp(0.0, np.logaddexp.reduce(d, axis=1))
+
+
+def _loss_check(z, t, tol):
+    x, w, z = _exact_logits(z)
+    loss, lse = da.linear_ce_fwd(x.cuda(), w.cuda(), torch.tensor(t, dtype=torch.int32).cuda())
+    _done()
+    want = _loss_of(z, t)
+    assert (_f(loss) >= 0).all(), _f(loss).min()
+    assert np.abs(_f(loss) - want).max() <= tol
+    at = z[np.arange(len(t)), t]
+    assert (np.abs(_f(lse) - (at + want)) <= tol + 2.0 ** -23 * np.abs(at + want)).all()
+
+
+@pytest.mark.parametrize("lo,hi", [(1.0, 20.0), (40.0, 60.0), (100.0, 400.0), (-300.0, -50.0)])
+def test_loss_of_sure_rows(lo, hi):
+    """One logit far above the rest, in every group of 32 words of a part of 128.  The
+    sum is its own exponential, 1 (2^-22 off), and a correction of the exponents' base
+    (an exponential 2^-22 off, two products): 2^-22 + 2^-22 + 2^-23, and ln of a number
+    next to 1 adds nothing: 6e-7."""
+    rng = np.random.default_rng(0)
+    N, V = 512, 700
+    z = rng.uniform(-1.0, 1.0, size=(V, N))
+    top = rng.uniform(lo, hi, size=N)
+    t = np.array([0, 31, 32, 63, 64, 96, 127, 128, 300, 640, 699])[np.arange(N) % 11]
+    z += (top - 41.0)[None]
+    z[t, np.arange(N)] = top
+    _loss_check(z, t, 1e-6)
+
+
+def test_loss_of_rows_with_several_large_logits():
+    """Equal largest logits in several groups, and largest logits that grow from group to
+    group: each group scales the sum once more (2^-22 each, and as much for the
+    correction, the exponentials and the logarithm's unit of a loss below 2)."""
+    rng = np.random.default_rng(1)
+    N, V = 512, 384
+    top = rng.uniform(16.0, 31.0, size=N)
+    z = np.broadcast_to(top - 40.0, (V, N)).copy()
+    for i in range(N):
+        k = i % 4
+        if i < 256:
+            z[[5 + 32 * j for j in range(k + 1)], i] = top[i]
+        else:
+            z[[5, 40, 70, 100], i] = top[i] + np.array([[0, .25, .5, 1], [1, 0, 1, 0], [0, 0, 0, 1], [0, 1, 1, 1]][k])
+    _loss_check(z, np.full(N, 5), 8 * 2.0 ** -22)
