@@ -2220,7 +2220,7 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
   CUtensorMap mx, mxk;
   if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, nd, "x")) != DETATTN_OK) return rc;
   if ((rc = encode_k_rows(&mxk, x, d, N, 1, d, nd, "x")) != DETATTN_OK) return rc;
-  if ((rc = launched(launch_ce_unit(targets, dloss, unit, N, V, st), "linear_ce_bwd (unit)")) != DETATTN_OK)
+  if ((rc = launched(launch_ce_unit(targets, dloss, dlse, unit, N, V, st), "linear_ce_bwd (unit)")) != DETATTN_OK)
     return rc;
   for (int v0 = 0; v0 < V; v0 += l.width) {
     const int width = std::min(l.width, V - v0);

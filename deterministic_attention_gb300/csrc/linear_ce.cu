@@ -14,7 +14,7 @@
 // the tensor core's second products need, is the one rounding between the
 // inputs and the results (half a step is 2^-8 of a dz at most); the sums over the
 // vocabulary and over the tokens are in fp32.  dz is held over the largest
-// |dloss|: where all rows weigh the same, as with a mean, a target's dz is then
+// |dloss| (ce_unit_kernel): where all rows weigh the same, as with a mean, a target's dz is then
 // next to -1, which is a bf16 number, and not next to -dloss, whose rounding
 // would be the same in every row and so in dx and dw as a whole (dloss = 1/240:
 // 3.4e-3).
@@ -162,24 +162,55 @@ __global__ void __launch_bounds__(kFinishWarps * 32) ce_finish_kernel(const CeFi
 }
 
 // ------------------------------------------------------------ backward: dz of a piece
+// The unit of dz: the largest |dloss| of the rows that have a target (1 where that is
+// zero or not finite).  Where a row's gradient over it would near an end of fp32's
+// range, above 2^32 (sums over 2^24 rows and words still fit) or below 2^-100 (times
+// the smaller exponentials), its mantissa alone: bf16 holds what fp32 does, so dz then
+// neither overflows nor vanishes before dx and dw do.
 __global__ void __launch_bounds__(1024) ce_unit_kernel(const int* __restrict__ targets,
                                                        const float* __restrict__ dloss,
-                                                       float* __restrict__ unit, int N, int V) {
-  __shared__ float sh[32];
+                                                       const float* __restrict__ dlse, float* __restrict__ unit,
+                                                       int N, int V) {
+  __shared__ float sh[3][32];
   griddep_launch_dependents();
-  float m = 0.0f;
+  float m = 0.0f, most = 0.0f, least = INFINITY;  // of |dloss|; of a row's dloss and dloss + dlse
+  auto row = [&](float x) {
+    x = fabsf(x);
+    if (x < INFINITY) most = fmaxf(most, x);  // (a row that is not finite is by itself)
+    if (x > 0.0f) least = fminf(least, x);
+  };
 #pragma unroll 4
   for (int i = threadIdx.x; i < N; i += 1024) {
     const int t = targets[i];
-    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
+    const float g = t >= 0 && t < V ? dloss[i] : 0.0f;
+    m = fmaxf(m, fabsf(g));
+    row(g);
+    if (dlse != nullptr) row(g + dlse[i]);
   }
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  auto warp = [&]() {
+    for (int o = 16; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+    }
+  };
+  warp();
+  if ((threadIdx.x & 31) == 0) {
+    sh[0][threadIdx.x >> 5] = m;
+    sh[1][threadIdx.x >> 5] = most;
+    sh[2][threadIdx.x >> 5] = least;
+  }
   __syncthreads();
   if (threadIdx.x >= 32) return;
-  m = sh[threadIdx.x];
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if (threadIdx.x == 0) *unit = m > 0.0f && m < INFINITY ? m : 1.0f;
+  m = sh[0][threadIdx.x];
+  most = sh[1][threadIdx.x];
+  least = sh[2][threadIdx.x];
+  warp();
+  if (threadIdx.x == 0) {
+    const bool near = most <= m * 0x1p32f && least >= m * 0x1p-100f;
+    int e;
+    *unit = !(m > 0.0f && m < INFINITY) ? 1.0f : near ? m : 2.0f * frexpf(m, &e);
+  }
 }
 
 struct GradEpi {
@@ -408,9 +439,9 @@ cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st) {
                           kFinishWarps * 32, st, true, a);
 }
 
-cudaError_t launch_ce_unit(const int* targets, const float* dloss, float* unit, int N, int V,
-                           cudaStream_t st) {
-  return launch_dependent(ce_unit_kernel, dim3(1), 1024, st, false, targets, dloss, unit, N, V);
+cudaError_t launch_ce_unit(const int* targets, const float* dloss, const float* dlse, float* unit, int N,
+                           int V, cudaStream_t st) {
+  return launch_dependent(ce_unit_kernel, dim3(1), 1024, st, false, targets, dloss, dlse, unit, N, V);
 }
 
 cudaError_t launch_ce_dz(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,

@@ -93,10 +93,9 @@ constexpr int kCeTile = 256;
 cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
                             const CeStatsArgs& a, cudaStream_t st);
 cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st);
-// *unit = the largest |dloss| of the rows that have a target (1 where that is
-// zero or not finite).
-cudaError_t launch_ce_unit(const int* targets, const float* dloss, float* unit, int N, int V,
-                           cudaStream_t st);
+// *unit = the largest |dloss| of the rows that have a target, as a rule (ce_unit_kernel).
+cudaError_t launch_ce_unit(const int* targets, const float* dloss, const float* dlse, float* unit, int N,
+                           int V, cudaStream_t st);
 cudaError_t launch_ce_dz(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
                          const CeGradArgs& a, cudaStream_t st);
 // mdz: dz as rows of K; mw: w with K along its rows.

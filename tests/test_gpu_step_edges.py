@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import deterministic_attention_gb300 as da
-from test_gpu_step import BF, _done, _f
+from test_gpu_step import BF, _ce_check, _ce_inputs, _done, _f, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,13 @@ def test_loss_of_rows_with_several_large_logits():
         else:
             z[[5, 40, 70, 100], i] = top[i] + np.array([[0, .25, .5, 1], [1, 0, 1, 0], [0, 0, 0, 1], [0, 1, 1, 1]][k])
     _loss_check(z, np.full(N, 5), 8 * 2.0 ** -22)
+
+
+# ------------------------------------------------------------ cross entropy: gradients
+@pytest.mark.parametrize("dloss,dlse", [(1e-38, 10.0), (1e-42, 1e-2), (1e-30, 1e15), (0.0, 1e3), (1e30, 1e-20)])
+def test_linear_ce_gradients_of_very_different_size(dloss, dlse):
+    """dlse / dloss past fp32's range, or next to it."""
+    x, w, t = _ce_inputs(200, 64, 300, seed=3)
+    g = _gen(4)
+    _ce_check(x, w, t, dloss * torch.rand((200,), generator=g), dlse=dlse * (0.1 + torch.rand((200,), generator=g)),
+              dw_fp32=True)
