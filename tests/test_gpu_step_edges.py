@@ -78,3 +78,34 @@ def test_linear_ce_gradients_of_very_different_size(dloss, dlse):
     g = _gen(4)
     _ce_check(x, w, t, dloss * torch.rand((200,), generator=g), dlse=dlse * (0.1 + torch.rand((200,), generator=g)),
               dw_fp32=True)
+
+
+@pytest.mark.parametrize("N,d,V", [(4096, 16, 400001), (1400100, 8, 1000)])
+def test_linear_ce_over_more_than_two_pieces(N, d, V):
+    """A middle piece's share of dx is added to the sum and kept: four pieces whose tiles of
+    dx are all cut along the words, and four of 256 words whose tiles are whole."""
+    x, w, t, g = (a.cuda() for a in (*_ce_inputs(N, d, V, seed=6, std=0.2), torch.full((N,), 1.0 / N)))
+    _, lse = da.linear_ce_fwd(x, w, t)
+    dx, dw = da.linear_ce_bwd(x, w, t, lse, g, dw_fp32=True)
+    _done()
+    X, W, rows = x.double(), w.double(), max(1, (1 << 28) // V)
+    ew = torch.zeros_like(W)
+    num = den = worst = worst_lse = 0.0
+    for r in range(0, N, rows):
+        z = X[r:r + rows] @ W.t()
+        top = torch.logsumexp(z, dim=1)
+        worst_lse = max(worst_lse, float((lse[r:r + rows] - top).abs().max()))
+        p = z.sub_(top[:, None]).exp_().div_(N)
+        tr = t[r:r + rows].long()
+        p[tr < 0] = 0
+        has = (tr >= 0).nonzero()[:, 0]
+        p[has, tr[has]] -= 1.0 / N
+        ex = p @ W
+        ew += p.t() @ X[r:r + rows]
+        num += float((dx[r:r + rows] - ex).square().sum())
+        den += float(ex.square().sum())
+        rms = float(ex.square().mean().sqrt())
+        worst = max(worst, float(((dx[r:r + rows] - ex).abs() / ex.abs().clamp(min=rms)).max()))
+    assert worst_lse <= 1e-5
+    assert (num / den) ** 0.5 <= 2.0 ** -8 and worst <= 2.0 ** -5
+    assert float((dw - ew).norm() / ew.norm()) <= 2.0 ** -8
