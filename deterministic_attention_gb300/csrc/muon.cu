@@ -10,7 +10,7 @@
 //
 // A and P are symmetric: their tiles on and below the diagonal are computed, and
 // what lies above is read as the transpose of what lies below.  Between the products the matrices are fp16, scaled by powers
-// of two (kMuonX, kMuonP): the singular values stay below about 1.2, so fp16's
+// of two (kMuonX, kMuonA, kMuonP): the singular values stay below about 1.2, so fp16's
 // eleven bits cost a step 2^-12 of a value where bf16 costs 2^-9, at the same
 // rate; five steps leave 1.2e-3 of the result's norm (768 x 768 of normal
 // numbers; bf16 9.8e-3).  Sums are fp32 throughout, the norm's in double.
@@ -364,10 +364,10 @@ struct MuonTile {
     ld = kind == kNext ? a.n : a.ld;
     at = (static_cast<size_t>(w.batch) * rows + row) * ld + col;
     const float* k = a.coeffs[w.step];
-    alpha = kind == kGram ? 1.0f / kMuonX : kind == kPoly ? k[2] * (kMuonP / (kMuonX * kMuonX))
+    alpha = kind == kGram ? kMuonA / (kMuonX * kMuonX) : kind == kPoly ? k[2] * (kMuonP / (kMuonA * kMuonA))
             : last        ? 1.0f / (kMuonX * kMuonP)
                           : 1.0f / kMuonP;
-    beta = k[1] * (kMuonP / kMuonX);
+    beta = k[1] * (kMuonP / kMuonA);
     diag = k[0] * kMuonP;
   }
   // What is added to A A: from L2, where other blocks' stores are.

@@ -120,9 +120,11 @@ struct MuonInArgs {
   bool g_fp32, nesterov;
   float beta, eps;
 };
-// Scales of the stored fp16 matrices: X and X X^T hold values up to about 1.2
-// (16 fit), the polynomial up to about 3 (64 fit).
-constexpr float kMuonX = 4096.0f, kMuonP = 1024.0f;
+// Scales of the stored fp16 matrices (65,504 is the largest): singular values of X are
+// about 1.2 at most, and 15.9 fit; X X^T holds their squares, so 128 is the most that fits
+// where X does (its entries below 2^-21 have fewer bits, off by 2^-32 at most, next to
+// the a of P); the polynomial is about 3, and 63.9 fit.
+constexpr float kMuonX = 4096.0f, kMuonA = 128.0f, kMuonP = 1024.0f;
 int muon_sum_blocks(int batch, long count);
 cudaError_t launch_muon_momentum(const MuonInArgs& a, cudaStream_t st);
 cudaError_t launch_muon_scale(const MuonInArgs& a, cudaStream_t st);

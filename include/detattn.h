@@ -542,9 +542,9 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
  *   `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X
  * o = X as bf16 [batch, m, n].  coeffs: HOST floats [steps][3] (a, b, c), NULL:
  * 3.4445, -4.7750, 2.0315 in every step.  Between the products X, X X^T and the
- * polynomial are fp16, scaled by powers of two, so singular values must stay
- * below 16 and the polynomial's values below 64 (with the coefficients above
- * they stay below 1.3 and 3.5); beyond, results are infinite or NaN.  o is within about
+ * polynomial are fp16, scaled by powers of two: singular values up to 15.9 and
+ * values of the polynomial up to 63.9 fit (with the coefficients above they stay
+ * below 1.3 and 3.5); beyond, results are infinite or NaN.  o is within about
  * 2e-3 of its norm of the formula (of which rounding it to bf16 is 1.7e-3) for
  * matrices of normal numbers; directions whose singular value is below 2^-11 of
  * the largest are only known to that.  Squares are summed in ranges, so the norm

@@ -66,7 +66,7 @@ def muon(g, momentum=None, beta=0.95, nesterov=True, steps=5, coeffs=None, eps=1
         x = x.T
     for k in range(steps):
         a, b, c = NS if coeffs is None else coeffs[k]
-        gram = rounding(x @ x.T, 4096.0)
+        gram = rounding(x @ x.T, 128.0)
         p = rounding(a * np.eye(len(x)) + b * gram + c * (gram @ gram), 1024.0)
         x = p @ x
         if k < steps - 1:

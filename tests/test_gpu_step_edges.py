@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import deterministic_attention_gb300 as da
-from test_gpu_step import BF, _ce_check, _ce_inputs, _done, _f, _gen
+from oracle import step as os_
+from test_gpu_step import BF, F32, _ce_check, _ce_inputs, _done, _f, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +110,32 @@ def test_linear_ce_over_more_than_two_pieces(N, d, V):
     assert worst_lse <= 1e-5
     assert (num / den) ** 0.5 <= 2.0 ** -8 and worst <= 2.0 ** -5
     assert float((dw - ew).norm() / ew.norm()) <= 2.0 ** -8
+
+
+# ------------------------------------------------------------ orthogonalised update
+@pytest.mark.parametrize("shape", [(64, 72), (72, 64), (300, 280)])
+@pytest.mark.parametrize("s", [3.9, 4.1, 9.0, 15.9])
+def test_muon_update_of_large_singular_values(s, shape):
+    """One entry, carried to s and back: X, P and X again are each off by 2^-11 at
+    most, the result by 2^-8."""
+    g = torch.zeros(shape)
+    g[5, 7] = -2.0
+    o = da.muon_update(g.cuda(), steps=2, coeffs=[(s, 0.0, 0.0), (1.0 / s, 0.0, 0.0)])
+    _done()
+    want = torch.zeros(shape)
+    want[5, 7] = -1.0
+    assert np.abs(_f(o) - want.numpy()).max() <= 2.0 ** -8 + 4.1 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("shape", [(64, 72), (72, 64)])
+def test_muon_update_of_large_singular_values_and_their_products(shape):
+    """All singular values 5, then through a quintic.  A's rounding (2^-11 of 25) goes into
+    P = 0.5 - 0.3125 + 0.0625 as 0.44 2^-11, 1.8 2^-11 of it; P's own and X's three are 2^-11
+    each, the result's 2^-8: below 2^-7 in all."""
+    q, _ = np.linalg.qr(np.random.default_rng(2).normal(size=(72, 64)))
+    g = torch.tensor(q if shape[0] > shape[1] else q.T, dtype=F32).contiguous()
+    c = [(40.0, 0.0, 0.0), (0.5, -0.0125, 0.0001)]
+    o = da.muon_update(g.cuda(), steps=2, coeffs=c)
+    _done()
+    want, _ = os_.muon(_f(g), steps=2, coeffs=c)
+    assert np.linalg.norm(_f(o) - want) <= 2.0 ** -7 * np.linalg.norm(want)
