@@ -548,8 +548,11 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
  * 2e-3 of its norm of the formula (of which rounding it to bf16 is 1.7e-3) for
  * matrices of normal numbers; directions whose singular value is below 2^-11 of
  * the largest are only known to that.  Squares are summed in ranges, so the norm
- * neither overflows nor vanishes for any finite fp32 update.  An infinity or NaN
- * in a matrix makes its o NaN and leaves the batch's other matrices as they are.
+ * neither overflows nor vanishes for any finite fp32 update.  u / (|u| + eps)
+ * itself is held to 2^-37 per entry, which keeps that accuracy while |u| is
+ * eps / 1024 or more; a smaller update's o is off by 2^-37 sqrt(m n) times the
+ * steps' a (3.4445^5 = 485), up to being zero.  An infinity or NaN in a matrix
+ * makes its o NaN and leaves the batch's other matrices as they are.
  * batch in [0, 65535], m in [1, 32768], n a multiple of 8 in [8, 32768], batch m n
  * at most 1.7e10, steps in [1, 64], eps >= 1e-30.  16-byte aligned device pointers;
  * o, momentum and g must not overlap.  The products are one cooperative launch,

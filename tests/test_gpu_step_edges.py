@@ -7,7 +7,7 @@ import torch
 
 import deterministic_attention_gb300 as da
 from oracle import step as os_
-from test_gpu_step import BF, F32, _ce_check, _ce_inputs, _done, _f, _gen
+from test_gpu_step import BF, F32, _ce_check, _ce_inputs, _done, _f, _gen, _muon_grad
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,22 @@ def test_muon_update_of_large_singular_values_and_their_products(shape):
     _done()
     want, _ = os_.muon(_f(g), steps=2, coeffs=c)
     assert np.linalg.norm(_f(o) - want) <= 2.0 ** -7 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(96, 160), (1024, 520)])
+def test_muon_update_of_gradients_below_eps(shape, dtype):
+    """|u| down to eps / 1024 keeps the accuracy: entries of X are held to 2^-37 at worst,
+    2^-37 sqrt(m n) in all against |X| = 2^-10 (7e-6 of 1024 x 520).  Below, that is
+    the error of X, times 3.4445 a step."""
+    eps = 1e-7
+    n = shape[0] * shape[1]
+    g = _muon_grad(shape, 50, dtype, eps / 1000 / n ** 0.5)
+    o = da.muon_update(g.cuda(), eps=eps)
+    tiny = _muon_grad(shape, 51, dtype, 1e-20)
+    o2 = da.muon_update(tiny.cuda(), eps=eps)
+    _done()
+    want, _ = os_.muon(_f(g), eps=eps)
+    assert np.linalg.norm(_f(o) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    want, _ = os_.muon(_f(tiny), eps=eps)
+    assert np.linalg.norm(_f(o2) - want) <= 3.4445 ** 5 * 2.0 ** -37 * n ** 0.5 * 1.01
