@@ -285,7 +285,7 @@ __device__ __forceinline__ bool wait_counts(const unsigned* p, const unsigned* q
 __device__ __forceinline__ bool wait_ready(uint32_t ready, int n, uint64_t limit_ns) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t it = 0; it < (1u << 26); ++it) {
+  for (uint32_t it = 0; it < (1u << 31); ++it) {  // (2^26 looks take a few seconds, less than limits may be)
     int v;
     asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(ready) : "memory");
     if (v >= n) return true;
@@ -621,6 +621,18 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(product::kThreads
   }
 }
 
+// Failure-detection self-test: the waits for other blocks' tiles, on a count that
+// nothing adds to, and for this block's producer.
+__device__ unsigned g_no_count = 0;
+__global__ void muon_wait_selftest_kernel(unsigned long long limit_ns) {
+  __shared__ int ready;
+  if (threadIdx.x == 0) ready = 0;
+  __syncwarp();
+  const bool counts = product::warp_all(wait_counts(&g_no_count, &g_no_count, 1u, limit_ns));
+  const bool seen = product::warp_all(wait_ready(smem_u32(&ready), 1, limit_ns));
+  if (threadIdx.x == 0 && !counts && !seen) atomicOr(&g_product_status, 1u);
+}
+
 template <int CTAS>
 cudaError_t launch_chain_t(const MuonChainArgs& a, long units, cudaStream_t st) {
   // Teams that are resident at once, by device (0: not asked yet).  Their number
@@ -720,6 +732,7 @@ cudaError_t launch_muon_chain(const MuonChainArgs& a, int ctas, long units, cuda
 cudaError_t take_muon_status(cudaStream_t st, unsigned* out) { return product::take_status(st, out); }
 cudaError_t launch_muon_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
   product::wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
+  muon_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
   return cudaGetLastError();
 }
 

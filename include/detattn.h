@@ -636,12 +636,13 @@ int detattn_diag_dkdv_list(int B, int T, int Hq, int Hkv, int causal, int c, int
  * Returns DETATTN_OK or DETATTN_ERR_SHAPE for another value. */
 int detattn_set_dkdv_deal(int mode);
 
-/* Failure-detection self-test.  Launches five small kernels on `stream`, one
+/* Failure-detection self-test.  Launches six small kernels on `stream`, one
  * after the other, that wait, with the same bounded waits that the attention
  * kernels, act8_wgrad, block_norm_bwd, linear_ce and muon_update use, on a
- * barrier nothing ever completes; each wait (eight in all) gives up after `limit_ns` (clamped to [1
- * ms, 10 s]), the kernel records a timeout in its status word and returns, so
- * the context stays usable.  A following detattn_check_status() returns
+ * barrier nothing ever completes (muon_update's waits for other blocks' tiles: on
+ * a count nothing adds to); each wait (ten in all) gives up after `limit_ns`
+ * (clamped to [1 ms, 10 s]), the kernel records a timeout in its status word and
+ * returns, so the context stays usable.  A following detattn_check_status() returns
  * DETATTN_ERR_DEVICE_TIMEOUT, whose text names the kinds (and clears the
  * words).  Not tied to a passage of the method: it exists to test the timeout
  * path without faulting a GPU. */

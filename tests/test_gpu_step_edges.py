@@ -158,3 +158,22 @@ def test_muon_update_of_gradients_below_eps(shape, dtype):
     assert np.linalg.norm(_f(o) - want) <= 2.0 ** -8 * np.linalg.norm(want)
     want, _ = os_.muon(_f(tiny), eps=eps)
     assert np.linalg.norm(_f(o2) - want) <= 3.4445 ** 5 * 2.0 ** -37 * n ** 0.5 * 1.01
+
+
+# ------------------------------------------------------------ waits
+def test_every_wait_of_the_step_operators_runs_out():
+    """The self-test's ten waits, one after another, the update's waits for other blocks'
+    tiles and for its producer among them: each lasts its limit."""
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    da.selftest_wait_timeout(1_000_000)
+    torch.cuda.synchronize()
+    with pytest.raises(da.DetAttnError):
+        da.check_status()
+    a.record()
+    da.selftest_wait_timeout(20_000_000)
+    b.record()
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) >= 10 * 20.0
+    with pytest.raises(da.DetAttnError, match="linear_ce 1, muon_update 1"):
+        da.check_status()
+    da.check_status()
