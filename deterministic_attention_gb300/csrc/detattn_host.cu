@@ -1417,8 +1417,8 @@ CeBwdLayout ce_bwd_layout(int N, int V, int d) {
   size_t part = 0;
   const int last = V % l.width == 0 ? l.width : V % l.width;
   for (int w : {l.width, last}) {
-    part = std::max(part, product_partial_bytes(product_plan(2, N, d, w, 1, true), 2));
-    part = std::max(part, product_partial_bytes(product_plan(2, w, d, N, 1, true), 2));
+    part = std::max(part, product_partial_bytes(product_plan(N, d, w, true)));
+    part = std::max(part, product_partial_bytes(product_plan(w, d, N, true)));
   }
   l.total = l.partial + up256(part) + 256;  // (a start on 256 bytes within the caller's)
   return l;
@@ -2173,7 +2173,7 @@ int linear_ce_fwd(const void* x, const void* w, const int* targets, float* loss,
   CUtensorMap mx, mw;
   if ((rc = encode_rows_of_k(&mx, x, d, N, 1, d, static_cast<long>(N) * d, "x")) != DETATTN_OK) return rc;
   if ((rc = encode_rows_of_k(&mw, w, d, V, 1, d, static_cast<long>(V) * d, "w")) != DETATTN_OK) return rc;
-  ProductPlan p = product_plan(2, N, V, d, 1, false);
+  ProductPlan p = product_plan(N, V, d, false);
   p.band = 16;
   p.wait_ns = g_wait_ns;
   char* ws = static_cast<char*>(workspace);
@@ -2232,16 +2232,16 @@ int linear_ce_bwd(const void* x, const void* w, const int* targets, const float*
     if ((rc = encode_k_rows(&mwk, wp, d, width, 1, d, wd, "w")) != DETATTN_OK) return rc;
     if ((rc = encode_rows_of_k(&mz, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
     if ((rc = encode_k_rows(&mzk, ws, width, N, 1, l.ld, nz, "dz")) != DETATTN_OK) return rc;
-    ProductPlan p = product_plan(2, N, width, d, 1, false);
+    ProductPlan p = product_plan(N, width, d, false);
     p.wait_ns = g_wait_ns;
     CeGradArgs ga{targets, lse, dloss, dlse, unit, ws, N, V, v0, width, l.ld};
     if ((rc = launched(launch_ce_dz(mx, mw, p, ga, st), "linear_ce_bwd (dz)")) != DETATTN_OK) return rc;
-    p = product_plan(2, N, d, width, 1, true);
+    p = product_plan(N, d, width, true);
     p.wait_ns = g_wait_ns;
     CeStoreArgs sa{unit, last ? dx : nullptr, acc, partial, N, d, first ? 0 : 1, 0,
                    d % 16 == 0 && (!last || on32(dx))};
     if ((rc = launched(launch_ce_dx(mz, mwk, p, sa, st), "linear_ce_bwd (dx)")) != DETATTN_OK) return rc;
-    p = product_plan(2, width, d, N, 1, true);
+    p = product_plan(width, d, N, true);
     p.wait_ns = g_wait_ns;
     sa = {unit, static_cast<char*>(dw) + static_cast<size_t>(v0) * d * dw_size, nullptr, partial, width, d, 0, dw_fp32,
           d % 16 == 0 && on32(dw)};

@@ -42,7 +42,6 @@ namespace detattn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPairs = 2;   // blocks per tile
 constexpr int kSumThreads = 256;
 
 // ------------------------------------------------------------ forward
@@ -395,16 +394,14 @@ cudaError_t launch_sum(const CeStoreArgs& a, const ProductPlan& p, cudaStream_t 
 
 }  // namespace
 
-ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool cut) {
-  const int tile = 128 * ctas;
+ProductPlan product_plan(long M, long N, long K, bool cut) {
   ProductPlan p{};
   p.band = 8;
-  p.tiles_m = static_cast<int>((M + tile - 1) / tile);
-  p.tiles_n = static_cast<int>((N + tile - 1) / tile);
-  p.batch = batch;
+  p.tiles_m = static_cast<int>((M + kCeTile - 1) / kCeTile);
+  p.tiles_n = static_cast<int>((N + kCeTile - 1) / kCeTile);
   p.n_k = static_cast<int>((K + product::kBK - 1) / product::kBK);
-  const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n * batch;
-  const int teams = product_teams(ctas);
+  const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n;
+  const int teams = product_teams(2);
   p.splits = 1;
   p.whole = static_cast<int>(tiles);
   const int rem = static_cast<int>(tiles % teams);
@@ -431,7 +428,7 @@ ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool cut) 
 
 cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
                             const CeStatsArgs& a, cudaStream_t st) {
-  return product::launch<kPairs, false, false, false, StatsEpi>(mx, mw, p, a, false, st);
+  return product::launch<false, false, StatsEpi>(mx, mw, p, a, false, st);
 }
 
 cudaError_t launch_ce_finish(const CeFinishArgs& a, cudaStream_t st) {
@@ -446,18 +443,18 @@ cudaError_t launch_ce_unit(const int* targets, const float* dloss, const float* 
 
 cudaError_t launch_ce_dz(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
                          const CeGradArgs& a, cudaStream_t st) {
-  return product::launch<kPairs, false, false, false, GradEpi>(mx, mw, p, a, true, st);
+  return product::launch<false, false, GradEpi>(mx, mw, p, a, true, st);
 }
 
 cudaError_t launch_ce_dx(const CUtensorMap& mdz, const CUtensorMap& mw, const ProductPlan& p,
                          const CeStoreArgs& a, cudaStream_t st) {
-  cudaError_t e = product::launch<kPairs, false, true, false, StoreEpi>(mdz, mw, p, a, true, st);
+  cudaError_t e = product::launch<false, true, StoreEpi>(mdz, mw, p, a, true, st);
   return e != cudaSuccess ? e : launch_sum(a, p, st);
 }
 
 cudaError_t launch_ce_dw(const CUtensorMap& mdz, const CUtensorMap& mx, const ProductPlan& p,
                          const CeStoreArgs& a, cudaStream_t st) {
-  cudaError_t e = product::launch<kPairs, true, true, false, StoreEpi>(mdz, mx, p, a, true, st);
+  cudaError_t e = product::launch<true, true, StoreEpi>(mdz, mx, p, a, true, st);
   return e != cudaSuccess ? e : launch_sum(a, p, st);
 }
 

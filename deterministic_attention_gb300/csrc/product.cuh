@@ -1,14 +1,13 @@
 // Products on the tensor cores for the ends of a training step, sm_103a:
 //
-//   C[m, n] = sum_k A[m, k] B[n, k]      (batched; bf16 or fp16 operands, fp32 sums)
+//   C[m, n] = sum_k A[m, k] B[n, k]      (bf16 operands, fp32 sums)
 //
 // with what becomes of a tile's sums given by an epilogue class.  An operand
 // lies in memory either with K contiguous or with its own index contiguous
 // (A_MN, B_MN); both are what the tensor core reads from a 128-byte swizzled
-// tile.  One persistent block per SM; CTAS = 2 blocks of a cluster work on one
+// tile.  One persistent block per SM; two blocks of a cluster work on one
 // tile of 256 x 256 (cta_group::2: each loads half of the rows of A and half of
-// the rows of B, 32 KB a step of 64 along K, for 512 clocks of MMA), or CTAS = 1
-// on one of 128 x 128 (the same 32 KB for 256 clocks):
+// the rows of B, 32 KB a step of 64 along K, for 512 clocks of MMA):
 //   warp 0       TMA producer, a ring of 7 stages
 //   warp 1       (even block) tcgen05.mma issuer
 //   warps 4-11   epilogue: warp w has rows 32 (w % 4) .. + 31 of its block's 128
@@ -16,6 +15,9 @@
 // Two accumulators in TMEM take turns, so a tile's epilogue runs beside the
 // next tile's products.  Units of work (tiles, or ranges along K of a tile) go
 // to teams in a fixed order: every element is summed in one order.
+//
+// The update's chain of products (muon.cu) has the same parts, with CTAS = 1 or 2
+// blocks on a tile (one block: 128 x 128, the same 32 KB for 256 clocks) and fp16.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -102,11 +104,11 @@ __device__ __forceinline__ void init_barriers(uint64_t* bars) {
 
 // ---------------------------------------------------------------- units of work
 struct Unit {
-  int batch, mt, nt;   // tile
+  int mt, nt;          // tile
   int kb0, kb1;        // steps [kb0, kb1)
   int part;            // partial slot, -1: a whole tile
 };
-// Row and column tile of tile `t` of one matrix.  Bands of p.band tile rows, and
+// Row and column tile of tile `t`.  Bands of p.band tile rows, and
 // in a band column by column: the teams at work at one time share few
 // rows of either operand.
 __device__ __forceinline__ void tile_at(const ProductPlan& p, int t, int* mt, int* nt) {
@@ -130,14 +132,12 @@ __device__ __forceinline__ Unit unit_at(const ProductPlan& p, int u) {
       w.part = r;
     }
   }
-  const int per = p.tiles_m * p.tiles_n;
-  w.batch = tile / per;
-  tile_at(p, tile - w.batch * per, &w.mt, &w.nt);
+  tile_at(p, tile, &w.mt, &w.nt);
   return w;
 }
 
 // Epi: a class with
-//   static constexpr int kCols: columns of a thread's part of the tile (64 CTAS)
+//   static constexpr int kCols: columns of a thread's part of the tile (128)
 //   static constexpr bool kOwnInputs: the operands are what the call got, not what
 //       the kernel before wrote: their copies need not wait for it
 //   struct Args
@@ -148,35 +148,28 @@ __device__ __forceinline__ Unit unit_at(const ProductPlan& p, int u) {
 //       what follows from them
 //   __device__ void take(uint32_t taddr)
 //       reads kCols columns of TMEM at taddr and stores them
-template <int CTAS, bool A_MN, bool B_MN, bool F16, class Epi>
-__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool A_MN, bool B_MN, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                    const ProductPlan p, const typename Epi::Args ea) {
-  constexpr int kTile = 128 * CTAS;
+  constexpr int kTile = 256;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CTAS == 2 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int team = blockIdx.x / CTAS, teams = gridDim.x / CTAS;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int team = blockIdx.x / 2, teams = gridDim.x / 2;
   // The same offsets in both blocks (the products read both at one address).
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  auto lead_bar = [&](int i) {
-    return CTAS == 2 ? map_shared_rank(smem_u32(&bars[i]), 0) : smem_u32(&bars[i]);
-  };
+  auto lead_bar = [&](int i) { return map_shared_rank(smem_u32(&bars[i]), 0); };
   if (warp == 1) {
-    if constexpr (CTAS == 2) {
-      tmem_alloc_pair(smem_u32(&tmem_slot), 2 * kTile);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(smem_u32(&tmem_slot), 2 * kTile);
+    tmem_relinquish_pair();
     tc_fence_before();
   }
   if (threadIdx.x == 0) {
-    init_barriers<CTAS>(bars);
+    init_barriers<2>(bars);
     fence_barrier_init();
   }
   if (threadIdx.x == 32) {
@@ -184,7 +177,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&mb);
   }
   __syncthreads();
-  if constexpr (CTAS == 2) cluster_sync();
+  cluster_sync();
   tc_fence_after();
   griddep_launch_dependents();
   const uint32_t tmem = tmem_slot;
@@ -202,15 +195,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
           if (it >= kStages && !(ok = mbar_wait_hint(bar(kBarEmpty + r.s), r.parity ^ 1u, p.wait_ns)))
             break;
-          if (rank == 0) mbar_arrive_expect_tx(bar(kBarFull + r.s), CTAS * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(bar(kBarFull + r.s), 2 * kStageBytes);
           const uint32_t to = lead_bar(kBarFull + r.s), da = s0 + r.s * kStageBytes;
           const uint32_t db = da + kOperandBytes;
           const int k = kb * kBK;
           auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
-            if constexpr (CTAS == 2)
-              tma_load_3d_pair(dst, map, to, c0, c1, w.batch);
-            else
-              tma_load_3d(dst, map, to, c0, c1, w.batch);
+            tma_load_3d_pair(dst, map, to, c0, c1, 0);
           };
           if constexpr (A_MN) {
             load(da, &ma, m, k);
@@ -242,7 +232,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
       steps += w.kb1 - w.kb0;
     }
   } else if (warp == 1) {
-    constexpr uint32_t kId = idesc(kTile, kTile, A_MN, B_MN, F16);
+    constexpr uint32_t kId = idesc(kTile, kTile, A_MN, B_MN, false);
     // K contiguous: 16 of K are 32 bytes of the swizzled row.  K along the rows:
     // 16 rows of 128 bytes, atoms of 64 columns 8 KB apart.
     constexpr uint32_t kStepA = A_MN ? 2048u : 32u, kStepB = B_MN ? 2048u : 32u;
@@ -254,40 +244,25 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit w = unit_at(p, u);
       const int acc = n & 1;
       if (n >= 2 &&
-          !(ok = warp_all(mbar_wait_hint<CTAS == 2>(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, p.wait_ns))))
+          !(ok = warp_all(mbar_wait_hint<true>(bar(kBarAccFree + acc), ((n >> 1) & 1) ^ 1, p.wait_ns))))
         break;
       tc_fence_after();
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         if (!(ok = warp_all(mbar_wait_hint(bar(kBarFull + r.s), r.parity, p.wait_ns)))) break;
         tc_fence_after();
         const uint64_t a = desc_add(dA0, r.s * kStageBytes), b = desc_add(dB0, r.s * kStageBytes);
-        if constexpr (CTAS == 2) {
-          mma_ss_x4_pair(tmem + acc * kTile, a, desc_add(a, kStepA), desc_add(a, 2 * kStepA),
-                         desc_add(a, 3 * kStepA), b, desc_add(b, kStepB), desc_add(b, 2 * kStepB),
-                         desc_add(b, 3 * kStepB), kId, kb > w.kb0 ? 1u : 0u);
-          mma_commit_pair(bar(kBarEmpty + r.s));
-        } else {
-          mma_ss_x4(tmem + acc * kTile, a, desc_add(a, kStepA), desc_add(a, 2 * kStepA),
-                    desc_add(a, 3 * kStepA), b, desc_add(b, kStepB), desc_add(b, 2 * kStepB),
-                    desc_add(b, 3 * kStepB), kId, kb > w.kb0 ? 1u : 0u);
-          mma_commit(bar(kBarEmpty + r.s));
-        }
+        mma_ss_x4_pair(tmem + acc * kTile, a, desc_add(a, kStepA), desc_add(a, 2 * kStepA),
+                       desc_add(a, 3 * kStepA), b, desc_add(b, kStepB), desc_add(b, 2 * kStepB),
+                       desc_add(b, 3 * kStepB), kId, kb > w.kb0 ? 1u : 0u);
+        mma_commit_pair(bar(kBarEmpty + r.s));
         r.next();
         ++steps;
       }
-      if (ok) {
-        if constexpr (CTAS == 2)
-          mma_commit_pair(bar(kBarAcc + acc));
-        else
-          mma_commit(bar(kBarAcc + acc));
-      }
+      if (ok) mma_commit_pair(bar(kBarAcc + acc));
     }
-    if constexpr (CTAS == 2)
-      mma_commit_pair(bar(kBarDrain));
-    else
-      mma_commit(bar(kBarDrain));
+    mma_commit_pair(bar(kBarDrain));
   } else if (warp >= kFirstEpiWarp) {
-    static_assert(Epi::kCols == 64 * CTAS, "half of the tile's columns");
+    static_assert(Epi::kCols == kTile / 2, "half of the tile's columns");
     const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
     const uint32_t tl = tmem + half * Epi::kCols + (static_cast<uint32_t>(quarter * 32) << 16);
     griddep_wait();
@@ -307,12 +282,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
       e.take(tl + acc * kTile);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (CTAS == 2)
-          mbar_arrive_pair(lead_bar(kBarAccFree + acc));
-        else
-          mbar_arrive(bar(kBarAccFree + acc));
-      }
+      if (lane == 0) mbar_arrive_pair(lead_bar(kBarAccFree + acc));
     }
     if (!ok && lane == 0) atomicOr(&g_product_status, 1u);
   }
@@ -329,19 +299,16 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
-  if constexpr (CTAS == 2) cluster_sync();
+  cluster_sync();
   if (threadIdx.x >> 5 == 1) {
     tc_fence_after();
-    if constexpr (CTAS == 2)
-      tmem_dealloc_pair(tmem_slot, 2 * kTile);
-    else
-      tmem_dealloc(tmem_slot, 2 * kTile);
+    tmem_dealloc_pair(tmem_slot, 2 * kTile);
   }
 }
 
 // dependent: starts while the kernel before it on the stream still runs and
 // waits for it before it reads or writes memory.
-template <int CTAS, bool A_MN, bool B_MN, bool F16, class Epi>
+template <bool A_MN, bool B_MN, class Epi>
 cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const ProductPlan& p,
                    const typename Epi::Args& a, bool dependent, cudaStream_t st) {
   static unsigned long long attr_ctx[64] = {};
@@ -349,14 +316,14 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const ProductPl
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long ctx = current_context_id();
-  auto* kernel = product_kernel<CTAS, A_MN, B_MN, F16, Epi>;
+  auto* kernel = product_kernel<A_MN, B_MN, Epi>;
   if (dev >= 64 || ctx == 0 || attr_ctx[dev] != ctx) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_ctx[dev] = ctx;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(CTAS * p.teams));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.teams));
   cfg.blockDim = kThreads;
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;

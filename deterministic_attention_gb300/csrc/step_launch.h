@@ -26,16 +26,17 @@ struct TurnArgs {
 cudaError_t launch_turn(const TurnArgs& a, cudaStream_t st);
 
 // ------------------------------------------------------------ products
-// Work of one launch of the tensor-core product (product.cuh): C tiles of
-// 128 CTAS x 128 CTAS, CTAS = 1 or 2 blocks on one tile.
+// Work of one launch of the tensor-core product (product.cuh): C tiles of 256 x 256,
+// two blocks on one tile.
+constexpr int kCeTile = 256;
 struct ProductPlan {
-  int tiles_m, tiles_n, batch;
+  int tiles_m, tiles_n;
   int n_k;                 // steps of 64 along K
   int band;                // tile rows that are walked together, column by column
   int whole;               // tiles computed by one team each
   int splits;              // K ranges of each of the other tiles (1: none cut)
   int units;               // whole + (tiles - whole) * splits
-  int teams;               // pairs (or blocks) at work
+  int teams;               // pairs at work
   unsigned long long wait_ns;
 };
 // Teams of the GB300's 152 SMs.  Constants, so that the deal of the work, and
@@ -44,10 +45,10 @@ constexpr int kProductSms = 152;
 inline int product_teams(int ctas) { return kProductSms / ctas; }
 // cut: whether tiles of an incomplete last round are cut along K (the caller
 // has then room for partial tiles and adds them up).
-ProductPlan product_plan(int ctas, long M, long N, long K, int batch, bool cut);
-inline size_t product_partial_bytes(const ProductPlan& p, int ctas) {
-  const size_t cut = static_cast<size_t>(p.tiles_m) * p.tiles_n * p.batch - p.whole;
-  return p.splits == 1 ? 0 : cut * p.splits * (128 * ctas) * (128 * ctas) * sizeof(float);
+ProductPlan product_plan(long M, long N, long K, bool cut);
+inline size_t product_partial_bytes(const ProductPlan& p) {
+  const size_t cut = static_cast<size_t>(p.tiles_m) * p.tiles_n - p.whole;
+  return p.splits == 1 ? 0 : cut * p.splits * kCeTile * kCeTile * sizeof(float);
 }
 
 // ------------------------------------------------------------ cross entropy of the output projection
@@ -88,7 +89,6 @@ struct CeStoreArgs {
   int out_fp32;
   int wide;                // rows of out begin on 32 bytes
 };
-constexpr int kCeTile = 256;
 // mx: x [N, d] as rows of K; mw: w [V, d] as rows of K.
 cudaError_t launch_ce_stats(const CUtensorMap& mx, const CUtensorMap& mw, const ProductPlan& p,
                             const CeStatsArgs& a, cudaStream_t st);
@@ -148,7 +148,6 @@ struct MuonChainArgs {
   int sym_tiles;           // tiles on and below the diagonal of a symmetric product
   int wide;                // m <= n
   int o_on32;              // rows of o begin on 32 bytes
-  int teams;
   unsigned long long wait_ns;
   float coeffs[64][3];
 };
