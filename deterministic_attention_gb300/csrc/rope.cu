@@ -8,8 +8,8 @@
 //
 // Angles: theta_i / 2 pi, a double, becomes a 64-bit fixed-point fraction of a
 // turn F_i; t F_i in 64-bit integers, which drop whole turns by themselves, is
-// the phase to within t 2^-54 turns at any position, and its upper 32 bits go
-// to sincospif.  (In fp32 the angle t theta of t = 131072 is off by 2^-8.)
+// the phase to within t 2^-54 turns at any position (theta_i up to 1; two roundings
+// of theta_i / 2 pi), and its upper 32 bits go to sincospif.  (In fp32 the angle t theta of t = 131072 is off by 2^-8.)
 //
 // Memory bounds it: every element is read and written once.  A block takes a
 // few tokens, forms their cosines and sines once in shared memory for all heads

@@ -469,7 +469,8 @@ int block_norm_bwd(const void* dx_out, const void* dh, const void* x, const void
  *   kind 3  over factor where fewer than `low` turns fit `context` positions, as
  *           they are where more than `high` do, between in proportion to the
  *           pair's number (whole pairs, from the numbers at which exactly
- *           `high` and `low` turns fit); *mscale = 0.1 ln(factor) + 1
+ *           `high` and `low` turns fit; pair 0 always as it is); *mscale =
+ *           0.1 ln(factor) + 1
  *   kind 4  the same in proportion to the number of turns (bands of
  *           wavelengths); *mscale = 1
  * rot even in [2, 1024]; base > 1; factor >= 1; 0 < low < high and context >= 1
@@ -489,8 +490,8 @@ int rope_freqs(double* freqs, float* mscale, int rot, double base, int kind, dou
  * pointers NULL).  freqs: double [rot / 2] on the DEVICE, radians per position,
  * finite (rope_freqs gives such).  positions: int32 [n_pos] on the device, token
  * r takes positions[r % n_pos] (any int32); NULL with n_pos = 0: t = r % T.
- * Angles are exact to t 2^-54 turns, whatever t; arithmetic is fp32, with one
- * rounding.  N in [0, 2^30], D in [2, 1024], rot even in [2, D].
+ * Angles are exact to t 2^-54 turns, whatever t (|f_i| t 2^-54 where |f_i| is
+ * above 1); arithmetic is fp32, with one rounding.  N in [0, 2^30], D in [2, 1024], rot even in [2, D].
  * Pointers need the alignment of their elements; with 16-byte aligned pointers,
  * strides, D and halves (rot / 2, or rot where interleaved) the memory is moved
  * 16 bytes at a time, which is several times faster. */

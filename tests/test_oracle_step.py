@@ -117,3 +117,10 @@ def test_rope_freqs_ramp():
     k = 1 - np.clip((np.arange(64) - lo) / (hi - lo), 0, 1)
     np.testing.assert_allclose(s, f * (k + (1 - k) / 16), rtol=1e-13)
     assert s[0] == f[0] and abs(s[-1] / f[-1] - 1 / 16) < 1e-12
+
+
+def test_rope_freqs_ramp_of_a_context_shorter_than_a_turn():
+    f, _ = _freqs(64)
+    s, _ = _freqs(64, scaling="ramp", factor=4.0, context=4)
+    assert s[0] == f[0]
+    np.testing.assert_allclose(s[1:], f[1:] / 4, rtol=1e-14)
