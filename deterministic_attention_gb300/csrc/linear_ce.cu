@@ -14,17 +14,19 @@
 // the tensor core's second products need, is the one rounding between the
 // inputs and the results (half a step is 2^-8 of a dz at most); the sums over the
 // vocabulary and over the tokens are in fp32.  dz is held over the largest
-// |dloss| (ce_unit_kernel): where all rows weigh the same, as with a mean, a target's dz is then
-// next to -1, which is a bf16 number, and not next to -dloss, whose rounding
-// would be the same in every row and so in dx and dw as a whole (dloss = 1/240:
-// 3.4e-3).
+// |dloss| (ce_unit_kernel): where all rows weigh the same, as with a mean, a
+// target's dz is then next to -1, which is a bf16 number, and not next to -dloss,
+// whose rounding would be the same in every row and so in dx and dw as a whole
+// (dloss = 1/240: 3.4e-3).
 //
-// Measured (device): 32,768 rows, d = 1536, V = 50,432: forward 2.5 ms (2.0 PFLOP/s, at
-// and above the measured bf16 peak), backward 8.9 ms (1.71 PFLOP/s, under the power
-// limit; 7.7 at best): a piece of 25,344 words takes 1.31 (dz), 1.30 (dx) and 1.31 ms
-// (dw), 1.35 at the measured peak.  1,187 rows, d = 768: backward 176 us, the tensor pipe
-// busy 81 to 84 % of the time; forward of 128 rows 21.4 us, 13 of them the weights'
-// 77 MB at 6 TB/s.  What mattered: tiles in bands (dx and dz had read dz and x from
+// Measured (device): 32,768 rows, d = 1536, V = 50,432: forward 2.5 ms in short runs
+// (2.0 PFLOP/s; the measured bf16 peak, 1.90, is a library product's), 2.83 for
+// seconds (1.79 PFLOP/s at 1,500 MHz, under the power limit); backward 8.9 ms (1.71
+// PFLOP/s, under the power limit; 7.7 at best, 9.3 for seconds): a piece of 12,800
+// words takes 0.69 (dz), 0.69 (dx) and 0.67 ms (dw), 0.68 at the measured peak.  1,187
+// rows, d = 768: backward 176 us (with fp32 dw 202), the tensor pipe busy 81 to 84 %
+// of the time; forward of 128 rows 21 us, 11.4 of them what the weights' 77 MB take at
+// the copy rate.  What mattered: tiles in bands (dx and dz had read dz and x from
 // DRAM once per column tile: 573 -> 407 and 484 -> 408 us), 32-byte stores, a
 // tile's row data loaded while the tile before it is taken (a tile of d = 768 takes
 // 4.8 us of products and took 5.3 of epilogue; now 3.3), all loads of a sum to add to

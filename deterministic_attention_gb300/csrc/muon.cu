@@ -9,9 +9,9 @@
 //   A = X X^T,   P = a I + b A + c A A,   X <- P X       (m <= n; X <- X P by columns else)
 //
 // A and P are symmetric: their tiles on and below the diagonal are computed, and
-// what lies above is read as the transpose of what lies below.  Between the products the matrices are fp16, scaled by powers
-// of two (kMuonX, kMuonA, kMuonP): the singular values stay below about 1.2, so fp16's
-// eleven bits cost a step 2^-12 of a value where bf16 costs 2^-9, at the same
+// what lies above is read as the transpose of what lies below.  Between the
+// products the matrices are fp16, scaled by powers of two (kMuonX, kMuonA, kMuonP):
+// the singular values stay below about 1.2 (15.9 fit), so fp16's eleven bits cost a step 2^-12 of a value where bf16 costs 2^-9, at the same
 // rate; five steps leave 1.2e-3 of the result's norm (768 x 768 of normal
 // numbers; bf16 9.8e-3).  Sums are fp32 throughout, the norm's in double.
 #include <cuda_bf16.h>
@@ -214,8 +214,9 @@ __global__ void __launch_bounds__(kInThreads) muon_scale_kernel(const MuonInArgs
 // of the producer (768 x 768: 122 us); all tiles of a symmetric result computed
 // where the teams are idle anyway (768 x 768: 109.4 us against 110.4); two groups of
 // matrices by turns (12 x 768 x 1280: 250 us); the tiles above the diagonal written
-// too (308 us); how an operand lies in memory chosen step by step and not in runs
-// (258 us: the issue of a product then takes longer than the product); sixteen
+// too (a tile's epilogue 6 us in the place of 2); how an operand lies in memory chosen
+// step by step and not in runs (258 us: the issue of a product then takes longer than
+// the product); sixteen
 // epilogue warps (107.8, 219 and 1,174 us where eight took 109.6, 215 and 1,179); one
 // count per block and tile in the place of its warps' (106.7, 217 and 1,200 against
 // 109.4, 216 and 1,200).
@@ -711,7 +712,7 @@ MuonPlan muon_plan(int batch, int m, int n) {
     // one tile's; a pair's step of 64 along K takes about 600, a block's 400
     // (what L2 delivers to all of them), and a tile's start and end
     // 2000 for each.  (768 x 768: 110 us with single blocks, 138 with pairs; 12 x 768 x
-    // 1280 276 and 226; 4096 x 6144 1,745 and 1,190.)
+    // 1280 276 and 226; 4096 x 6144 1,745 and 1,190.  Their transposes take the same.)
     auto product_clocks = [&](long tiles, long k) {
       const double t = static_cast<double>((k + 63) / 64) * (p.ctas == 2 ? 600.0 : 400.0) + p.ctas * 2000.0;
       const double all = t * static_cast<double>(tiles) * batch / static_cast<double>(teams);
