@@ -491,7 +491,8 @@ int rope_freqs(double* freqs, float* mscale, int rot, double base, int kind, dou
  * finite (rope_freqs gives such).  positions: int32 [n_pos] on the device, token
  * r takes positions[r % n_pos] (any int32); NULL with n_pos = 0: t = r % T.
  * Angles are exact to t 2^-54 turns, whatever t (|f_i| t 2^-54 where |f_i| is
- * above 1); arithmetic is fp32, with one rounding.  N in [0, 2^30], D in [2, 1024], rot even in [2, D].
+ * above 1); arithmetic is fp32, with one rounding.  N in [0, 2^30], D in [2, 1024],
+ * rot even in [2, D].
  * Pointers need the alignment of their elements; with 16-byte aligned pointers,
  * strides, D and halves (rot / 2, or rot where interleaved) the memory is moved
  * 16 bytes at a time, which is several times faster. */
